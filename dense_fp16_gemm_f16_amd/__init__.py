@@ -1,5 +1,7 @@
 """MI355X (gfx950) fp16 GEMM: C = fp16(A @ B^T) with fp32 accumulation, and the
-second contract D = A @ B (B [K,N], fp32 out).
+second contract D = A @ B (B [K,N], fp32 out).  Beside them the segmented
+products (segments.py): row grouping, products grouped by expert with their
+gradients, and low-rank adapters.
 
 Thin ctypes binding over ``libgemm_f16.so`` (C ABI declared in
 ``include/gemm_f16.h``).  This module only marshals arguments: shapes,
@@ -54,6 +56,14 @@ EXPORTS = (
     "gemm_f16_tile_coord",
     "gemm_f16_select_tile",
     "gemm_f16_select_xcd",
+    "gemm_f16_group_rows",
+    "gemm_f16_group_rows_workspace",
+    "gemm_f16_grouped_nt",
+    "gemm_f16_grouped_nn",
+    "gemm_f16_grouped_tn",
+    "gemm_f16_grouped_workspace",
+    "gemm_f16_lora_nt",
+    "gemm_f16_lora_workspace",
 )
 
 
@@ -99,6 +109,21 @@ def lib() -> ctypes.CDLL:
     L.gemm_f16_select_tile.restype = ctypes.c_int
     L.gemm_f16_select_xcd.argtypes = [i64, i64, i32, i32]
     L.gemm_f16_select_xcd.restype = ctypes.c_int
+    L.gemm_f16_group_rows.argtypes = [i64, i64, p, i32, p, p, p, p, i64, p]
+    L.gemm_f16_group_rows.restype = ctypes.c_int
+    L.gemm_f16_group_rows_workspace.argtypes = [i64, i64]
+    L.gemm_f16_group_rows_workspace.restype = i64
+    L.gemm_f16_grouped_nt.argtypes = [i64, i64, i64, i64, p, i64, p, p, p, i64, p, i32, p, i64, p]
+    L.gemm_f16_grouped_nt.restype = ctypes.c_int
+    for f in (L.gemm_f16_grouped_nn, L.gemm_f16_grouped_tn):
+        f.argtypes = [i64, i64, i64, i64, p, p, p, p, i32, p, i64, p]
+        f.restype = ctypes.c_int
+    L.gemm_f16_grouped_workspace.argtypes = [i32, i64, i64, i64, i64]
+    L.gemm_f16_grouped_workspace.restype = i64
+    L.gemm_f16_lora_nt.argtypes = [i64, i64, i64, i64, i64, p, p, p, p, p, p, p, p, p, p, i64, p]
+    L.gemm_f16_lora_nt.restype = ctypes.c_int
+    L.gemm_f16_lora_workspace.argtypes = [i64, i64, i64, i64, i64]
+    L.gemm_f16_lora_workspace.restype = i64
     _lib = L
     return L
 
@@ -208,3 +233,8 @@ def select_xcd(num_m: int, num_n: int, swizzle: int = 4, cus: int = 256) -> int:
     if rc < 0:
         raise GemmError(rc)
     return rc
+
+
+from .segments import (  # noqa: E402
+    GROUPED_NN, GROUPED_NT, GROUPED_TN, gemm_f16_grouped_nn, gemm_f16_grouped_nt, gemm_f16_grouped_tn,
+    gemm_f16_lora_nt, group_rows)

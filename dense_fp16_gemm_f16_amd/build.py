@@ -47,10 +47,11 @@ HIPCC_FLAGS = [
 
 
 def sources() -> list[str]:
-    """Translation units of libgemm_f16.so: the host side, one per block tile and one
-    per block tile of the ring kernel's variants."""
+    """Translation units of libgemm_f16.so: the host side, one per block tile, one
+    per block tile of the ring kernel's variants and the segmented products'."""
     return ([os.path.join(CSRC, "gemm_f16.hip")] + sorted(glob.glob(os.path.join(CSRC, "tile_*.hip")))
-            + sorted(glob.glob(os.path.join(CSRC, "ring_*.hip"))))
+            + sorted(glob.glob(os.path.join(CSRC, "ring_*.hip")))
+            + [os.path.join(CSRC, "segments.hip")] + sorted(glob.glob(os.path.join(CSRC, "seg_*.hip"))))
 
 
 def _hipcc() -> str:

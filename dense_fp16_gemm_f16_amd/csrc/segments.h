@@ -1,0 +1,607 @@
+// Segmented products for gfx950: matrix products whose rows fall into
+// consecutive segments ("groups") of ragged sizes that only the GPU knows.
+//
+//   NT  C[r] = A[src(r)] B_g^T   r in segment g, B_g [N,K]   (forward)
+//   NN  C[r] = A[r] B_g          r in segment g, B_g [K,N]   (data gradient)
+//   TN  C_g  = A_g^T B_g         A_g, B_g the rows of segment g: [K,N] (weight gradient)
+//
+// Segment g holds rows offsets[g] .. offsets[g+1]-1.  The offsets are read
+// by the kernels: every workgroup scans them, finds the tile it owns, and
+// those past the last tile leave.  Offsets are clamped to [0, rows] and
+// gathered rows to A, so no content of them leads to an access out of
+// range; rows behind the last segment come out as zeros.
+//
+// The building blocks (LDS layouts, fragment reads, C staging) are those of
+// kernels.h.
+#pragma once
+
+#include "kernels.h"
+
+namespace gemm_f16 {
+
+enum SegKind : int { kSegNT = 0, kSegNN = 1, kSegTN = 2 };
+
+struct SegParams {
+    const _Float16 *a;      // NT, NN: [a_rows, k]; TN: [rows, k]
+    const _Float16 *b;      // NT: [groups, n, k]; NN: [groups, k, n]; TN: [rows, n]
+    void *c;                // NT, NN: [rows, n]; TN: [groups, k, n]; fp16 or fp32
+    const int32_t *offsets; // [groups + 1]
+    const int32_t *index;   // NT: row r takes A's row index[r] / fan; null: row r
+    int64_t a_rows;
+    int32_t rows, groups, n, k, fan;
+    int32_t num_m;          // TN: tiles along k; otherwise the most row tiles there can be
+    int32_t num_n;          // tiles along n
+    // low-rank adapters (kLora kernels): rows sorted by adapter, row r of
+    // C and A is order[r]
+    const int32_t *order;
+    const float *h;         // [rows, h_ld] fp32: scale_s (x D_s^T), zeros past the rank
+    const _Float16 *up;     // [adapters, n, rank]
+    const float *scale;     // [adapters]: multiplies the rows of h (null: 1)
+    int32_t adapters, rank, h_ld;
+};
+
+// Segment bounds, clamped so that any content of offsets stays in range.
+__device__ __forceinline__ int seg_bound(const int32_t *offsets, int g, int rows) {
+    return g <= 0 ? 0 : min(max(offsets[g], 0), rows);
+}
+
+struct SegTile {
+    int g;      // segment; groups: the rows behind the last one
+    int row0;   // first row of the tile
+    int valid;  // rows of the tile inside the segment
+};
+
+__device__ __forceinline__ int wave_scan(int v, int lane) {
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+        const int u = __shfl_up(v, d);
+        if (lane >= d) v += u;
+    }
+    return v;
+}
+
+// The row tiles of all segments, BM rows each and none across a border, in
+// segment order.  One wave-wide scan per 64 segments: lane l holds segment
+// base + l.
+template <int BM>
+struct SegMap {
+    int lo, hi, tiles, scan;  // this lane's segment of the first 64
+    int total;
+
+    __device__ __forceinline__ void chunk(const SegParams &p, int base, int lane, int &l, int &h, int &t) const {
+        const int g = base + lane;
+        l = h = 0;
+        if (g <= p.groups) {  // segment `groups`: the rows behind the last one
+            l = seg_bound(p.offsets, g, p.rows);
+            h = g < p.groups ? seg_bound(p.offsets, g + 1, p.rows) : p.rows;
+        }
+        t = h > l ? (int)(((int64_t)(h - l) + BM - 1) / BM) : 0;
+    }
+
+    __device__ __forceinline__ void init(const SegParams &p, int lane) {
+        chunk(p, 0, lane, lo, hi, tiles);
+        scan = wave_scan(tiles, lane);
+        total = __builtin_amdgcn_readlane(scan, kWave - 1);
+        for (int base = kWave; base <= p.groups; base += kWave) {
+            int l, h, t;
+            chunk(p, base, lane, l, h, t);
+            total += __builtin_amdgcn_readlane(wave_scan(t, lane), kWave - 1);
+        }
+        // offsets that decrease could claim more tiles than the grid has
+        total = min(max(total, 0), p.num_m);
+    }
+
+    // tile m < total
+    __device__ __forceinline__ SegTile find(const SegParams &p, int m, int lane) const {
+        int l = lo, h = hi, t = tiles, s = scan, base = 0, before = 0;
+        for (;;) {
+            const uint64_t hit = __ballot(before + s > m);
+            if (hit) {
+                const int who = __builtin_ctzll(hit);
+                SegTile r;
+                r.g = base + who;
+                const int seg_lo = __builtin_amdgcn_readlane(l, who), seg_hi = __builtin_amdgcn_readlane(h, who);
+                const int first = before + __builtin_amdgcn_readlane(s, who) - __builtin_amdgcn_readlane(t, who);
+                r.row0 = seg_lo + (m - first) * BM;
+                // (always inside, unless decreasing offsets made the counts wrap)
+                r.valid = r.row0 >= seg_lo && r.row0 < seg_hi ? min(BM, seg_hi - r.row0) : 0;
+                return r;
+            }
+            before += __builtin_amdgcn_readlane(s, kWave - 1);
+            base += kWave;
+            if (base > p.groups) return SegTile{p.groups, 0, 0};  // not reached for m < total
+            chunk(p, base, lane, l, h, t);
+            s = wave_scan(t, lane);
+        }
+    }
+};
+
+// ---- operands staged through registers -----------------------------------------
+//
+// For rows that are not 16-byte aligned (K or N not a multiple of 8) and
+// gathers from more than 2 GiB: 16-byte global loads at any 2-byte aligned
+// address, written to the LDS layouts that the direct-to-LDS operands of
+// kernels.h use, so both share their fragment reads.
+
+typedef int int4u __attribute__((ext_vector_type(4), aligned(2)));
+
+// 8 elements from p; those at or past end (the tensor's end) are zero and
+// never touched.
+__device__ __forceinline__ int4v load_chunk(const _Float16 *p, const _Float16 *end) {
+    if ((uintptr_t)(p + 8) <= (uintptr_t)end) return *reinterpret_cast<const int4u *>(p);
+    union {
+        int4v v;
+        _Float16 e[8];
+    } u;
+    u.v = int4v{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+        if ((uintptr_t)(p + i) < (uintptr_t)end) u.e[i] = p[i];
+    return u.v;
+}
+
+// elements e >= kv of a chunk become zero
+__device__ __forceinline__ int4v mask_chunk(int4v v, int kv) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] &= (kv > 2 * j + 1) ? -1 : (kv > 2 * j) ? 0xffff : 0;
+    return v;
+}
+
+// Rows of K contiguous elements (KMajorDirect's layout).
+template <class C, int ROWS>
+struct KMajorStaged {
+    static constexpr int kRow = 128;
+    static constexpr int kStage = ROWS * kRow;
+    static constexpr int kLoads = kStage / 1024 / C::kWaves;
+    static_assert(kLoads * 1024 * C::kWaves == kStage, "whole blocks per wave");
+
+    const _Float16 *row[kLoads];  // this lane's row of load i, null past the tile
+    const _Float16 *end;
+    int4v regs[kLoads];
+    int kc, k_elems, kv;
+    int lds_w, r_lane[C::KS];
+
+    static __device__ __forceinline__ int sw(int r) { return (r >> 1) & 7; }
+    // tile row of load i
+    static __device__ __forceinline__ int tile_row(int i, int wave, int lane) {
+        return (i * C::kWaves + wave) * 8 + (lane >> 3);
+    }
+
+    __device__ __forceinline__ void init(const _Float16 *tensor_end, int K, int wave, int lane, int frag_row, int lds) {
+        end = tensor_end;
+        k_elems = K;
+        kc = ((lane & 7) ^ sw(tile_row(0, wave, lane))) * 8;
+        lds_w = lds + wave * 1024 + lane * 16;
+        const int q = lane / 16, frow = frag_row + lane % 16;
+#pragma unroll
+        for (int ks = 0; ks < C::KS; ++ks) r_lane[ks] = lds + frow * kRow + (((4 * ks + q) ^ sw(frow)) << 4);
+    }
+
+    __device__ __forceinline__ void load(int t) {
+        const int k0 = t * C::BK + kc;
+        kv = k_elems - k0;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            regs[i] = (row[i] && kv > 0) ? load_chunk(row[i] + k0, end) : int4v{0, 0, 0, 0};
+    }
+
+    __device__ __forceinline__ void store(char *smem, int stage) const {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            *reinterpret_cast<int4v *>(smem + lds_w + stage * kStage + i * C::kWaves * 1024) = mask_chunk(regs[i], kv);
+    }
+
+    __device__ __forceinline__ half8 read(const char *smem, int stage, int ks, int f) const {
+        return *reinterpret_cast<const half8 *>(smem + r_lane[ks] + stage * kStage + f * 16 * kRow);
+    }
+};
+
+// COLS columns of a [contraction, ld] matrix (NMajorDirect's layout).
+// Columns past the matrix hold whatever follows in memory: they reach only
+// outputs that are never stored.  Contraction rows past the last are zero.
+template <class C, int COLS, int F>
+struct NMajorStaged {
+    static constexpr int CPR = COLS / 8, kRowB = COLS * 2;
+    static constexpr int kStage = C::BK * kRowB;
+    static constexpr int kRowsPerBlock = 1024 / kRowB;
+    static constexpr int kLoads = kStage / 1024 / C::kWaves;
+    static_assert(CPR >= 16 && CPR <= 64 && kLoads * 1024 * C::kWaves == kStage, "layout");
+
+    const _Float16 *base, *end;  // first contraction row, first column of the tile
+    int64_t ld;
+    int count, cols;             // contraction rows; columns from the tile's first on
+    int r0[kLoads], c0[kLoads];
+    int4v regs[kLoads];
+    int lds_w, r_lane[F];
+
+    static __device__ __forceinline__ int sw(int r) { return 2 * ((r & 3) | ((r >> 1) & 4)); }
+
+    __device__ __forceinline__ void init(const _Float16 *first, const _Float16 *tensor_end, int64_t pitch, int rows,
+                                         int columns, int wave, int lane, int frag_col, int lds) {
+        base = first;
+        end = tensor_end;
+        ld = pitch;
+        count = rows;
+        cols = columns;
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            r0[i] = (i * C::kWaves + wave) * kRowsPerBlock + lane / CPR;
+            c0[i] = ((lane % CPR) ^ sw(r0[i])) * 8;
+        }
+        lds_w = lds + wave * 1024 + lane * 16;
+        const int g = lane >> 4, j = lane & 15;
+        const int row = 8 * g + (j >> 2);
+        const int fsw = sw(row) >> 1;
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+            r_lane[f] = lds + row * kRowB + ((((frag_col >> 4) + f) ^ fsw) << 5) + (((j >> 1) & 1) << 4) + ((j & 1) << 3);
+    }
+
+    __device__ __forceinline__ void load(int t) {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int r = t * C::BK + r0[i];
+            regs[i] = (r < count && c0[i] < cols) ? load_chunk(base + r * ld + c0[i], end) : int4v{0, 0, 0, 0};
+        }
+    }
+
+    __device__ __forceinline__ void store(char *smem, int stage) const {
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i)
+            *reinterpret_cast<int4v *>(smem + lds_w + stage * kStage + i * C::kWaves * 1024) = regs[i];
+    }
+
+    __device__ __forceinline__ half8 read(const char *smem, int stage, int ks, int f) const {
+        char *p0 = const_cast<char *>(smem) + r_lane[f] + stage * kStage + ks * 32 * kRowB;
+        const fp16x4 lo = lds_read_tr16((lds_fp16x4 *)p0);
+        const fp16x4 hi = lds_read_tr16((lds_fp16x4 *)(p0 + 4 * kRowB));
+        half8 r;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            r[e] = (_Float16)lo[e];
+            r[4 + e] = (_Float16)hi[e];
+        }
+        return r;
+    }
+};
+
+// ---- epilogue ------------------------------------------------------------------
+//
+// The wave's accumulators through its share of LDS (CStaging) into rows of
+// C: 16-byte stores where C's rows are 16-byte aligned, else element by
+// element.  rows: valid rows of the tile; n: columns of C; row_of(r): row of
+// C of tile row r.
+template <class C, bool F32, int kWaveBytes, class RowOf>
+__device__ __forceinline__ void seg_store(const floatx4 (&acc)[C::FN][C::FM], char *stg, void *c, int rows, int n,
+                                          int n0, int wm, int wn, int lane, RowOf row_of) {
+    using CS = CStaging<C, F32, kWaveBytes>;
+    using Out = typename CS::Out;
+    constexpr int E = 16 / CS::ES;
+    const int erow = CS::opaque_row(lane);
+    const bool vec = (n % E) == 0 && ((uintptr_t)c % 16) == 0;
+#pragma unroll
+    for (int pass = 0; pass < CS::kPasses; ++pass) {
+        CS::write_pass(acc, stg, pass, erow, lane);
+#pragma unroll
+        for (int s = 0; s < CS::kPerPass; ++s) {
+            const int idx = s * kWave + lane;
+            const int r = wm * C::TM + pass * CS::SR + idx / CS::CPR;
+            const int col = n0 + wn * C::TN + (idx % CS::CPR) * E;
+            const int4v v = CS::read_chunk(stg, s, lane);
+            if (r < rows && col < n) {
+                Out *dst = static_cast<Out *>(c) + (int64_t)row_of(r) * n + col;
+                if (vec) {
+                    *reinterpret_cast<int4v *>(dst) = v;
+                } else {
+                    union {
+                        int4v v;
+                        Out e[E];
+                    } u;
+                    u.v = v;
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        if (col + e < n) dst[e] = u.e[e];
+                }
+            }
+        }
+    }
+}
+
+// ---- adapters: the low-rank product on top of a tile ---------------------------
+//
+// Adds scale_s (x D_s^T) U_s^T to a tile of x W^T whose rows are sorted by
+// adapter: for each adapter with rows in the tile and each 32 of its ranks,
+// one K-tile of 64 whose A half is h = scale_s x D_s^T, zero in rows of
+// other adapters, and whose B half is U_s.  h is fp32: its fp16 rounding
+// and the rest that the rounding leaves take the K-tile's two 32-wide steps
+// (h = hi + lo to 2^-22), against U_s twice.  Rows whose |h| passes fp16's
+// range are scaled by a power of two, and the accumulators with them, so
+// the sum stays what fp32 gives.
+template <class C>
+__device__ __forceinline__ void lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *smem, float *row_scale,
+                                           const SegParams &p, int row0, int valid, int n0, int tid, int lane, int wm,
+                                           int wn) {
+    constexpr int kRow = 128, kB = C::BM * kRow;
+    auto sw = [](int r) { return (r >> 1) & 7; };
+    // power of two that takes a row's largest |h| below 2^15
+    int scaled = 0;
+    for (int r = tid; r < C::BM; r += C::kThreads) {
+        float top = 0.0f;
+        if (r < valid) {
+            const float *h = p.h + (int64_t)(row0 + r) * p.h_ld;
+            for (int q = 0; q < p.h_ld; q += 4) {
+                const floatx4 v = *reinterpret_cast<const floatx4 *>(h + q);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float m = fabsf(v[e]);
+                    if (m < __builtin_inff()) top = fmaxf(top, m);  // infinities and NaN stay what they are
+                }
+            }
+        }
+        float s = 1.0f;
+        if (top >= 32768.0f) {
+            s = ldexpf(1.0f, 14 - ilogbf(top));
+            scaled = 1;
+        }
+        row_scale[r] = s;
+    }
+    const bool any_scaled = __syncthreads_or(scaled);
+    auto scale_acc = [&](bool back) {
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) {
+            float s = row_scale[wm * C::TM + i * 16 + lane % 16];
+            if (back) s = 1.0f / s;  // a power of two: exact
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) acc[j][i] *= s;
+        }
+    };
+    if (any_scaled) scale_acc(false);
+
+    for (int s = 0; s < p.adapters; ++s) {
+        const int lo = max(seg_bound(p.offsets, s, p.rows) - row0, 0);
+        const int hi = min(seg_bound(p.offsets, s + 1, p.rows) - row0, valid);
+        if (lo >= hi) continue;
+        const _Float16 *up = p.up + (int64_t)s * p.n * p.rank;
+        const _Float16 *up_end = p.up + (int64_t)p.adapters * p.n * p.rank;
+        for (int c = 0; c < p.rank; c += 32) {
+            for (int x = tid; x < C::BM * 4; x += C::kThreads) {
+                const int r = x >> 2, q = x & 3;
+                half8 top = {}, rest = {};
+                if (r >= lo && r < hi) {
+                    const float *h = p.h + (int64_t)(row0 + r) * p.h_ld + c + 8 * q;
+                    const float f = row_scale[r];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float v = h[e] * f;
+                        top[e] = (_Float16)v;
+                        const float d = v - (float)top[e];
+                        rest[e] = (_Float16)(fabsf(v) < __builtin_inff() ? d : 0.0f);
+                    }
+                }
+                *reinterpret_cast<half8 *>(smem + r * kRow + ((q ^ sw(r)) << 4)) = top;
+                *reinterpret_cast<half8 *>(smem + r * kRow + (((q + 4) ^ sw(r)) << 4)) = rest;
+            }
+            for (int x = tid; x < C::BN * 4; x += C::kThreads) {
+                const int r = x >> 2, q = x & 3, kv = p.rank - c - 8 * q;
+                int4v v = {0, 0, 0, 0};
+                if (n0 + r < p.n && kv > 0)
+                    v = mask_chunk(load_chunk(up + (int64_t)(n0 + r) * p.rank + c + 8 * q, up_end), kv);
+                *reinterpret_cast<int4v *>(smem + kB + r * kRow + ((q ^ sw(r)) << 4)) = v;
+                *reinterpret_cast<int4v *>(smem + kB + r * kRow + (((q + 4) ^ sw(r)) << 4)) = v;
+            }
+            __syncthreads();
+            half8 af[2][C::FM];
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) {
+                const int r = wm * C::TM + i * 16 + lane % 16;
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+                    af[ks][i] = *reinterpret_cast<const half8 *>(smem + r * kRow + (((4 * ks + lane / 16) ^ sw(r)) << 4));
+            }
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) {
+                const int r = wn * C::TN + j * 16 + lane % 16;
+                half8 bf[2];
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks)
+                    bf[ks] = *reinterpret_cast<const half8 *>(smem + kB + r * kRow + (((4 * ks + lane / 16) ^ sw(r)) << 4));
+#pragma unroll
+                for (int i = 0; i < C::FM; ++i) {
+                    // rows of other adapters keep their value: their zeros
+                    // times an infinity in U_s would be a NaN
+                    const int m = wm * C::TM + i * 16 + lane % 16;
+                    const floatx4 sum = Mfma<16>::run(bf[1], af[1][i], Mfma<16>::run(bf[0], af[0][i], acc[j][i]));
+                    if (m >= lo && m < hi) acc[j][i] = sum;
+                }
+            }
+            __syncthreads();
+        }
+    }
+    if (any_scaled) scale_acc(true);
+}
+
+// ---- the any-alignment kernel --------------------------------------------------
+//
+// One workgroup per tile, operands staged through registers one K-tile
+// ahead, two LDS stages, one barrier per K-tile.  Every size, alignment and
+// gather.
+enum SegMode : int {
+    kSegPlain = 0,
+    kSegLoraDown = 1,  // NT by adapter into fp32 h: columns past n up to h_ld are zeros, rows times scale[g]
+    kSegLoraUp = 2     // x W^T over rows sorted by adapter, then lora_tiles; rows leave through order
+};
+
+template <int KIND, class C, bool F32, int MODE>
+__global__ __launch_bounds__(C::kThreads) void seg_staged_kernel(const SegParams p) {
+    static_assert(C::MB == 16 && C::KS == 2, "16x16x32 tiles");
+    static_assert(MODE == kSegPlain || KIND == kSegNT, "adapters are NT products");
+    using OpA = std::conditional_t<KIND == kSegTN, NMajorStaged<C, C::BM, C::FM>, KMajorStaged<C, C::BM>>;
+    using OpB = std::conditional_t<KIND == kSegNT, KMajorStaged<C, C::BN>, NMajorStaged<C, C::BN, C::FN>>;
+    constexpr int kLdsB = 2 * OpA::kStage, kLds = kLdsB + 2 * OpB::kStage;
+    static_assert(kLds <= 160 * 1024, "LDS budget");
+    __shared__ __attribute__((aligned(1024))) char smem[kLds];
+    __shared__ float row_scale[MODE == kSegLoraUp ? C::BM : 1];
+    GEMM_POISON_LDS(smem);
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wm = wave / C::WN, wn = wave % C::WN;
+
+    OpA opa;
+    OpB opb;
+    int g, row0, valid, n0, kt_count;
+    if constexpr (KIND == kSegTN) {
+        const uint32_t per = (uint32_t)p.num_m * (uint32_t)p.num_n;
+        g = (int)(blockIdx.x / per);
+        const TileCoord tc = tile_coord<uint32_t>(blockIdx.x % per, p.num_m, p.num_n, 4, false);
+        const int m0 = (int)tc.m_block * C::BM;
+        n0 = (int)tc.n_block * C::BN;
+        const int lo = seg_bound(p.offsets, g, p.rows), cnt = max(seg_bound(p.offsets, g + 1, p.rows) - lo, 0);
+        row0 = m0;
+        valid = min(C::BM, p.k - m0);
+        kt_count = (cnt + C::BK - 1) / C::BK;
+        opa.init(p.a + (int64_t)lo * p.k + m0, p.a + (int64_t)p.rows * p.k, p.k, cnt, p.k - m0, wave, lane, wm * C::TM,
+                 0);
+        opb.init(p.b + (int64_t)lo * p.n + n0, p.b + (int64_t)p.rows * p.n, p.n, cnt, p.n - n0, wave, lane,
+                 wn * C::TN, kLdsB);
+    } else {
+        const uint32_t pid = blockIdx.x;
+        if constexpr (MODE == kSegLoraUp) {
+            g = 0;
+            const TileCoord tc = tile_coord<uint32_t>(pid, (p.rows + C::BM - 1) / C::BM, p.num_n, 4, true);
+            row0 = (int)tc.m_block * C::BM;
+            valid = min(C::BM, p.rows - row0);
+            n0 = (int)tc.n_block * C::BN;
+        } else {
+            SegMap<C::BM> map;
+            map.init(p, lane);
+            if (pid >= (uint32_t)map.total * (uint32_t)p.num_n) return;  // num_m * num_n < 2^31
+            const TileCoord tc = tile_coord<uint32_t>(pid, map.total, p.num_n, 4, true);
+            const SegTile st = map.find(p, (int)tc.m_block, lane);
+            g = st.g;
+            row0 = st.row0;
+            valid = st.valid;
+            n0 = (int)tc.n_block * C::BN;
+        }
+        // the rows behind the last segment: no K-tile, so zeros
+        const bool live = MODE == kSegLoraUp || g < p.groups;
+        kt_count = live ? (p.k + C::BK - 1) / C::BK : 0;
+        const _Float16 *a_end = p.a + p.a_rows * p.k;
+        const int32_t *from = MODE == kSegLoraUp ? p.order : p.index;
+        opa.init(a_end, p.k, wave, lane, wm * C::TM, 0);
+#pragma unroll
+        for (int i = 0; i < OpA::kLoads; ++i) {
+            const int r = OpA::tile_row(i, wave, lane);
+            int64_t src = row0 + r;
+            if (from && r < valid) {
+                const int v = from[row0 + r];
+                src = v < 0 ? -1 : MODE == kSegLoraUp ? v : v / p.fan;
+            }
+            opa.row[i] = (live && r < valid && src >= 0 && src < p.a_rows) ? p.a + src * p.k : nullptr;
+        }
+        const int64_t per_group = (int64_t)p.n * p.k;
+        const int64_t count = MODE == kSegLoraUp ? 1 : p.groups;
+        const _Float16 *b = p.b + (live ? g : 0) * per_group, *b_end = p.b + count * per_group;
+        if constexpr (KIND == kSegNT) {
+            opb.init(b_end, p.k, wave, lane, wn * C::TN, kLdsB);
+#pragma unroll
+            for (int i = 0; i < OpB::kLoads; ++i) {
+                const int r = n0 + OpB::tile_row(i, wave, lane);
+                opb.row[i] = r < p.n ? b + (int64_t)r * p.k : nullptr;
+            }
+        } else {
+            opb.init(b + n0, b_end, p.n, p.k, p.n - n0, wave, lane, wn * C::TN, kLdsB);
+        }
+    }
+
+    floatx4 acc[C::FN][C::FM];
+#pragma unroll
+    for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+        for (int i = 0; i < C::FM; ++i) acc[j][i] = floatx4{};
+
+    if (kt_count > 0) {
+        opa.load(0);
+        opb.load(0);
+        opa.store(smem, 0);
+        opb.store(smem, 0);
+    }
+    lds_barrier();
+    for (int t = 0; t < kt_count; ++t) {
+        const bool more = t + 1 < kt_count;
+        if (more) {
+            opa.load(t + 1);
+            opb.load(t + 1);
+        }
+#pragma unroll
+        for (int ks = 0; ks < C::KS; ++ks) {
+            half8 af[C::FM];
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) af[i] = opa.read(smem, t & 1, ks, i);
+#pragma unroll
+            for (int j = 0; j < C::FN; ++j) {
+                const half8 bf = opb.read(smem, t & 1, ks, j);
+#pragma unroll
+                for (int i = 0; i < C::FM; ++i) acc[j][i] = Mfma<16>::run(bf, af[i], acc[j][i]);
+            }
+        }
+        // the other stage was last read before the barrier that ended K-tile t-1
+        if (more) {
+            opa.store(smem, (t + 1) & 1);
+            opb.store(smem, (t + 1) & 1);
+        }
+        lds_barrier();
+    }
+
+    constexpr int kWaveBytes = kLds / C::kWaves;
+    char *const stg = smem + wave * kWaveBytes;
+    if constexpr (MODE == kSegLoraUp) {
+        lora_tiles<C>(acc, smem, row_scale, p, row0, valid, n0, tid, lane, wm, wn);
+        const int32_t *order = p.order;
+        const int rows = p.rows;
+        seg_store<C, F32, kWaveBytes>(acc, stg, p.c, valid, p.n, n0, wm, wn, lane, [&](int r) {
+            return min(max(order[row0 + r], 0), rows - 1);
+        });
+    } else if constexpr (MODE == kSegLoraDown) {
+        const float f = g < p.groups && p.scale ? p.scale[g] : 1.0f;
+#pragma unroll
+        for (int j = 0; j < C::FN; ++j)
+#pragma unroll
+            for (int i = 0; i < C::FM; ++i) acc[j][i] *= f;
+        seg_store<C, F32, kWaveBytes>(acc, stg, p.c, valid, p.h_ld, n0, wm, wn, lane, [&](int r) { return row0 + r; });
+    } else if constexpr (KIND == kSegTN) {
+        using Out = std::conditional_t<F32, float, _Float16>;
+        Out *c = static_cast<Out *>(p.c) + (int64_t)g * p.k * p.n;
+        seg_store<C, F32, kWaveBytes>(acc, stg, c, valid, p.n, n0, wm, wn, lane, [&](int r) { return row0 + r; });
+    } else {
+        seg_store<C, F32, kWaveBytes>(acc, stg, p.c, valid, p.n, n0, wm, wn, lane, [&](int r) { return row0 + r; });
+    }
+}
+
+template <class Kernel>
+inline hipError_t launch_seg(Kernel kernel, int64_t grid, int threads, hipStream_t stream, const SegParams &p) {
+    if (grid <= 0) return hipSuccess;
+    void *args[] = {const_cast<SegParams *>(&p)};
+    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3((unsigned)grid), dim3((unsigned)threads), args,
+                           0, stream);
+}
+
+// Row tiles that the segments can need at most, whatever their sizes: each
+// segment that is not empty (at most one per row; the rows behind the last
+// one count as one) takes ceil(size / bm) <= (size - 1) / bm + 1.
+inline int64_t seg_row_tiles(int64_t rows, int64_t groups, int64_t bm) {
+    const int64_t used = groups + 1 < rows ? groups + 1 : rows;
+    return (rows - used) / bm + used;
+}
+
+using SegCfg128 = Cfg<128, 128, 2, 2, 16>;
+
+constexpr int kGroupOneBlock = 8192;  // rows that one workgroup sorts
+constexpr int kGroupMax = 2048;       // groups (a wave's counters of every group fit in LDS)
+int64_t group_blocks(int64_t rows);
+// counts: group_blocks(rows) * (groups + 1) ints, used with more than one block
+hipError_t launch_group_rows(int64_t rows, int groups, const void *ids, int id_bytes, int32_t *order, int32_t *inverse,
+                             int32_t *offsets, int32_t *counts, hipStream_t s);
+hipError_t launch_seg_staged(int kind, bool f32, int mode, SegParams p, hipStream_t s);
+
+}  // namespace gemm_f16

@@ -1,0 +1,227 @@
+// Host side of the segmented products: argument checks, the choice of
+// kernel and the launches (see segments.h).
+#include "segments.h"
+
+#include <algorithm>
+
+#include "device.h"
+#include "gemm_f16.h"
+
+namespace gemm_f16 {
+
+constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxK = int64_t(1) << 22, kMaxNMajor = int64_t(1) << 25;
+constexpr int64_t kMaxElems = int64_t(1) << 47, kMaxGroups = int64_t(1) << 20;
+
+// One buffer of a call, for the checks on pointers.
+struct Buffer {
+    const void *p;
+    int64_t bytes;
+    int align;
+    bool out;
+};
+
+// Null, alignment and overlap: outputs (and the workspace) against every
+// other buffer.
+template <int N>
+static int check_buffers(const Buffer (&bufs)[N]) {
+    for (const Buffer &b : bufs)
+        if (b.bytes > 0 && !b.p) return GEMM_F16_ENULL;
+    for (const Buffer &b : bufs)
+        if (b.bytes > 0 && ((uintptr_t)b.p % (uintptr_t)b.align) != 0) return GEMM_F16_EALIGN;
+    for (int i = 0; i < N; ++i)
+        for (int j = 0; j < N; ++j) {
+            if (i == j || !bufs[i].out || bufs[i].bytes <= 0 || bufs[j].bytes <= 0) continue;
+            const uintptr_t a0 = (uintptr_t)bufs[i].p, a1 = a0 + (uintptr_t)bufs[i].bytes;
+            const uintptr_t b0 = (uintptr_t)bufs[j].p, b1 = b0 + (uintptr_t)bufs[j].bytes;
+            if (a0 < b1 && b0 < a1) return GEMM_F16_EOVERLAP;
+        }
+    return GEMM_F16_OK;
+}
+
+static bool below(int64_t limit, int64_t a, int64_t b, int64_t c = 1) {
+    // a, b, c >= 0 and below 2^31: a * b cannot wrap
+    if (a == 0 || b == 0 || c == 0) return true;
+    return a * b < limit && a * b <= (limit - 1) / c;
+}
+
+static int check_grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k) {
+    if (kind < kSegNT || kind > kSegTN) return GEMM_F16_EINVAL;
+    if (rows < 0 || n < 0 || k < 0 || rows >= kMaxRows || n >= kMaxRows || k >= kMaxK) return GEMM_F16_EINVAL;
+    if (kind != kSegNT && n >= kMaxNMajor) return GEMM_F16_EINVAL;
+    if (groups < 1 || groups > kMaxGroups) return GEMM_F16_EINVAL;
+    if (!below(kMaxElems, rows, n) || !below(kMaxElems, n, k, groups)) return GEMM_F16_EINVAL;
+    return GEMM_F16_OK;
+}
+
+static int status(hipError_t e) { return e == hipSuccess ? GEMM_F16_OK : e == hipErrorInvalidValue ? GEMM_F16_EINVAL : GEMM_F16_EHIP; }
+
+static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a, int64_t a_rows,
+                   const void *b, const int32_t *offsets, const int32_t *index, int64_t fan, void *c, int32_t out_f32,
+                   void *workspace, int64_t workspace_bytes, void *stream) {
+    int rc = check_grouped(kind, rows, groups, n, k);
+    if (rc != GEMM_F16_OK) return rc;
+    if (a_rows < 0 || a_rows >= kMaxRows || fan < 1 || fan >= kMaxRows || out_f32 < 0 || out_f32 > 1)
+        return GEMM_F16_EINVAL;
+    if (!index && a_rows < rows) return GEMM_F16_EINVAL;
+    const int64_t need = gemm_f16_grouped_workspace(kind, rows, groups, n, k);
+    if (workspace_bytes < need) return GEMM_F16_EINVAL;
+    const int64_t out = kind == kSegTN ? groups * n * k : rows * n;
+    if (out == 0) return GEMM_F16_OK;
+    const int es = out_f32 ? 4 : 2;
+    const Buffer bufs[] = {{c, out * es, es, true},
+                           {workspace, need, 16, true},
+                           {a, a_rows * k * 2, 2, false},
+                           {b, (kind == kSegTN ? rows * n : groups * n * k) * 2, 2, false},
+                           {offsets, (groups + 1) * 4, 4, false},
+                           {index, index ? rows * 4 : 0, 4, false}};
+    rc = check_buffers(bufs);
+    if (rc != GEMM_F16_OK) return rc;
+    int cus;
+    rc = current_device(&cus);
+    if (rc != GEMM_F16_OK) return rc;
+
+    SegParams p = {};
+    p.a = static_cast<const _Float16 *>(a);
+    p.b = static_cast<const _Float16 *>(b);
+    p.c = c;
+    p.offsets = offsets;
+    p.index = index;
+    p.a_rows = a_rows;
+    p.rows = (int32_t)rows;
+    p.groups = (int32_t)groups;
+    p.n = (int32_t)n;
+    p.k = (int32_t)k;
+    p.fan = (int32_t)fan;
+    return status(launch_seg_staged(kind, out_f32 != 0, kSegPlain, p, (hipStream_t)stream));
+}
+
+// h's row pitch: whole 32-wide steps
+static int64_t lora_h_ld(int64_t rank) { return (rank + 31) / 32 * 32; }
+
+static int check_lora(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64_t rank) {
+    if (rows < 0 || n < 0 || k < 0 || rows >= kMaxRows || n >= kMaxRows || k >= kMaxK) return GEMM_F16_EINVAL;
+    if (adapters < 1 || adapters > kMaxGroups || rank < 1 || rank > 4096) return GEMM_F16_EINVAL;
+    if (!below(kMaxElems, rows, n) || !below(kMaxElems, n, k) || !below(kMaxElems, n + k, rank, adapters) ||
+        !below(kMaxElems, rows, lora_h_ld(rank)))
+        return GEMM_F16_EINVAL;
+    return GEMM_F16_OK;
+}
+
+}  // namespace gemm_f16
+
+using namespace gemm_f16;
+
+extern "C" {
+
+int64_t gemm_f16_group_rows_workspace(int64_t rows, int64_t groups) {
+    if (rows < 0 || rows >= kMaxRows || groups < 1 || groups > kGroupMax) return GEMM_F16_EINVAL;
+    const int64_t blocks = group_blocks(rows);
+    return blocks > 1 ? blocks * (groups + 1) * 4 : 0;
+}
+
+int gemm_f16_group_rows(int64_t rows, int64_t groups, const void *ids, int32_t id_bytes, int32_t *order,
+                        int32_t *inverse, int32_t *offsets, void *workspace, int64_t workspace_bytes, void *stream) {
+    const int64_t need = gemm_f16_group_rows_workspace(rows, groups);
+    if (need < 0 || workspace_bytes < need || (id_bytes != 4 && id_bytes != 8)) return GEMM_F16_EINVAL;
+    const Buffer bufs[] = {{order, rows * 4, 4, true},
+                           {inverse, rows * 4, 4, true},
+                           {offsets, (groups + 1) * 4, 4, true},
+                           {workspace, need, 16, true},
+                           {ids, rows * id_bytes, id_bytes, false}};
+    int rc = check_buffers(bufs);
+    if (rc != GEMM_F16_OK) return rc;
+    int cus;
+    rc = current_device(&cus);
+    if (rc != GEMM_F16_OK) return rc;
+    return status(launch_group_rows(rows, (int)groups, ids, id_bytes, order, inverse, offsets,
+                                    static_cast<int32_t *>(workspace), (hipStream_t)stream));
+}
+
+int64_t gemm_f16_grouped_workspace(int32_t kind, int64_t rows, int64_t groups, int64_t n, int64_t k) {
+    const int rc = check_grouped(kind, rows, groups, n, k);
+    return rc != GEMM_F16_OK ? rc : 0;
+}
+
+int gemm_f16_grouped_nt(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a, int64_t a_rows,
+                        const void *b, const int32_t *offsets, const int32_t *index, int64_t fan, void *c,
+                        int32_t out_f32, void *workspace, int64_t workspace_bytes, void *stream) {
+    return grouped(kSegNT, rows, groups, n, k, a, a_rows, b, offsets, index, fan, c, out_f32, workspace,
+                   workspace_bytes, stream);
+}
+
+int gemm_f16_grouped_nn(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a, const void *b,
+                        const int32_t *offsets, void *c, int32_t out_f32, void *workspace, int64_t workspace_bytes,
+                        void *stream) {
+    return grouped(kSegNN, rows, groups, n, k, a, rows, b, offsets, nullptr, 1, c, out_f32, workspace, workspace_bytes,
+                   stream);
+}
+
+int gemm_f16_grouped_tn(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a, const void *b,
+                        const int32_t *offsets, void *c, int32_t out_f32, void *workspace, int64_t workspace_bytes,
+                        void *stream) {
+    return grouped(kSegTN, rows, groups, n, k, a, rows, b, offsets, nullptr, 1, c, out_f32, workspace, workspace_bytes,
+                   stream);
+}
+
+int64_t gemm_f16_lora_workspace(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64_t rank) {
+    const int rc = check_lora(rows, n, k, adapters, rank);
+    return rc != GEMM_F16_OK ? rc : rows * lora_h_ld(rank) * 4;
+}
+
+int gemm_f16_lora_nt(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64_t rank, const void *x, const void *w,
+                     const void *down, const void *up, const int32_t *ids, const int32_t *order,
+                     const int32_t *offsets, const float *scale, void *y, void *workspace, int64_t workspace_bytes,
+                     void *stream) {
+    int rc = check_lora(rows, n, k, adapters, rank);
+    if (rc != GEMM_F16_OK) return rc;
+    const int64_t need = gemm_f16_lora_workspace(rows, n, k, adapters, rank);
+    if (workspace_bytes < need) return GEMM_F16_EINVAL;
+    if (rows == 0 || n == 0) return GEMM_F16_OK;
+    const Buffer bufs[] = {{y, rows * n * 2, 2, true},
+                           {workspace, need, 16, true},
+                           {x, rows * k * 2, 2, false},
+                           {w, n * k * 2, 2, false},
+                           {down, adapters * rank * k * 2, 2, false},
+                           {up, adapters * rank * n * 2, 2, false},
+                           {ids, rows * 4, 4, false},
+                           {order, rows * 4, 4, false},
+                           {offsets, (adapters + 1) * 4, 4, false},
+                           {scale, scale ? adapters * 4 : 0, 4, false}};
+    rc = check_buffers(bufs);
+    if (rc != GEMM_F16_OK) return rc;
+    int cus;
+    rc = current_device(&cus);
+    if (rc != GEMM_F16_OK) return rc;
+
+    SegParams p = {};
+    p.a = static_cast<const _Float16 *>(x);
+    p.offsets = offsets;
+    p.a_rows = rows;
+    p.rows = (int32_t)rows;
+    p.k = (int32_t)k;
+    p.fan = 1;
+    p.adapters = (int32_t)adapters;
+    p.rank = (int32_t)rank;
+    p.h_ld = (int32_t)lora_h_ld(rank);
+    p.scale = scale;
+    // h = scale_s (x D_s^T), rows in adapter order
+    SegParams d = p;
+    d.b = static_cast<const _Float16 *>(down);
+    d.c = workspace;
+    d.index = order;
+    d.groups = (int32_t)adapters;
+    d.n = (int32_t)rank;
+    rc = status(launch_seg_staged(kSegNT, true, kSegLoraDown, d, (hipStream_t)stream));
+    if (rc != GEMM_F16_OK) return rc;
+    // x W^T + h U_s^T
+    p.b = static_cast<const _Float16 *>(w);
+    p.c = y;
+    p.order = order;
+    p.h = static_cast<const float *>(workspace);
+    p.up = static_cast<const _Float16 *>(up);
+    p.groups = 1;
+    p.n = (int32_t)n;
+    return status(launch_seg_staged(kSegNT, false, kSegLoraUp, p, (hipStream_t)stream));
+}
+
+}  // extern "C"

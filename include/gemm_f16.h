@@ -19,8 +19,9 @@
  * runtime allocated on the current device, e.g. through PyTorch).
  *
  * Ownership: the caller owns every buffer.  The library allocates no device
- * memory, keeps no pointer after the call returns and needs no workspace.
- * c must not overlap a or b.
+ * memory and keeps no pointer after the call returns; the dense products need
+ * no workspace, the segmented ones (at the end of this file) take the
+ * caller's.  c must not overlap a or b.
  *
  * Asynchrony: the work is enqueued on `stream` (a hipStream_t passed as
  * void*; NULL is the null stream) and the call returns without waiting.
@@ -188,6 +189,112 @@ int gemm_f16_select_tile(int64_t m, int64_t n, int64_t k);
  * grid of 2^31 tiles or more.  Pure host function: no HIP call.
  */
 int gemm_f16_select_xcd(int64_t num_m, int64_t num_n, int32_t swizzle, int32_t cus);
+
+/* ---- segmented products ------------------------------------------------------
+ *
+ * Matrix products over rows that fall into consecutive segments of ragged
+ * sizes: the tokens of each expert of a routed layer, or the requests of
+ * each low-rank adapter.  Segment g holds rows offsets[g] .. offsets[g+1]-1
+ * of `rows`; the sizes live on the GPU only and the host never waits for
+ * them.
+ *
+ * Common rules: device pointers, row-major dense operands, asynchronous on
+ * `stream`, the errors above; int32 arrays are 4-byte aligned.  offsets is
+ * int32 [groups+1], non-decreasing, offsets[0] read as 0, other values
+ * clamped to [0, rows].  Offsets, ids, indices and orders that break these
+ * rules give unspecified outputs but no access out of range.  An output
+ * must not overlap any input or the workspace (GEMM_F16_EOVERLAP).
+ * workspace: device memory of at least the bytes that the matching
+ * *_workspace function returns (0: may be NULL), 16-byte aligned, its
+ * content free to be overwritten until the call's work is done; too few
+ * bytes give GEMM_F16_EINVAL.
+ * Sums run in fp32, in an order that depends on the sizes alone: the same
+ * call gives the same bits.
+ */
+
+/*
+ * The plan of a routed batch: a stable sort of row numbers by group.
+ *   ids      int32 (id_bytes 4) or int64 (id_bytes 8) [rows]: the group of
+ *            each row; an id outside [0, groups) belongs to no group and
+ *            sorts behind all of them
+ *   order    int32 [rows]      row at each place of the sorted order
+ *   inverse  int32 [rows]      place of each row: order[inverse[r]] == r
+ *   offsets  int32 [groups+1]  first place of each group; offsets[groups]
+ *            is where the rows of no group begin
+ * 0 <= rows < 2^30, 1 <= groups <= 2048.
+ */
+int gemm_f16_group_rows(int64_t rows, int64_t groups, const void *ids, int32_t id_bytes,
+                        int32_t *order, int32_t *inverse, int32_t *offsets,
+                        void *workspace, int64_t workspace_bytes, void *stream);
+int64_t gemm_f16_group_rows_workspace(int64_t rows, int64_t groups);
+
+/*
+ * Products grouped by segment, with the segment g of row r:
+ *
+ *   grouped_nt   C[r][n] = sum_k A[src(r)][k] * B[g][n][k]      B [groups,N,K]
+ *   grouped_nn   C[r][n] = sum_k A[r][k] * B[g][k][n]           B [groups,K,N]
+ *   grouped_tn   C[g][k][n] = sum_{r in g} A[r][k] * B[r][n]    A [rows,K], B [rows,N]
+ *
+ * A and B are fp16, C is fp16 (out_f32 0; rounded once, to nearest even) or
+ * fp32 (out_f32 1).  grouped_nt reads A [a_rows,K] at src(r) = index[r] / fan
+ * (index NULL: r): with `order` of gemm_f16_group_rows as the index, row
+ * order[r] / fan is the token of the r-th routed row when each token has
+ * `fan` of them.  A row whose src lies outside [0, a_rows) is taken as
+ * zeros.  grouped_nn and grouped_tn with C's fp16 gradient in A give the
+ * gradients of grouped_nt by its input rows and by its weights.
+ * Rows behind offsets[groups] come out as zeros; so does C[g] of an empty
+ * segment (grouped_tn).
+ *
+ * rows, a_rows < 2^30; n < 2^30 (nn, tn: 2^25); k < 2^22; 1 <= groups <=
+ * 2^20; 1 <= fan; rows*n, groups*n*k < 2^47.
+ */
+int gemm_f16_grouped_nt(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a,
+                        int64_t a_rows, const void *b, const int32_t *offsets,
+                        const int32_t *index, int64_t fan, void *c, int32_t out_f32,
+                        void *workspace, int64_t workspace_bytes, void *stream);
+int gemm_f16_grouped_nn(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a,
+                        const void *b, const int32_t *offsets, void *c, int32_t out_f32,
+                        void *workspace, int64_t workspace_bytes, void *stream);
+int gemm_f16_grouped_tn(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a,
+                        const void *b, const int32_t *offsets, void *c, int32_t out_f32,
+                        void *workspace, int64_t workspace_bytes, void *stream);
+
+enum {
+    GEMM_F16_GROUPED_NT = 0,
+    GEMM_F16_GROUPED_NN = 1,
+    GEMM_F16_GROUPED_TN = 2
+};
+/* Workspace bytes of a grouped product (kind: GEMM_F16_GROUPED_*), or a
+ * negative status for invalid sizes. */
+int64_t gemm_f16_grouped_workspace(int32_t kind, int64_t rows, int64_t groups, int64_t n,
+                                   int64_t k);
+
+/*
+ * A projection shared by requests that each have a low-rank adapter of
+ * their own (or none):
+ *
+ *   Y[r][n] = fp16( sum_k X[r][k] W[n][k]
+ *                   + scale[s] * sum_j (sum_k X[r][k] D[s][j][k]) * U[s][n][j] ),  s = ids[r]
+ *
+ *   x        fp16 [rows,K]            w   fp16 [N,K]
+ *   down     fp16 [adapters,rank,K]   up  fp16 [adapters,N,rank]
+ *   ids      int32 [rows]: the adapter of each row; outside [0, adapters): none
+ *   order, offsets   of gemm_f16_group_rows(rows, adapters, ids, ...)
+ *   scale    fp32 [adapters], or NULL for ones
+ *   y        fp16 [rows,N]
+ *
+ * The inner product is kept in fp32 (or as two fp16 parts that hold 22 bits
+ * of it) until the second product, and Y is rounded once.
+ * rows, n < 2^30; k < 2^22; 1 <= rank <= 4096; 1 <= adapters <= 2^20;
+ * rows*n, n*k, adapters*rank*(n+k) < 2^47.
+ */
+int gemm_f16_lora_nt(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64_t rank,
+                     const void *x, const void *w, const void *down, const void *up,
+                     const int32_t *ids, const int32_t *order, const int32_t *offsets,
+                     const float *scale, void *y, void *workspace, int64_t workspace_bytes,
+                     void *stream);
+int64_t gemm_f16_lora_workspace(int64_t rows, int64_t n, int64_t k, int64_t adapters,
+                                int64_t rank);
 
 #ifdef __cplusplus
 }
