@@ -1,0 +1,17 @@
+// Adapters on direct-to-LDS tiles (see segments_direct.h).
+#include "segments_direct.h"
+
+namespace gemm_f16 {
+
+hipError_t launch_seg_lora(int tile, const SegParams &p, hipStream_t s) {
+    switch (tile) {
+        case kSeg256x128: return launch_seg_tile<kSegNT, Cfg<256, 128, 2, 2, 16>, true>(p, false, s);
+        case kSeg128x256: return launch_seg_tile<kSegNT, Cfg<128, 256, 2, 2, 16>, true>(p, false, s);
+        case kSeg128x128: return launch_seg_tile<kSegNT, Cfg<128, 128, 2, 2, 16>, true>(p, false, s);
+        case kSeg64x128: return launch_seg_tile<kSegNT, Cfg<64, 128, 2, 2, 16>, true>(p, false, s);
+        case kSeg32x128: return launch_seg_tile<kSegNT, Cfg<32, 128, 1, 4, 16>, true>(p, false, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace gemm_f16

@@ -1,0 +1,16 @@
+// C_g = A_g^T B_g on direct-to-LDS tiles (see segments_direct.h).
+#include "segments_direct.h"
+
+namespace gemm_f16 {
+
+hipError_t launch_seg_tn(int tile, bool f32, const SegParams &p, hipStream_t s) {
+    switch (tile) {
+        case kSeg256x256: return launch_seg_tile<kSegTN, Cfg<256, 256, 2, 2, 16>>(p, f32, s);
+        case kSeg256x128: return launch_seg_tile<kSegTN, Cfg<256, 128, 2, 2, 16>>(p, f32, s);
+        case kSeg128x256: return launch_seg_tile<kSegTN, Cfg<128, 256, 2, 2, 16>>(p, f32, s);
+        case kSeg128x128: return launch_seg_tile<kSegTN, Cfg<128, 128, 2, 2, 16>>(p, f32, s);
+        default: return hipErrorInvalidValue;
+    }
+}
+
+}  // namespace gemm_f16

@@ -355,7 +355,11 @@ __device__ __forceinline__ void lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *s
             for (int j = 0; j < C::FN; ++j) acc[j][i] *= s;
         }
     };
-    if (any_scaled) scale_acc(false);
+    acc_fence(acc);
+    if (any_scaled) {
+        scale_acc(false);
+        acc_fence(acc);
+    }
 
     for (int s = 0; s < p.adapters; ++s) {
         const int lo = max(seg_bound(p.offsets, s, p.rows) - row0, 0);
@@ -381,15 +385,21 @@ __device__ __forceinline__ void lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *s
                 *reinterpret_cast<half8 *>(smem + r * kRow + ((q ^ sw(r)) << 4)) = top;
                 *reinterpret_cast<half8 *>(smem + r * kRow + (((q + 4) ^ sw(r)) << 4)) = rest;
             }
+            int wild = 0;
             for (int x = tid; x < C::BN * 4; x += C::kThreads) {
                 const int r = x >> 2, q = x & 3, kv = p.rank - c - 8 * q;
                 int4v v = {0, 0, 0, 0};
                 if (n0 + r < p.n && kv > 0)
                     v = mask_chunk(load_chunk(up + (int64_t)(n0 + r) * p.rank + c + 8 * q, up_end), kv);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    wild |= (v[e] & 0x7c00) == 0x7c00 || (v[e] & 0x7c000000) == 0x7c000000;
                 *reinterpret_cast<int4v *>(smem + kB + r * kRow + ((q ^ sw(r)) << 4)) = v;
                 *reinterpret_cast<int4v *>(smem + kB + r * kRow + (((q + 4) ^ sw(r)) << 4)) = v;
             }
-            __syncthreads();
+            // A non-finite U_s must not reach the rows of other adapters, whose
+            // zeros in A would make it a NaN there.
+            const bool careful = __syncthreads_or(wild) && hi - lo < valid;
             half8 af[2][C::FM];
 #pragma unroll
             for (int i = 0; i < C::FM; ++i) {
@@ -398,25 +408,40 @@ __device__ __forceinline__ void lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *s
                 for (int ks = 0; ks < 2; ++ks)
                     af[ks][i] = *reinterpret_cast<const half8 *>(smem + r * kRow + (((4 * ks + lane / 16) ^ sw(r)) << 4));
             }
-#pragma unroll
-            for (int j = 0; j < C::FN; ++j) {
+            auto b_frag = [&](int ks, int j) {
                 const int r = wn * C::TN + j * 16 + lane % 16;
-                half8 bf[2];
+                return *reinterpret_cast<const half8 *>(smem + kB + r * kRow + (((4 * ks + lane / 16) ^ sw(r)) << 4));
+            };
+            if (!careful) {
 #pragma unroll
                 for (int ks = 0; ks < 2; ++ks)
-                    bf[ks] = *reinterpret_cast<const half8 *>(smem + kB + r * kRow + (((4 * ks + lane / 16) ^ sw(r)) << 4));
 #pragma unroll
-                for (int i = 0; i < C::FM; ++i) {
-                    // rows of other adapters keep their value: their zeros
-                    // times an infinity in U_s would be a NaN
-                    const int m = wm * C::TM + i * 16 + lane % 16;
-                    const floatx4 sum = Mfma<16>::run(bf[1], af[1][i], Mfma<16>::run(bf[0], af[0][i], acc[j][i]));
-                    if (m >= lo && m < hi) acc[j][i] = sum;
+                    for (int j = 0; j < C::FN; ++j) {
+                        const half8 bf = b_frag(ks, j);
+#pragma unroll
+                        for (int i = 0; i < C::FM; ++i) mfma16_tied(bf, af[ks][i], acc[j][i]);
+                    }
+            } else {
+                acc_fence(acc);
+#pragma unroll
+                for (int j = 0; j < C::FN; ++j) {
+                    const half8 b0 = b_frag(0, j), b1 = b_frag(1, j);
+#pragma unroll
+                    for (int i = 0; i < C::FM; ++i) {
+                        const int m = wm * C::TM + i * 16 + lane % 16;
+                        asm volatile("" : "+a"(acc[j][i]));  // one block at a time out of its AGPRs
+                        const floatx4 sum = Mfma<16>::run(b1, af[1][i], Mfma<16>::run(b0, af[0][i], floatx4{}));
+                        if (m >= lo && m < hi) acc[j][i] += sum;
+                        asm volatile("" : "+a"(acc[j][i]));
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
                 }
+                acc_fence(acc);
             }
             __syncthreads();
         }
     }
+    acc_fence(acc);
     if (any_scaled) scale_acc(true);
 }
 
@@ -602,6 +627,13 @@ int64_t group_blocks(int64_t rows);
 // counts: group_blocks(rows) * (groups + 1) ints, used with more than one block
 hipError_t launch_group_rows(int64_t rows, int groups, const void *ids, int id_bytes, int32_t *order, int32_t *inverse,
                              int32_t *offsets, int32_t *counts, hipStream_t s);
+// Direct-to-LDS kernels (segments_direct.h), by block tile.
+enum SegTileId : int { kSeg256x256, kSeg256x128, kSeg128x256, kSeg128x128, kSeg64x128, kSeg32x128, kSegTiles };
+hipError_t launch_seg_nt(int tile, bool f32, const SegParams &p, hipStream_t s);
+hipError_t launch_seg_nn(int tile, bool f32, const SegParams &p, hipStream_t s);
+hipError_t launch_seg_tn(int tile, bool f32, const SegParams &p, hipStream_t s);
+hipError_t launch_seg_lora(int tile, const SegParams &p, hipStream_t s);
+
 hipError_t launch_seg_staged(int kind, bool f32, int mode, SegParams p, hipStream_t s);
 
 }  // namespace gemm_f16

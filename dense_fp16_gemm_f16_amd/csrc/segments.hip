@@ -3,6 +3,7 @@
 #include "segments.h"
 
 #include <algorithm>
+#include <cstdlib>
 
 #include "device.h"
 #include "gemm_f16.h"
@@ -55,6 +56,59 @@ static int check_grouped(int kind, int64_t rows, int64_t groups, int64_t n, int6
 
 static int status(hipError_t e) { return e == hipSuccess ? GEMM_F16_OK : e == hipErrorInvalidValue ? GEMM_F16_EINVAL : GEMM_F16_EHIP; }
 
+// Whether the operands' rows can go straight into LDS: 16-byte chunks, and
+// a gathered A below 2 GiB (one descriptor spans it).
+static bool direct_rows(int kind, const SegParams &p) {
+    if ((((uintptr_t)p.a | (uintptr_t)p.b) % 16) != 0 || p.k % 8 != 0 || p.k == 0) return false;
+    if (kind != kSegNT && p.n % 8 != 0) return false;
+    return !(p.index || p.order) || p.a_rows * p.k * 2 < (int64_t(1) << 31);
+}
+
+static int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Block tile with the smallest modelled time c + a rounds k_tiles + b
+// tiles / cus (us; the dense product's model, auto_tile in gemm_f16.hip),
+// over the row tiles to expect: half a tile more per segment than the rows
+// fill.
+static int pick_tile(int kind, const SegParams &p, int cus) {
+    struct Cand {
+        int id, bm, bn;
+        double c, a, b;
+    };
+    static const Cand cands[] = {
+        {kSeg256x256, 256, 256, 8.280, 1.115, 6.212}, {kSeg256x128, 256, 128, 5.825, 0.663, 3.036},
+        {kSeg128x256, 128, 256, 5.856, 0.661, 2.886}, {kSeg128x128, 128, 128, 4.492, 0.436, 1.517},
+        {kSeg64x128, 64, 128, 3.545, 0.391, 0.780},   {kSeg32x128, 32, 128, 3.3, 0.30, 0.45},
+    };
+#ifdef GEMM_F16_SEG_TUNE
+    if (const char *force = std::getenv("SEG_TILE")) return std::atoi(force);
+#endif
+    const int64_t segments = std::min<int64_t>(p.groups, p.rows);
+    int best = kSeg128x128;
+    double best_t = 1e300;
+    for (const Cand &c : cands) {
+        if (kind == kSegTN && c.bm < 128) continue;
+        // lora_tiles next to 256 accumulators a lane would spill
+        if (p.order && c.id == kSeg256x256) continue;
+        double m_tiles;
+        int64_t k_tiles;
+        if (kind == kSegTN) {
+            m_tiles = (double)(cdiv64(p.k, c.bm) * p.groups);
+            k_tiles = cdiv64(cdiv64(p.rows, p.groups), 64);
+        } else {
+            m_tiles = (double)p.rows / c.bm + 0.5 * (double)segments;
+            k_tiles = cdiv64(p.k, 64);
+        }
+        const double tiles = m_tiles * (double)cdiv64(p.n, c.bn), rounds = (double)(int64_t)((tiles + cus - 1) / cus);
+        const double t = c.c + c.a * rounds * (double)k_tiles + c.b * tiles / cus;
+        if (t < best_t) {
+            best_t = t;
+            best = c.id;
+        }
+    }
+    return best;
+}
+
 static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a, int64_t a_rows,
                    const void *b, const int32_t *offsets, const int32_t *index, int64_t fan, void *c, int32_t out_f32,
                    void *workspace, int64_t workspace_bytes, void *stream) {
@@ -92,6 +146,16 @@ static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k,
     p.n = (int32_t)n;
     p.k = (int32_t)k;
     p.fan = (int32_t)fan;
+    if (direct_rows(kind, p)) {
+        const int tile = pick_tile(kind, p, cus);
+        hipError_t e;
+        switch (kind) {
+            case kSegNT: e = launch_seg_nt(tile, out_f32 != 0, p, (hipStream_t)stream); break;
+            case kSegNN: e = launch_seg_nn(tile, out_f32 != 0, p, (hipStream_t)stream); break;
+            default: e = launch_seg_tn(tile, out_f32 != 0, p, (hipStream_t)stream); break;
+        }
+        return status(e);
+    }
     return status(launch_seg_staged(kind, out_f32 != 0, kSegPlain, p, (hipStream_t)stream));
 }
 
@@ -221,6 +285,7 @@ int gemm_f16_lora_nt(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64
     p.up = static_cast<const _Float16 *>(up);
     p.groups = 1;
     p.n = (int32_t)n;
+    if (direct_rows(kSegNT, p)) return status(launch_seg_lora(pick_tile(kSegNT, p, cus), p, (hipStream_t)stream));
     return status(launch_seg_staged(kSegNT, false, kSegLoraUp, p, (hipStream_t)stream));
 }
 

@@ -1,0 +1,266 @@
+// Segmented products with operands loaded straight into LDS: 16-byte
+// aligned rows (K, and N where B or A is read along it, multiples of 8).
+#pragma once
+
+#include "segments.h"
+
+namespace gemm_f16 {
+
+// A configuration whose columns are C's rows: the layout of TN's A.
+template <class C>
+struct RowsAsCols : C {
+    static constexpr int BN = C::BM, FN = C::FM;
+};
+
+// A tile's place in the product and its operands' first rows.
+template <int KIND, class C, bool LORA>
+struct SegWork {
+    int g, row0, valid, n0, k_count;  // k_count: length of the contraction
+    bool live;
+
+    // false: past the last tile
+    __device__ __forceinline__ bool find(const SegParams &p, uint32_t pid, int lane) {
+        live = true;
+        if constexpr (KIND == kSegTN) {
+            const uint32_t per = (uint32_t)p.num_m * (uint32_t)p.num_n;
+            g = (int)(pid / per);
+            const TileCoord tc = tile_coord<uint32_t>(pid % per, p.num_m, p.num_n, 4, false);
+            row0 = (int)tc.m_block * C::BM;
+            n0 = (int)tc.n_block * C::BN;
+            valid = min(C::BM, p.k - row0);
+            k_count = max(seg_bound(p.offsets, g + 1, p.rows) - seg_bound(p.offsets, g, p.rows), 0);
+            return true;
+        }
+        TileCoord tc;
+        if constexpr (LORA) {
+            g = 0;
+            tc = tile_coord<uint32_t>(pid, (p.rows + C::BM - 1) / C::BM, p.num_n, 4, true);
+            row0 = (int)tc.m_block * C::BM;
+            valid = min(C::BM, p.rows - row0);
+        } else {
+            SegMap<C::BM> map;
+            map.init(p, lane);
+            if (pid >= (uint32_t)map.total * (uint32_t)p.num_n) return false;
+            tc = tile_coord<uint32_t>(pid, map.total, p.num_n, 4, true);
+            const SegTile st = map.find(p, (int)tc.m_block, lane);
+            g = st.g;
+            row0 = st.row0;
+            valid = st.valid;
+            live = g < p.groups;
+        }
+        n0 = (int)tc.n_block * C::BN;
+        k_count = live ? p.k : 0;
+        return true;
+    }
+};
+
+// One workgroup per tile.  The K loop is gemm_f16_direct_ahead_kernel's:
+// two LDS stages, both k steps' fragments of K-tile t+1 read during K-tile
+// t, a release and an acquire barrier per K-tile.
+template <int KIND, class C, bool F32, bool LORA>
+__global__ __launch_bounds__(C::kThreads)
+__attribute__((amdgpu_waves_per_eu(C::kMinWavesPerEU, C::kMinWavesPerEU)))
+void seg_tile_kernel(const SegParams p) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
+    constexpr int TM = C::TM, TN = C::TN, FM = C::FM, FN = C::FN;
+    static_assert(C::MB == 16 && C::KS == 2, "two 32-wide k steps per K-tile");
+    using OpA = std::conditional_t<KIND == kSegTN, NMajorDirect<RowsAsCols<C>, false>, KMajorDirect<C, C::BM, false>>;
+    using OpB = std::conditional_t<KIND == kSegNT, KMajorDirect<C, C::BN, false>, NMajorDirect<C, false>>;
+    constexpr int kLdsB = OpA::kLdsBytes, kLds = OpA::kLdsBytes + OpB::kLdsBytes;
+    constexpr int LA = OpA::kLoads, L = OpA::kLoads + OpB::kLoads;
+    static_assert(kLds <= 160 * 1024, "LDS budget");
+    static_assert(2 * L < 64, "vmcnt range");
+    __shared__ __attribute__((aligned(1024))) char smem[kLds];
+    __shared__ float row_scale[LORA ? C::BM : 1];
+    GEMM_POISON_LDS(smem);
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wm = wave / C::WN, wn = wave % C::WN;
+
+    SegWork<KIND, C, LORA> w;
+    if (!w.find(p, blockIdx.x, lane)) return;
+    const int kt_count = (w.k_count + C::BK - 1) / C::BK;
+
+    OpA opa;
+    OpB opb;
+    if constexpr (KIND == kSegTN) {
+        const int64_t lo = seg_bound(p.offsets, w.g, p.rows);
+        opa.init(p.a + lo * p.k, w.row0, p.k, w.k_count, kt_count, wave, lane, wm * TM, 0);
+        opb.init(p.b + lo * p.n, w.n0, p.n, w.k_count, kt_count, wave, lane, wn * TN, kLdsB);
+    } else {
+        const int32_t *from = LORA ? p.order : p.index;
+        if (from) {
+            // gathered rows: the descriptor spans A (below 2 GiB), each lane's
+            // rows start where the index says
+            opa.init(p.a, (int)p.a_rows, p.k, kt_count, wave, lane, wm * TM, 0);
+#pragma unroll
+            for (int i = 0; i < OpA::kLoads; ++i) {
+                const int r = (i * C::kWaves + wave) * 8 + (lane >> 3);
+                uint32_t off = kOutOfRange;
+                if (w.live && r < w.valid) {
+                    const int v = from[w.row0 + r];
+                    const int64_t src = v < 0 ? -1 : LORA ? v : v / p.fan;
+                    if (src >= 0 && src < p.a_rows) off = (uint32_t)((src * p.k + opa.kc) * 2);
+                }
+                opa.voff[i] = off;
+            }
+        } else {
+            opa.init(p.a + (int64_t)w.row0 * p.k, w.valid, p.k, kt_count, wave, lane, wm * TM, 0);
+        }
+        const _Float16 *b = p.b + (int64_t)(w.live ? w.g : 0) * p.n * p.k;
+        if constexpr (KIND == kSegNT)
+            opb.init(b + (int64_t)w.n0 * p.k, min(C::BN, p.n - w.n0), p.k, kt_count, wave, lane, wn * TN, kLdsB);
+        else
+            opb.init(b, w.n0, p.n, p.k, kt_count, wave, lane, wn * TN, kLdsB);
+    }
+
+    floatx4 acc[FN][FM];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int i = 0; i < FM; ++i) acc[j][i] = floatx4{};
+    acc_fence(acc);
+
+    half8 af[3][FM];
+    half8 bf[3][FN];
+    constexpr int NR = FM + FN;  // fragment reads per k step
+    // in the order the MFMAs consume them: B0, A0..A(FM-1), B1..
+    auto read_frag = [&](int buf, int stage, int ks, int r) {
+        if (r == 0)
+            bf[buf][0] = opb.read(smem, stage, ks, 0);
+        else if (r <= FM)
+            af[buf][r - 1] = opa.read(smem, stage, ks, r - 1);
+        else
+            bf[buf][r - FM] = opb.read(smem, stage, ks, r - FM);
+    };
+    auto load = [&](auto s_c, int t, int i) {
+        constexpr int S = decltype(s_c)::value;
+        if (i < LA)
+            opa.template load<S>(smem, t, i);
+        else
+            opb.template load<S>(smem, t, i - LA);
+    };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    constexpr int NM = FM * FN;
+    constexpr int kRelAt = GEMM_AHEAD_REL_MFMA < NM ? GEMM_AHEAD_REL_MFMA : NM - 1;
+    constexpr int kAcqAt = GEMM_AHEAD_ACQ_MFMA < NM ? GEMM_AHEAD_ACQ_MFMA : NM - 1;
+    constexpr int L0 = L * GEMM_AHEAD_STEP0_LOADS / 16;  // loads of K-tile t+2 in step 0
+
+    if (kt_count > 0) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) load(S0{}, 0, i);
+#pragma unroll
+        for (int i = 0; i < L; ++i) load(S1{}, 1, i);
+    }
+    vm_barrier<L>();
+#pragma unroll
+    for (int r = 0; r < NR; ++r) read_frag(0, 0, 0, r);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) read_frag(1, 0, 1, r);
+
+    auto k_iter = [&](auto s_c, int t) {
+        constexpr int S = decltype(s_c)::value;
+        constexpr int SN = S ^ 1;
+        constexpr int B1 = S == 0 ? 1 : 2;   // this K-tile's step-1 buffer
+        constexpr int NB1 = S == 0 ? 2 : 1;  // the next K-tile's
+        static_range<0, NM>([&](auto m_c) {
+            constexpr int m = decltype(m_c)::value;
+            constexpr int j = m / FM, i = (j & 1) ? FM - 1 - m % FM : m % FM;
+            mfma16_tied(bf[0][j], af[0][i], acc[j][i]);
+            if constexpr (m == kRelAt) lgkm_barrier();
+            if constexpr (m >= kRelAt) {
+                constexpr int q = m - kRelAt, slots = NM - kRelAt;
+                static_range<q * L0 / slots, (q + 1) * L0 / slots>(
+                    [&](auto o_c) { load(s_c, t + 2, decltype(o_c)::value); });
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+#pragma unroll
+        for (int j = 0; j < FN; ++j) asm volatile("" ::"v"(bf[0][j]));
+#pragma unroll
+        for (int i = 0; i < FM; ++i) asm volatile("" ::"v"(af[0][i]));
+        static_range<0, NM>([&](auto m_c) {
+            constexpr int m = decltype(m_c)::value;
+            constexpr int j = m / FM, i = (j & 1) ? FM - 1 - m % FM : m % FM;
+            mfma16_tied(bf[B1][j], af[B1][i], acc[j][i]);
+            if constexpr (m == kAcqAt) vm_only_barrier<L0>();
+            if constexpr (m >= kAcqAt) {
+                constexpr int nl = L - L0, total = 2 * NR + nl, slots = NM - kAcqAt, q = m - kAcqAt;
+                // R R L R R L ...: the reads first while both remain
+                static_range<q * total / slots, (q + 1) * total / slots>([&](auto o_c) {
+                    constexpr int o = decltype(o_c)::value;
+                    constexpr int groups = (2 * NR) / 2 < nl ? (2 * NR) / 2 : nl;  // (R, R, L) groups
+                    constexpr bool in_groups = o < 3 * groups;
+                    constexpr bool is_read = in_groups ? (o % 3 != 2) : (2 * NR > 2 * groups);
+                    constexpr int idx = in_groups ? (is_read ? (o / 3) * 2 + (o % 3) : o / 3)
+                                                  : (is_read ? 2 * groups + (o - 3 * groups) : groups + (o - 3 * groups));
+                    if constexpr (is_read) {
+                        constexpr int ks = idx / NR, r = idx % NR;
+                        read_frag(ks == 0 ? 0 : NB1, SN, ks, r);
+                    } else {
+                        load(s_c, t + 2, L0 + idx);
+                    }
+                });
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+#pragma unroll
+        for (int j = 0; j < FN; ++j) asm volatile("" ::"v"(bf[B1][j]));
+#pragma unroll
+        for (int i = 0; i < FM; ++i) asm volatile("" ::"v"(af[B1][i]));
+    };
+    int kt = 0;
+    for (; kt + 1 < kt_count; kt += 2) {
+        k_iter(S0{}, kt);
+        k_iter(S1{}, kt + 1);
+    }
+    if (kt < kt_count) k_iter(S0{}, kt);
+
+    vm_barrier<0>();  // no load is still writing LDS when C is staged there
+    acc_fence(acc);
+
+    constexpr int kWaveBytes = kLds / C::kWaves;
+    char *const stg = smem + wave * kWaveBytes;
+    lds_barrier();
+    const int row0 = w.row0;
+    if constexpr (LORA) {
+        lora_tiles<C>(acc, smem, row_scale, p, row0, w.valid, w.n0, tid, lane, wm, wn);
+        const int32_t *order = p.order;
+        const int rows = p.rows;
+        seg_store<C, F32, kWaveBytes>(acc, stg, p.c, w.valid, p.n, w.n0, wm, wn, lane, [&](int r) {
+            return min(max(order[row0 + r], 0), rows - 1);
+        });
+    } else if constexpr (KIND == kSegTN) {
+        using Out = std::conditional_t<F32, float, _Float16>;
+        Out *c = static_cast<Out *>(p.c) + (int64_t)w.g * p.k * p.n;
+        seg_store<C, F32, kWaveBytes>(acc, stg, c, w.valid, p.n, w.n0, wm, wn, lane, [&](int r) { return row0 + r; });
+    } else {
+        seg_store<C, F32, kWaveBytes>(acc, stg, p.c, w.valid, p.n, w.n0, wm, wn, lane, [&](int r) { return row0 + r; });
+    }
+#endif
+}
+
+// Launch of tile C: the grid holds every tile that any sizes could need.
+template <int KIND, class C, bool LORA = false>
+hipError_t launch_seg_tile(SegParams p, bool f32, hipStream_t s) {
+    p.num_n = (p.n + C::BN - 1) / C::BN;
+    int64_t grid;
+    if constexpr (KIND == kSegTN) {
+        p.num_m = (p.k + C::BM - 1) / C::BM;
+        grid = (int64_t)p.groups * p.num_m * p.num_n;
+    } else {
+        const int64_t m_tiles = LORA ? (p.rows + C::BM - 1) / C::BM : seg_row_tiles(p.rows, p.groups, C::BM);
+        p.num_m = (int32_t)m_tiles;
+        grid = m_tiles * p.num_n;
+    }
+    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    if constexpr (LORA)
+        return launch_seg(seg_tile_kernel<KIND, C, false, LORA>, grid, C::kThreads, s, p);
+    else
+        return f32 ? launch_seg(seg_tile_kernel<KIND, C, true, LORA>, grid, C::kThreads, s, p)
+                   : launch_seg(seg_tile_kernel<KIND, C, false, LORA>, grid, C::kThreads, s, p);
+}
+
+}  // namespace gemm_f16
