@@ -5,6 +5,7 @@ namespace gemm_f16 {
 
 hipError_t launch_seg_lora(int tile, const SegParams &p, hipStream_t s) {
     switch (tile) {
+        case kSeg256x256: return launch_seg_tile<kSegNT, Cfg<256, 256, 2, 2, 16>, true>(p, false, s);
         case kSeg256x128: return launch_seg_tile<kSegNT, Cfg<256, 128, 2, 2, 16>, true>(p, false, s);
         case kSeg128x256: return launch_seg_tile<kSegNT, Cfg<128, 256, 2, 2, 16>, true>(p, false, s);
         case kSeg128x128: return launch_seg_tile<kSegNT, Cfg<128, 128, 2, 2, 16>, true>(p, false, s);
@@ -12,6 +13,18 @@ hipError_t launch_seg_lora(int tile, const SegParams &p, hipStream_t s) {
         case kSeg32x128: return launch_seg_tile<kSegNT, Cfg<32, 128, 1, 4, 16>, true>(p, false, s);
         default: return hipErrorInvalidValue;
     }
+}
+
+hipError_t launch_lora_down(SegParams p, int splits, hipStream_t s) {
+    using C = Cfg<64, 64, 2, 2, 16>;
+    constexpr int S = 6;
+    p.num_n = (p.h_ld + C::BN - 1) / C::BN;
+    p.num_m = (int32_t)seg_row_tiles(p.rows, p.groups, C::BM);
+    const int64_t grid = (int64_t)p.num_m * p.num_n;
+    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    void *args[] = {&p};
+    return hipLaunchKernel(reinterpret_cast<const void *>(seg_ring_kernel<kSegNT, C, S, true, true>),
+                           dim3((unsigned)grid, (unsigned)splits), dim3(C::kThreads), args, 0, s);
 }
 
 }  // namespace gemm_f16

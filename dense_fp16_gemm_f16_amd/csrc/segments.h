@@ -38,6 +38,7 @@ struct SegParams {
     const _Float16 *up;     // [adapters, n, rank]
     const float *scale;     // [adapters]: multiplies the rows of h (null: 1)
     int32_t adapters, rank, h_ld;
+    int32_t h_parts;        // h is the sum of this many [rows, h_ld] arrays, one after the other
 };
 
 // Segment bounds, clamped so that any content of offsets stays in range.
@@ -124,6 +125,7 @@ struct SegMap {
 // kernels.h use, so both share their fragment reads.
 
 typedef int int4u __attribute__((ext_vector_type(4), aligned(2)));
+typedef int int2u __attribute__((ext_vector_type(2), aligned(2)));
 
 // 8 elements from p; those at or past end (the tensor's end) are zero and
 // never touched.
@@ -309,140 +311,207 @@ __device__ __forceinline__ void seg_store(const floatx4 (&acc)[C::FN][C::FM], ch
 
 // ---- adapters: the low-rank product on top of a tile ---------------------------
 //
-// Adds scale_s (x D_s^T) U_s^T to a tile of x W^T whose rows are sorted by
-// adapter: for each adapter with rows in the tile and each 32 of its ranks,
-// one K-tile of 64 whose A half is h = scale_s x D_s^T, zero in rows of
-// other adapters, and whose B half is U_s.  h is fp32: its fp16 rounding
-// and the rest that the rounding leaves take the K-tile's two 32-wide steps
-// (h = hi + lo to 2^-22), against U_s twice.  Rows whose |h| passes fp16's
-// range are scaled by a power of two, and the accumulators with them, so
-// the sum stays what fp32 gives.
-template <class C>
-__device__ __forceinline__ void lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *smem, float *row_scale,
-                                           const SegParams &p, int row0, int valid, int n0, int tid, int lane, int wm,
-                                           int wn) {
+// Adds h U_s^T, h = scale_s x D_s^T in fp32, to a tile of x W^T whose rows
+// are sorted by adapter: for each adapter with rows in the tile and each 32
+// of its ranks, one K-tile whose A is h, zero in rows of other adapters,
+// and whose B is U_s.  h has fp32's range, so it goes through the MFMA as
+// two bf16 parts (h = h0 + h1 to 2^-18 of it) and U_s as two that hold it
+// exactly; the product leaves out h1 u1, at most 2^-18 of h U.  Against the
+// 2^-11 half step of y, one fp16 part would have cost accuracy and range.
+//
+// An infinity or NaN in U_s would reach the rows of other adapters as
+// 0 * inf: it is taken as 0 here, and lora_wild adds its products to the
+// rows of its adapter afterwards.
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ void mfma16_tied_bf16(bf16x8 a, bf16x8 b, floatx4 &c) {
+    asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+
+// The adapters with rows in [row0, row0 + valid), in order: lane l looks at
+// adapter base + l.
+struct LoraWalk {
+    int base = -kWave, seg_lo = 0, seg_hi = 0;
+    uint64_t todo = 0;
+    int s = -1, lo = 0, hi = 0;  // the current one (-1: none left), its rows inside the tile
+
+    __device__ __forceinline__ void next(const SegParams &p, int row0, int valid, int lane) {
+        while (todo == 0 && base + kWave < p.adapters) {
+            base += kWave;
+            const int t = base + lane;
+            seg_lo = seg_hi = 0;
+            if (t < p.adapters) {
+                seg_lo = max(seg_bound(p.offsets, t, p.rows) - row0, 0);
+                seg_hi = min(seg_bound(p.offsets, t + 1, p.rows) - row0, valid);
+            }
+            todo = __ballot(seg_lo < seg_hi);
+        }
+        const int who = todo ? __builtin_ctzll(todo) : 0;
+        s = todo ? base + who : -1;
+        todo &= todo - 1;
+        lo = __builtin_amdgcn_readlane(seg_lo, who);
+        hi = __builtin_amdgcn_readlane(seg_hi, who);
+    }
+};
+
+// Returns (to every thread) whether some U_s of the tile is not finite.
+// votes: one int per wave, in the kernel's one LDS array (a library vote
+// would bring an array of its own, see seg_tile_kernel).  RANK4: the rank is
+// a multiple of 4, so half chunks lie wholly inside a row of U_s; the tails
+// of other ranks cost scalar registers that the 256-wide tiles do not have.
+template <class C, bool RANK4>
+__device__ __forceinline__ bool lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *smem, int *votes, const SegParams &p,
+                                           int row0, int valid, int n0, int tid, int lane, int wm, int wn) {
     constexpr int kRow = 128, kB = C::BM * kRow;
     auto sw = [](int r) { return (r >> 1) & 7; };
-    // power of two that takes a row's largest |h| below 2^15
-    int scaled = 0;
-    for (int r = tid; r < C::BM; r += C::kThreads) {
-        float top = 0.0f;
-        if (r < valid) {
-            const float *h = p.h + (int64_t)(row0 + r) * p.h_ld;
-            for (int q = 0; q < p.h_ld; q += 4) {
-                const floatx4 v = *reinterpret_cast<const floatx4 *>(h + q);
+    // This thread's chunks of one K-tile: h's 8 ranks at 8 (x % 4) of tile
+    // rows x / 4, and U's.  Loaded one K-tile ahead.
+    constexpr int HA = (C::BM * 4 + C::kThreads - 1) / C::kThreads, HB = C::BN * 4 / C::kThreads;
+    static_assert(HB * C::kThreads == C::BN * 4, "whole passes");
+    floatx4 h0[HA], h1[HA];
+    int4v u[HB];
+    const _Float16 *up_end = p.up + (int64_t)p.adapters * p.n * p.rank;
+    auto fetch = [&](const LoraWalk &w, int c) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float m = fabsf(v[e]);
-                    if (m < __builtin_inff()) top = fmaxf(top, m);  // infinities and NaN stay what they are
+        for (int i = 0; i < HA; ++i) {
+            const int x = i * C::kThreads + tid, r = x >> 2;
+            h0[i] = h1[i] = floatx4{};
+            if (r >= w.lo && r < w.hi) {
+                const float *h = p.h + (int64_t)(row0 + r) * p.h_ld + c + 8 * (x & 3);
+                for (int q = 0; q < p.h_parts; ++q, h += (int64_t)p.rows * p.h_ld) {
+                    h0[i] += *reinterpret_cast<const floatx4 *>(h);
+                    h1[i] += *reinterpret_cast<const floatx4 *>(h + 4);
                 }
             }
         }
-        float s = 1.0f;
-        if (top >= 32768.0f) {
-            s = ldexpf(1.0f, 14 - ilogbf(top));
-            scaled = 1;
-        }
-        row_scale[r] = s;
-    }
-    const bool any_scaled = __syncthreads_or(scaled);
-    auto scale_acc = [&](bool back) {
+        const _Float16 *up = p.up + (int64_t)w.s * p.n * p.rank;
 #pragma unroll
-        for (int i = 0; i < C::FM; ++i) {
-            float s = row_scale[wm * C::TM + i * 16 + lane % 16];
-            if (back) s = 1.0f / s;  // a power of two: exact
-#pragma unroll
-            for (int j = 0; j < C::FN; ++j) acc[j][i] *= s;
+        for (int i = 0; i < HB; ++i) {
+            const int x = i * C::kThreads + tid, r = n0 + (x >> 2), k = c + 8 * (x & 3);
+            u[i] = int4v{0, 0, 0, 0};
+            const _Float16 *row = up + (int64_t)r * p.rank + k;
+            if constexpr (RANK4) {
+                if (r < p.n && k < p.rank) {
+                    const int2u v = *reinterpret_cast<const int2u *>(row);
+                    u[i][0] = v[0];
+                    u[i][1] = v[1];
+                }
+                if (r < p.n && k + 4 < p.rank) {
+                    const int2u v = *reinterpret_cast<const int2u *>(row + 4);
+                    u[i][2] = v[0];
+                    u[i][3] = v[1];
+                }
+            } else {
+                if (r < p.n && k < p.rank) u[i] = mask_chunk(load_chunk(row, up_end), p.rank - k);
+            }
         }
     };
-    acc_fence(acc);
-    if (any_scaled) {
-        scale_acc(false);
-        acc_fence(acc);
-    }
 
-    for (int s = 0; s < p.adapters; ++s) {
-        const int lo = max(seg_bound(p.offsets, s, p.rows) - row0, 0);
-        const int hi = min(seg_bound(p.offsets, s + 1, p.rows) - row0, valid);
-        if (lo >= hi) continue;
-        const _Float16 *up = p.up + (int64_t)s * p.n * p.rank;
-        const _Float16 *up_end = p.up + (int64_t)p.adapters * p.n * p.rank;
-        for (int c = 0; c < p.rank; c += 32) {
-            for (int x = tid; x < C::BM * 4; x += C::kThreads) {
-                const int r = x >> 2, q = x & 3;
-                half8 top = {}, rest = {};
-                if (r >= lo && r < hi) {
-                    const float *h = p.h + (int64_t)(row0 + r) * p.h_ld + c + 8 * q;
-                    const float f = row_scale[r];
+    int wild = 0, c = 0;
+    LoraWalk w;
+    w.next(p, row0, valid, lane);
+    if (w.s >= 0) fetch(w, 0);
+    while (w.s >= 0) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float v = h[e] * f;
-                        top[e] = (_Float16)v;
-                        const float d = v - (float)top[e];
-                        rest[e] = (_Float16)(fabsf(v) < __builtin_inff() ? d : 0.0f);
-                    }
+        for (int i = 0; i < HA; ++i) {
+            const int x = i * C::kThreads + tid, r = x >> 2, q = x & 3;
+            if (HA * C::kThreads > C::BM * 4 && r >= C::BM) continue;
+            bf16x8 top, rest;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = e < 4 ? h0[i][e & 3] : h1[i][e & 3];
+                top[e] = (__bf16)v;
+                rest[e] = (__bf16)(fabsf(v) < __builtin_inff() ? v - (float)top[e] : 0.0f);
+            }
+            *reinterpret_cast<bf16x8 *>(smem + r * kRow + ((q ^ sw(r)) << 4)) = top;
+            *reinterpret_cast<bf16x8 *>(smem + r * kRow + (((q + 4) ^ sw(r)) << 4)) = rest;
+        }
+#pragma unroll
+        for (int i = 0; i < HB; ++i) {
+            const int x = i * C::kThreads + tid, r = x >> 2, q = x & 3;
+            const half8 v = __builtin_bit_cast(half8, u[i]);
+            bf16x8 top, rest;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float f = (float)v[e];
+                if (!(fabsf(f) < __builtin_inff())) {
+                    f = 0.0f;
+                    wild = 1;
                 }
-                *reinterpret_cast<half8 *>(smem + r * kRow + ((q ^ sw(r)) << 4)) = top;
-                *reinterpret_cast<half8 *>(smem + r * kRow + (((q + 4) ^ sw(r)) << 4)) = rest;
+                top[e] = (__bf16)f;
+                rest[e] = (__bf16)(f - (float)top[e]);  // exact: at most 3 bits are left
             }
-            int wild = 0;
-            for (int x = tid; x < C::BN * 4; x += C::kThreads) {
-                const int r = x >> 2, q = x & 3, kv = p.rank - c - 8 * q;
-                int4v v = {0, 0, 0, 0};
-                if (n0 + r < p.n && kv > 0)
-                    v = mask_chunk(load_chunk(up + (int64_t)(n0 + r) * p.rank + c + 8 * q, up_end), kv);
+            *reinterpret_cast<bf16x8 *>(smem + kB + r * kRow + ((q ^ sw(r)) << 4)) = top;
+            *reinterpret_cast<bf16x8 *>(smem + kB + r * kRow + (((q + 4) ^ sw(r)) << 4)) = rest;
+        }
+        lds_barrier();
+        c += 32;
+        if (c >= p.rank) {
+            w.next(p, row0, valid, lane);
+            c = 0;
+        }
+        if (w.s >= 0) fetch(w, c);
+
+        // u0 h0 and u1 h0, then u0 h1
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    wild |= (v[e] & 0x7c00) == 0x7c00 || (v[e] & 0x7c000000) == 0x7c000000;
-                *reinterpret_cast<int4v *>(smem + kB + r * kRow + ((q ^ sw(r)) << 4)) = v;
-                *reinterpret_cast<int4v *>(smem + kB + r * kRow + (((q + 4) ^ sw(r)) << 4)) = v;
-            }
-            // A non-finite U_s must not reach the rows of other adapters, whose
-            // zeros in A would make it a NaN there.
-            const bool careful = __syncthreads_or(wild) && hi - lo < valid;
-            half8 af[2][C::FM];
+        for (int ka = 0; ka < 2; ++ka) {
+            bf16x8 af[C::FM];
 #pragma unroll
             for (int i = 0; i < C::FM; ++i) {
                 const int r = wm * C::TM + i * 16 + lane % 16;
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks)
-                    af[ks][i] = *reinterpret_cast<const half8 *>(smem + r * kRow + (((4 * ks + lane / 16) ^ sw(r)) << 4));
+                af[i] = *reinterpret_cast<const bf16x8 *>(smem + r * kRow + (((4 * ka + lane / 16) ^ sw(r)) << 4));
             }
-            auto b_frag = [&](int ks, int j) {
-                const int r = wn * C::TN + j * 16 + lane % 16;
-                return *reinterpret_cast<const half8 *>(smem + kB + r * kRow + (((4 * ks + lane / 16) ^ sw(r)) << 4));
-            };
-            if (!careful) {
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks)
-#pragma unroll
-                    for (int j = 0; j < C::FN; ++j) {
-                        const half8 bf = b_frag(ks, j);
-#pragma unroll
-                        for (int i = 0; i < C::FM; ++i) mfma16_tied(bf, af[ks][i], acc[j][i]);
-                    }
-            } else {
-                acc_fence(acc);
+            for (int kb = 0; kb < 2 - ka; ++kb)
 #pragma unroll
                 for (int j = 0; j < C::FN; ++j) {
-                    const half8 b0 = b_frag(0, j), b1 = b_frag(1, j);
+                    const int r = wn * C::TN + j * 16 + lane % 16;
+                    const bf16x8 bf = *reinterpret_cast<const bf16x8 *>(smem + kB + r * kRow +
+                                                                        (((4 * kb + lane / 16) ^ sw(r)) << 4));
 #pragma unroll
-                    for (int i = 0; i < C::FM; ++i) {
-                        const int m = wm * C::TM + i * 16 + lane % 16;
-                        asm volatile("" : "+a"(acc[j][i]));  // one block at a time out of its AGPRs
-                        const floatx4 sum = Mfma<16>::run(b1, af[1][i], Mfma<16>::run(b0, af[0][i], floatx4{}));
-                        if (m >= lo && m < hi) acc[j][i] += sum;
-                        asm volatile("" : "+a"(acc[j][i]));
-                        __builtin_amdgcn_sched_barrier(0);
-                    }
+                    for (int i = 0; i < C::FM; ++i) mfma16_tied_bf16(bf, af[i], acc[j][i]);
                 }
-                acc_fence(acc);
-            }
-            __syncthreads();
         }
+        lds_barrier();
     }
     acc_fence(acc);
-    if (any_scaled) scale_acc(true);
+    const uint64_t ballot = __ballot(wild);
+    if (lane == 0) votes[tid / kWave] = ballot != 0;
+    lds_barrier();
+    int r = 0;
+#pragma unroll
+    for (int q = 0; q < C::kWaves; ++q) r |= votes[q];
+    return __builtin_amdgcn_readfirstlane(r) != 0;
+}
+
+// Adds the products with the elements of U_s that are not finite to the
+// stored tile (never on a model's path: such weights are broken, and this
+// keeps the other adapters' rows whole).
+template <class C>
+__device__ __forceinline__ void lora_wild(const SegParams &p, int row0, int valid, int n0, int tid, int lane) {
+    __threadfence();
+    __syncthreads();  // the tile is stored
+    const int cols = min(C::BN, p.n - n0);
+    LoraWalk w;
+    for (w.next(p, row0, valid, lane); w.s >= 0; w.next(p, row0, valid, lane)) {
+        for (int r = row0 + w.lo; r < row0 + w.hi; ++r) {
+            _Float16 *y = static_cast<_Float16 *>(p.c) + (int64_t)min(max(p.order[r], 0), p.rows - 1) * p.n + n0;
+            for (int n = tid; n < cols; n += C::kThreads) {
+                const _Float16 *up = p.up + ((int64_t)w.s * p.n + n0 + n) * p.rank;
+                float sum = 0.0f;
+#pragma unroll 1
+                for (int j = 0; j < p.rank; ++j) {
+                    const float f = (float)up[j];
+                    if (fabsf(f) < __builtin_inff()) continue;
+                    float h = 0.0f;
+                    for (int q = 0; q < p.h_parts; ++q) h += p.h[((int64_t)q * p.rows + r) * p.h_ld + j];
+                    sum += h * f;
+                }
+                if (!(fabsf(sum) < __builtin_inff())) y[n] = (_Float16)((float)y[n] + sum);
+            }
+        }
+    }
 }
 
 // ---- the any-alignment kernel --------------------------------------------------
@@ -450,22 +519,20 @@ __device__ __forceinline__ void lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *s
 // One workgroup per tile, operands staged through registers one K-tile
 // ahead, two LDS stages, one barrier per K-tile.  Every size, alignment and
 // gather.
-enum SegMode : int {
-    kSegPlain = 0,
-    kSegLoraDown = 1,  // NT by adapter into fp32 h: columns past n up to h_ld are zeros, rows times scale[g]
-    kSegLoraUp = 2     // x W^T over rows sorted by adapter, then lora_tiles; rows leave through order
-};
-
-template <int KIND, class C, bool F32, int MODE>
+// LORA: x W^T over rows sorted by adapter, then lora_tiles; rows leave through
+// order.
+template <int KIND, class C, bool F32, bool LORA>
 __global__ __launch_bounds__(C::kThreads) void seg_staged_kernel(const SegParams p) {
     static_assert(C::MB == 16 && C::KS == 2, "16x16x32 tiles");
-    static_assert(MODE == kSegPlain || KIND == kSegNT, "adapters are NT products");
+    static_assert(!LORA || KIND == kSegNT, "adapters are NT products");
     using OpA = std::conditional_t<KIND == kSegTN, NMajorStaged<C, C::BM, C::FM>, KMajorStaged<C, C::BM>>;
     using OpB = std::conditional_t<KIND == kSegNT, KMajorStaged<C, C::BN>, NMajorStaged<C, C::BN, C::FN>>;
     constexpr int kLdsB = 2 * OpA::kStage, kLds = kLdsB + 2 * OpB::kStage;
-    static_assert(kLds <= 160 * 1024, "LDS budget");
-    __shared__ __attribute__((aligned(1024))) char smem[kLds];
-    __shared__ float row_scale[MODE == kSegLoraUp ? C::BM : 1];
+    // one LDS array: with two, the compiler waits for every load in flight
+    // before each fragment read
+    constexpr int kVotes = LORA ? 64 : 0;
+    static_assert(kLds + kVotes <= 160 * 1024, "LDS budget");
+    __shared__ __attribute__((aligned(1024))) char smem[kLds + kVotes];
     GEMM_POISON_LDS(smem);
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -491,7 +558,7 @@ __global__ __launch_bounds__(C::kThreads) void seg_staged_kernel(const SegParams
                  wn * C::TN, kLdsB);
     } else {
         const uint32_t pid = blockIdx.x;
-        if constexpr (MODE == kSegLoraUp) {
+        if constexpr (LORA) {
             g = 0;
             const TileCoord tc = tile_coord<uint32_t>(pid, (p.rows + C::BM - 1) / C::BM, p.num_n, 4, true);
             row0 = (int)tc.m_block * C::BM;
@@ -509,10 +576,10 @@ __global__ __launch_bounds__(C::kThreads) void seg_staged_kernel(const SegParams
             n0 = (int)tc.n_block * C::BN;
         }
         // the rows behind the last segment: no K-tile, so zeros
-        const bool live = MODE == kSegLoraUp || g < p.groups;
+        const bool live = LORA || g < p.groups;
         kt_count = live ? (p.k + C::BK - 1) / C::BK : 0;
         const _Float16 *a_end = p.a + p.a_rows * p.k;
-        const int32_t *from = MODE == kSegLoraUp ? p.order : p.index;
+        const int32_t *from = LORA ? p.order : p.index;
         opa.init(a_end, p.k, wave, lane, wm * C::TM, 0);
 #pragma unroll
         for (int i = 0; i < OpA::kLoads; ++i) {
@@ -520,12 +587,12 @@ __global__ __launch_bounds__(C::kThreads) void seg_staged_kernel(const SegParams
             int64_t src = row0 + r;
             if (from && r < valid) {
                 const int v = from[row0 + r];
-                src = v < 0 ? -1 : MODE == kSegLoraUp ? v : v / p.fan;
+                src = v < 0 ? -1 : LORA ? v : v / p.fan;
             }
             opa.row[i] = (live && r < valid && src >= 0 && src < p.a_rows) ? p.a + src * p.k : nullptr;
         }
         const int64_t per_group = (int64_t)p.n * p.k;
-        const int64_t count = MODE == kSegLoraUp ? 1 : p.groups;
+        const int64_t count = LORA ? 1 : p.groups;
         const _Float16 *b = p.b + (live ? g : 0) * per_group, *b_end = p.b + count * per_group;
         if constexpr (KIND == kSegNT) {
             opb.init(b_end, p.k, wave, lane, wn * C::TN, kLdsB);
@@ -580,20 +647,14 @@ __global__ __launch_bounds__(C::kThreads) void seg_staged_kernel(const SegParams
 
     constexpr int kWaveBytes = kLds / C::kWaves;
     char *const stg = smem + wave * kWaveBytes;
-    if constexpr (MODE == kSegLoraUp) {
-        lora_tiles<C>(acc, smem, row_scale, p, row0, valid, n0, tid, lane, wm, wn);
+    if constexpr (LORA) {
+        const bool wild = lora_tiles<C, false>(acc, smem, reinterpret_cast<int *>(smem + kLds), p, row0, valid, n0, tid, lane, wm, wn);
         const int32_t *order = p.order;
         const int rows = p.rows;
         seg_store<C, F32, kWaveBytes>(acc, stg, p.c, valid, p.n, n0, wm, wn, lane, [&](int r) {
             return min(max(order[row0 + r], 0), rows - 1);
         });
-    } else if constexpr (MODE == kSegLoraDown) {
-        const float f = g < p.groups && p.scale ? p.scale[g] : 1.0f;
-#pragma unroll
-        for (int j = 0; j < C::FN; ++j)
-#pragma unroll
-            for (int i = 0; i < C::FM; ++i) acc[j][i] *= f;
-        seg_store<C, F32, kWaveBytes>(acc, stg, p.c, valid, p.h_ld, n0, wm, wn, lane, [&](int r) { return row0 + r; });
+        if (wild) lora_wild<C>(p, row0, valid, n0, tid, lane);
     } else if constexpr (KIND == kSegTN) {
         using Out = std::conditional_t<F32, float, _Float16>;
         Out *c = static_cast<Out *>(p.c) + (int64_t)g * p.k * p.n;
@@ -634,6 +695,15 @@ hipError_t launch_seg_nn(int tile, bool f32, const SegParams &p, hipStream_t s);
 hipError_t launch_seg_tn(int tile, bool f32, const SegParams &p, hipStream_t s);
 hipError_t launch_seg_lora(int tile, const SegParams &p, hipStream_t s);
 
-hipError_t launch_seg_staged(int kind, bool f32, int mode, SegParams p, hipStream_t s);
+// Few rows (seg_thin.hip).
+constexpr int64_t kLoraFewRows = 64;  // rows up to here: launch_lora_few
+hipError_t launch_seg_thin(bool f32, const SegParams &p, hipStream_t s);
+// h in adapter order: direct-to-LDS tiles, K in `splits` slices; or any rows
+hipError_t launch_lora_down(SegParams p, int splits, hipStream_t s);
+hipError_t launch_lora_down_thin(const SegParams &p, hipStream_t s);
+// sums: fp32 [rows, n]; down.c is h with rows in their own order
+hipError_t launch_lora_few(const SegParams &p, const SegParams &down, float *sums, const int32_t *ids, hipStream_t s);
+
+hipError_t launch_seg_staged(int kind, bool f32, bool lora, SegParams p, hipStream_t s);
 
 }  // namespace gemm_f16

@@ -88,15 +88,14 @@ static int pick_tile(int kind, const SegParams &p, int cus) {
     double best_t = 1e300;
     for (const Cand &c : cands) {
         if (kind == kSegTN && c.bm < 128) continue;
-        // lora_tiles next to 256 accumulators a lane would spill
-        if (p.order && c.id == kSeg256x256) continue;
         double m_tiles;
         int64_t k_tiles;
         if (kind == kSegTN) {
             m_tiles = (double)(cdiv64(p.k, c.bm) * p.groups);
             k_tiles = cdiv64(cdiv64(p.rows, p.groups), 64);
         } else {
-            m_tiles = (double)p.rows / c.bm + 0.5 * (double)segments;
+            m_tiles = p.order || p.groups == 1 ? (double)cdiv64(p.rows, c.bm)
+                                               : (double)p.rows / c.bm + 0.5 * (double)segments;
             k_tiles = cdiv64(p.k, 64);
         }
         const double tiles = m_tiles * (double)cdiv64(p.n, c.bn), rounds = (double)(int64_t)((tiles + cus - 1) / cus);
@@ -146,6 +145,11 @@ static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k,
     p.n = (int32_t)n;
     p.k = (int32_t)k;
     p.fan = (int32_t)fan;
+#ifdef GEMM_F16_SEG_TUNE
+    if (kind == kSegNT && std::getenv("SEG_TILE") && std::atoi(std::getenv("SEG_TILE")) == kSegTiles)
+        return status(launch_seg_thin(out_f32 != 0, p, (hipStream_t)stream));
+#endif
+    if (kind == kSegNT && k >= 8 && rows <= 16 * std::min(groups, rows)) return status(launch_seg_thin(out_f32 != 0, p, (hipStream_t)stream));
     if (direct_rows(kind, p)) {
         const int tile = pick_tile(kind, p, cus);
         hipError_t e;
@@ -156,17 +160,35 @@ static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k,
         }
         return status(e);
     }
-    return status(launch_seg_staged(kind, out_f32 != 0, kSegPlain, p, (hipStream_t)stream));
+    return status(launch_seg_staged(kind, out_f32 != 0, false, p, (hipStream_t)stream));
 }
 
-// h's row pitch: whole 32-wide steps
-static int64_t lora_h_ld(int64_t rank) { return (rank + 31) / 32 * 32; }
+// The few-row kernel's loads need a whole chunk of K.
+static bool lora_few(int64_t rows, int64_t k) { return rows <= kLoraFewRows && k >= 8; }
+
+// h's row pitch: whole 16-byte stores, and for lora_tiles whole 32-wide steps
+static int64_t lora_h_ld(int64_t rows, int64_t k, int64_t rank) {
+    const int64_t to = lora_few(rows, k) ? 4 : 32;
+    return (rank + to - 1) / to * to;
+}
+
+// Slices of K that h is summed in: 64 x 64 tiles alone fill too few CUs.
+static int lora_parts(int64_t rows, int64_t k) {
+    if (lora_few(rows, k)) return 1;
+#ifdef GEMM_F16_SEG_TUNE
+    if (const char *f = std::getenv("SEG_PARTS")) return std::atoi(f);
+#endif
+    const int64_t tiles = (rows + 63) / 64;
+    int parts = 1;
+    while (parts < 4 && tiles * parts < 256 && k >= parts * 1024) parts *= 2;
+    return parts;
+}
 
 static int check_lora(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64_t rank) {
     if (rows < 0 || n < 0 || k < 0 || rows >= kMaxRows || n >= kMaxRows || k >= kMaxK) return GEMM_F16_EINVAL;
     if (adapters < 1 || adapters > kMaxGroups || rank < 1 || rank > 4096) return GEMM_F16_EINVAL;
     if (!below(kMaxElems, rows, n) || !below(kMaxElems, n, k) || !below(kMaxElems, n + k, rank, adapters) ||
-        !below(kMaxElems, rows, lora_h_ld(rank)))
+        !below(kMaxElems, rows, rank))
         return GEMM_F16_EINVAL;
     return GEMM_F16_OK;
 }
@@ -229,7 +251,9 @@ int gemm_f16_grouped_tn(int64_t rows, int64_t groups, int64_t n, int64_t k, cons
 
 int64_t gemm_f16_lora_workspace(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64_t rank) {
     const int rc = check_lora(rows, n, k, adapters, rank);
-    return rc != GEMM_F16_OK ? rc : rows * lora_h_ld(rank) * 4;
+    if (rc != GEMM_F16_OK) return rc;
+    // h, and x W^T in fp32 for few rows
+    return rows * lora_h_ld(rows, k, rank) * lora_parts(rows, k) * 4 + (lora_few(rows, k) ? rows * n * 4 : 0);
 }
 
 int gemm_f16_lora_nt(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64_t rank, const void *x, const void *w,
@@ -266,7 +290,7 @@ int gemm_f16_lora_nt(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64
     p.fan = 1;
     p.adapters = (int32_t)adapters;
     p.rank = (int32_t)rank;
-    p.h_ld = (int32_t)lora_h_ld(rank);
+    p.h_ld = (int32_t)lora_h_ld(rows, k, rank);
     p.scale = scale;
     // h = scale_s (x D_s^T), rows in adapter order
     SegParams d = p;
@@ -275,18 +299,24 @@ int gemm_f16_lora_nt(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64
     d.index = order;
     d.groups = (int32_t)adapters;
     d.n = (int32_t)rank;
-    rc = status(launch_seg_staged(kSegNT, true, kSegLoraDown, d, (hipStream_t)stream));
-    if (rc != GEMM_F16_OK) return rc;
-    // x W^T + h U_s^T
     p.b = static_cast<const _Float16 *>(w);
     p.c = y;
-    p.order = order;
     p.h = static_cast<const float *>(workspace);
     p.up = static_cast<const _Float16 *>(up);
     p.groups = 1;
     p.n = (int32_t)n;
-    if (direct_rows(kSegNT, p)) return status(launch_seg_lora(pick_tile(kSegNT, p, cus), p, (hipStream_t)stream));
-    return status(launch_seg_staged(kSegNT, false, kSegLoraUp, p, (hipStream_t)stream));
+    if (lora_few(rows, k))
+        return status(launch_lora_few(p, d, static_cast<float *>(workspace) + rows * lora_h_ld(rows, k, rank), ids, (hipStream_t)stream));
+    const bool direct = direct_rows(kSegNT, d) && direct_rows(kSegNT, p);
+    p.h_parts = direct ? lora_parts(rows, k) : 1;
+    rc = status(direct ? launch_lora_down(d, p.h_parts, (hipStream_t)stream)
+                       : launch_lora_down_thin(d, (hipStream_t)stream));
+    if (rc != GEMM_F16_OK) return rc;
+    // x W^T + h U_s^T
+    p.order = order;
+    if (direct && rank % 4 == 0)
+        return status(launch_seg_lora(pick_tile(kSegNT, p, cus), p, (hipStream_t)stream));
+    return status(launch_seg_staged(kSegNT, false, true, p, (hipStream_t)stream));
 }
 
 }  // extern "C"

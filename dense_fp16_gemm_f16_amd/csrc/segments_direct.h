@@ -68,10 +68,12 @@ void seg_tile_kernel(const SegParams p) {
     using OpB = std::conditional_t<KIND == kSegNT, KMajorDirect<C, C::BN, false>, NMajorDirect<C, false>>;
     constexpr int kLdsB = OpA::kLdsBytes, kLds = OpA::kLdsBytes + OpB::kLdsBytes;
     constexpr int LA = OpA::kLoads, L = OpA::kLoads + OpB::kLoads;
-    static_assert(kLds <= 160 * 1024, "LDS budget");
+    // one LDS array: with two, the compiler waits for every load in flight
+    // before each fragment read
+    constexpr int kVotes = LORA ? 64 : 0;
+    static_assert(kLds + kVotes <= 160 * 1024, "LDS budget");
     static_assert(2 * L < 64, "vmcnt range");
-    __shared__ __attribute__((aligned(1024))) char smem[kLds];
-    __shared__ float row_scale[LORA ? C::BM : 1];
+    __shared__ __attribute__((aligned(1024))) char smem[kLds + kVotes];
     GEMM_POISON_LDS(smem);
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -221,25 +223,150 @@ void seg_tile_kernel(const SegParams p) {
     vm_barrier<0>();  // no load is still writing LDS when C is staged there
     acc_fence(acc);
 
+    // opaque copies: what hangs on them is computed here, not held in
+    // registers through the K loop
+    int t = tid, row0 = w.row0, n0 = w.n0, valid = w.valid;
+    asm volatile("" : "+v"(t), "+s"(row0), "+s"(n0), "+s"(valid));
+    const int l = t & (kWave - 1);
     constexpr int kWaveBytes = kLds / C::kWaves;
     char *const stg = smem + wave * kWaveBytes;
     lds_barrier();
-    const int row0 = w.row0;
     if constexpr (LORA) {
-        lora_tiles<C>(acc, smem, row_scale, p, row0, w.valid, w.n0, tid, lane, wm, wn);
+        const bool wild =
+            lora_tiles<C, true>(acc, smem, reinterpret_cast<int *>(smem + kLds), p, row0, valid, n0, t, l, wm, wn);
         const int32_t *order = p.order;
         const int rows = p.rows;
-        seg_store<C, F32, kWaveBytes>(acc, stg, p.c, w.valid, p.n, w.n0, wm, wn, lane, [&](int r) {
-            return min(max(order[row0 + r], 0), rows - 1);
-        });
-    } else if constexpr (KIND == kSegTN) {
+        seg_store<C, F32, kWaveBytes>(acc, stg, p.c, valid, p.n, n0, wm, wn, l,
+                                      [&](int r) { return min(max(order[row0 + r], 0), rows - 1); });
+        if (wild) lora_wild<C>(p, row0, valid, n0, t, l);
+    } else {
         using Out = std::conditional_t<F32, float, _Float16>;
-        Out *c = static_cast<Out *>(p.c) + (int64_t)w.g * p.k * p.n;
-        seg_store<C, F32, kWaveBytes>(acc, stg, c, w.valid, p.n, w.n0, wm, wn, lane, [&](int r) { return row0 + r; });
+        Out *c = static_cast<Out *>(p.c) + (KIND == kSegTN ? (int64_t)w.g * p.k * p.n : 0);
+        seg_store<C, F32, kWaveBytes>(acc, stg, c, valid, p.n, n0, wm, wn, l, [&](int r) { return row0 + r; });
+    }
+#endif
+}
+
+// Small tiles, where the operands' bytes bound the product: one workgroup
+// per tile and K slice, a ring of S LDS stages loaded S - 1 K-tiles ahead,
+// one barrier per K-tile (before it, every wave has read the stage that the
+// next load fills, and has waited for its own loads of the next K-tile).
+// A K-tile of 2 stages in flight leaves a CU waiting for memory most of the
+// time here; the ring keeps S - 1 of them in flight.
+// SPLIT: workgroup x of gridDim.y slices of K writes its fp32 sums to its
+// part of the workspace (h of the adapters, times their scale).
+template <int KIND, class C, int S, bool F32, bool SPLIT>
+__global__ __launch_bounds__(C::kThreads) void seg_ring_kernel(const SegParams p) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
+    constexpr int TM = C::TM, TN = C::TN, FM = C::FM, FN = C::FN;
+    using OpA = KMajorDirect<C, C::BM, false>;
+    using OpB = std::conditional_t<KIND == kSegNT, KMajorDirect<C, C::BN, false>, NMajorDirect<C, false>>;
+    constexpr int kStage = OpA::kStage + OpB::kStage;
+    constexpr int LA = OpA::kLoads, L = OpA::kLoads + OpB::kLoads;
+    constexpr int kLds = S * kStage;
+    static_assert(kLds <= 160 * 1024 && S >= 3 && (S - 1) * L < 64, "LDS budget, vmcnt range");
+    __shared__ __attribute__((aligned(1024))) char smem[kLds];
+    GEMM_POISON_LDS(smem);
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    SegWork<KIND, C, false> w;
+    if (!w.find(p, blockIdx.x, lane)) return;
+    // this slice's K-tiles
+    const int all = (w.k_count + C::BK - 1) / C::BK;
+    const int per = SPLIT ? (all + (int)gridDim.y - 1) / (int)gridDim.y : all;
+    const int kt0 = SPLIT ? min(all, (int)blockIdx.y * per) : 0, kt1 = SPLIT ? min(all, kt0 + per) : all;
+
+    OpA opa;
+    OpB opb;
+    if (p.index) {
+        opa.init(p.a, (int)p.a_rows, p.k, kt1, wave, lane, wm * TM, 0);
+#pragma unroll
+        for (int i = 0; i < OpA::kLoads; ++i) {
+            const int r = (i * C::kWaves + wave) * 8 + (lane >> 3);
+            uint32_t off = kOutOfRange;
+            if (w.live && r < w.valid) {
+                const int v = p.index[w.row0 + r];
+                const int64_t src = v < 0 ? -1 : v / p.fan;
+                if (src >= 0 && src < p.a_rows) off = (uint32_t)((src * p.k + opa.kc) * 2);
+            }
+            opa.voff[i] = off;
+        }
+    } else {
+        opa.init(p.a + (int64_t)w.row0 * p.k, w.valid, p.k, kt1, wave, lane, wm * TM, 0);
+    }
+    const _Float16 *b = p.b + (int64_t)(w.live ? w.g : 0) * p.n * p.k;
+    if constexpr (KIND == kSegNT)
+        opb.init(b + (int64_t)w.n0 * p.k, max(min(C::BN, p.n - w.n0), 0), p.k, kt1, wave, lane, wn * TN, OpA::kStage);
+    else
+        opb.init(b, w.n0, p.n, p.k, kt1, wave, lane, wn * TN, OpA::kStage);
+
+    floatx4 acc[FN][FM];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int i = 0; i < FM; ++i) acc[j][i] = floatx4{};
+    auto load = [&](int t, int stage) {
+        char *to = smem + stage * kStage;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+            if (i < LA)
+                opa.template load<0>(to, t, i);
+            else
+                opb.template load<0>(to, t, i - LA);
+        }
+    };
+    if (kt0 < kt1) {
+#pragma unroll
+        for (int s = 0; s < S - 1; ++s) load(kt0 + s, s);  // past the last: empty loads, for the count
+        int stage = 0;
+        for (int t = kt0; t < kt1; ++t) {
+            vm_barrier<(S - 2) * L>();
+            load(t + S - 1, stage == 0 ? S - 1 : stage - 1);
+            const char *from = smem + stage * kStage;
+#pragma unroll
+            for (int ks = 0; ks < C::KS; ++ks) {
+                half8 af[FM], bf[FN];
+#pragma unroll
+                for (int i = 0; i < FM; ++i) af[i] = opa.read(from, 0, ks, i);
+#pragma unroll
+                for (int j = 0; j < FN; ++j) bf[j] = opb.read(from, 0, ks, j);
+#pragma unroll
+                for (int j = 0; j < FN; ++j)
+#pragma unroll
+                    for (int i = 0; i < FM; ++i) acc[j][i] = Mfma<16>::run(bf[j], af[i], acc[j][i]);
+            }
+            stage = stage == S - 1 ? 0 : stage + 1;
+        }
+    }
+    vm_barrier<0>();  // no load is still writing LDS when C is staged there
+
+    constexpr int kWaveBytes = kLds / C::kWaves / 1024 * 1024;
+    char *const stg = smem + wave * kWaveBytes;
+    const int row0 = w.row0;
+    if constexpr (SPLIT) {
+        const float f = w.live && p.scale ? p.scale[w.g] : 1.0f;
+#pragma unroll
+        for (int j = 0; j < FN; ++j)
+#pragma unroll
+            for (int i = 0; i < FM; ++i) acc[j][i] *= f;
+        float *c = static_cast<float *>(p.c) + (int64_t)blockIdx.y * p.rows * p.h_ld;
+        seg_store<C, true, kWaveBytes>(acc, stg, c, w.valid, p.h_ld, w.n0, wm, wn, lane, [&](int r) { return row0 + r; });
     } else {
         seg_store<C, F32, kWaveBytes>(acc, stg, p.c, w.valid, p.n, w.n0, wm, wn, lane, [&](int r) { return row0 + r; });
     }
 #endif
+}
+
+template <int KIND, class C, int S>
+hipError_t launch_seg_ring(SegParams p, bool f32, hipStream_t s) {
+    p.num_n = (p.n + C::BN - 1) / C::BN;
+    p.num_m = (int32_t)seg_row_tiles(p.rows, p.groups, C::BM);
+    const int64_t grid = (int64_t)p.num_m * p.num_n;
+    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    return f32 ? launch_seg(seg_ring_kernel<KIND, C, S, true, false>, grid, C::kThreads, s, p)
+               : launch_seg(seg_ring_kernel<KIND, C, S, false, false>, grid, C::kThreads, s, p);
 }
 
 // Launch of tile C: the grid holds every tile that any sizes could need.

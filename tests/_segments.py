@@ -64,8 +64,9 @@ def lora(x, w, down, up, ids, scale):
         mag = torch.mm(x[rows].abs(), down[s].abs().T.contiguous()) * abs(f)
         y[rows] += torch.mm(low, up[s].T.contiguous())
         err[rows] += torch.mm(mag, up[s].abs().T.contiguous())
-    # h: k terms, its scale and its two fp16 parts (2^-22 together); then k + 2 rank terms
-    return y, err * ((2 * k + 2 * rank + 4) * 2.0**-23 + 2.0**-22)
+    # h: k terms and its scale; its two bf16 parts without the least product (2^-17); then
+    # k + 3 rank terms
+    return y, err * ((2 * k + 3 * rank + 4) * 2.0**-23 + 2.0**-17)
 
 
 def worst(got, ref, err, dtype):
