@@ -2,11 +2,11 @@
 // adapters' inner product there.  The time is B's bytes, so what matters is
 // how many of them are in flight.
 //
-// A workgroup owns a segment and 16 columns.  Its waves split K, each taking
-// 32 KST contiguous elements at a time; a wave's part of B goes straight from
-// memory to registers in the MFMA's layout (lane l: row l % 16, 8 elements at
-// 8 (l / 16)), all of it in flight at once, and stays there for all of the
-// segment's rows, 16 at a time, if one pass covers K.  No LDS and no barrier
+// A workgroup owns a segment and 16 columns.  Its waves share K evenly, in
+// 32-wide steps, each taking up to kThinSteps at a time; a wave's part of B
+// goes straight from memory to registers in the MFMA's layout (lane l: row
+// l % 16, 8 elements at 8 (l / 16)), all of it in flight at once, and stays
+// there for all of the segment's rows, 16 at a time, if that is all.  No LDS and no barrier
 // until the waves' sums meet, in wave order.  Any K, N and alignment: global
 // loads take 2-byte aligned addresses, and the part past K is masked.
 #include <algorithm>
@@ -15,7 +15,7 @@
 
 namespace gemm_f16 {
 
-constexpr int kThinSteps = 8, kThinPass = 32 * kThinSteps;  // a wave's elements of K in one pass
+constexpr int kThinSteps = 8;  // 32-wide steps of K that a wave takes at a time
 
 struct ThinParams {
     SegParams main;       // rows against main.b
@@ -24,26 +24,25 @@ struct ThinParams {
     int32_t down_blocks;  // kThinLora: workgroups of the inner product
 };
 
-// A wave's steps of a row (K >= 8) from kb on, 8 elements at kl of each 32.
-// Chunks past K become zeros, a chunk across K is loaded from the row's last
-// 8 elements and shifted, so every load stays inside the row.
-__device__ __forceinline__ void thin_load(half8 (&v)[kThinSteps], const _Float16 *row, int kb, int kl, int k_elems) {
-    if (kb + kThinPass <= k_elems) {
+// `count` steps of a row (K >= 8), 32 elements each, from the one that ends
+// a wave's part downwards; 8 elements at kl of each.  The first one, where
+// `partial`, reaches past K: its chunks past K become zeros, and the chunk
+// across K is loaded from the row's last 8 elements and shifted, so every
+// load stays inside the row.
+__device__ __forceinline__ void thin_load(half8 (&v)[kThinSteps], const _Float16 *row, int top, int count, bool partial,
+                                          int kl, int k_elems) {
+    const int k0 = 32 * (top - 1) + kl;
 #pragma unroll
-        for (int s = 0; s < kThinSteps; ++s)
-            v[s] = __builtin_bit_cast(half8, (int4v)*reinterpret_cast<const int4u *>(row + kb + 32 * s + kl));
-    } else {
-        int4v t[kThinSteps];
-#pragma unroll
-        for (int s = 0; s < kThinSteps; ++s)
-            t[s] = *reinterpret_cast<const int4u *>(row + min(kb + 32 * s + kl, k_elems - 8));
-#pragma unroll
-        for (int s = 0; s < kThinSteps; ++s) {
-            const int past = 8 - (k_elems - (kb + 32 * s + kl));  // elements to shift out
-            unsigned __int128 w = __builtin_bit_cast(unsigned __int128, t[s]);
-            if (past > 0) w = past < 8 ? w >> (16 * past) : 0;
-            v[s] = __builtin_bit_cast(half8, w);
-        }
+    for (int s = 0; s < kThinSteps; ++s) {
+        if (s >= count) continue;
+        const int k = s == 0 ? min(k0, k_elems - 8) : k0 - 32 * s;
+        v[s] = __builtin_bit_cast(half8, (int4v)*reinterpret_cast<const int4u *>(row + k));
+    }
+    if (partial) {
+        const int past = 8 - (k_elems - k0);  // elements to shift out
+        unsigned __int128 w = __builtin_bit_cast(unsigned __int128, v[0]);
+        if (past > 0) w = past < 8 ? w >> (16 * past) : 0;
+        v[0] = __builtin_bit_cast(half8, w);
     }
 }
 
@@ -85,8 +84,10 @@ __global__ __launch_bounds__(1024) void seg_thin_kernel(const ThinParams tp) {
     // their results are never stored.
     const int kl = 8 * (lane / 16);
     const _Float16 *br = p.b + ((int64_t)g * p.n + min(n0 + lane % 16, p.n - 1)) * p.k;
-    const int first = wave * kThinPass, stride = waves * kThinPass;
-    const bool one_pass = stride >= p.k;
+    // this wave's steps, [part0, part1)
+    const int steps = (p.k + 31) / 32;
+    const int part0 = (int)((int64_t)steps * wave / waves), part1 = (int)((int64_t)steps * (wave + 1) / waves);
+    const bool one_pass = part1 - part0 <= kThinSteps;
     const float f = is_down && p.scale ? p.scale[g] : 1.0f;
     half8 bf[kThinSteps], af[kThinSteps];
     int parity = 0;
@@ -94,9 +95,11 @@ __global__ __launch_bounds__(1024) void seg_thin_kernel(const ThinParams tp) {
         floatx4 acc = {};
         bool found = true;  // an index outside A: a row of zeros
         const _Float16 *ar = nullptr;
-        for (int kb = first; kb < p.k; kb += stride) {
-            if (!one_pass || r0 == lo) thin_load(bf, br, kb, kl, p.k);
-            if (kb == first) {  // behind B's loads
+        for (int top = part1; top > part0; top -= kThinSteps) {
+            const int count = min(top - part0, kThinSteps);
+            const bool partial = 32 * top > p.k;
+            if (!one_pass || r0 == lo) thin_load(bf, br, top, count, partial, kl, p.k);
+            if (top == part1) {  // behind B's loads
                 const int r = min(r0 + lane % 16, hi - 1);
                 int64_t src = r;
                 if (p.index) {
@@ -106,9 +109,10 @@ __global__ __launch_bounds__(1024) void seg_thin_kernel(const ThinParams tp) {
                 found = src >= 0 && src < p.a_rows;
                 ar = p.a + (found ? src : 0) * p.k;
             }
-            thin_load(af, ar, kb, kl, p.k);
+            thin_load(af, ar, top, count, partial, kl, p.k);
 #pragma unroll
-            for (int s = 0; s < kThinSteps; ++s) acc = Mfma<16>::run(bf[s], af[s], acc);
+            for (int s = 0; s < kThinSteps; ++s)
+                if (s < count) acc = Mfma<16>::run(bf[s], af[s], acc);
         }
         red[parity][wave][lane] = acc;
         lds_barrier();
@@ -184,7 +188,7 @@ static hipError_t launch_thin(Kernel kernel, int64_t grid, int threads, hipStrea
 // waves that K keeps busy in one pass
 static int thin_threads(int k) {
     int w = 1;
-    while (w < 16 && w * kThinPass < k) w *= 2;
+    while (w < 16 && w * kThinSteps * 32 < k) w *= 2;
     return w * kWave;
 }
 

@@ -3,7 +3,9 @@
 #include "segments.h"
 
 #include <algorithm>
+#include <cmath>
 #include <cstdlib>
+#include <iterator>
 
 #include "device.h"
 #include "gemm_f16.h"
@@ -60,52 +62,133 @@ static int status(hipError_t e) { return e == hipSuccess ? GEMM_F16_OK : e == hi
 // a gathered A below 2 GiB (one descriptor spans it).
 static bool direct_rows(int kind, const SegParams &p) {
     if ((((uintptr_t)p.a | (uintptr_t)p.b) % 16) != 0 || p.k % 8 != 0 || p.k == 0) return false;
-    if (kind != kSegNT && p.n % 8 != 0) return false;
+    // (64 rows of B below 2^31 bytes)
+    if (kind != kSegNT && (p.n % 8 != 0 || p.n >= (1 << 24))) return false;
     return !(p.index || p.order) || p.a_rows * p.k * 2 < (int64_t(1) << 31);
 }
 
 static int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Block tile with the smallest modelled time c + a rounds k_tiles + b
-// tiles / cus (us; the dense product's model, auto_tile in gemm_f16.hip),
-// over the row tiles to expect: half a tile more per segment than the rows
-// fill.
-static int pick_tile(int kind, const SegParams &p, int cus) {
+// Whether the walking kernel can run the product on a bm x bn tile: more
+// tiles than CUs but no more than fit its lists, and C's rows in whole
+// 16-byte stores.
+static bool can_walk(int kind, int bm, int bn, bool f32, const SegParams &p, int cus) {
+    const int es = f32 ? 4 : 2;
+    if (kind == kSegTN || p.order || p.n % (16 / es) != 0 || (uintptr_t)p.c % 16 != 0 ||
+        (int64_t)bm * p.n * es >= (int64_t(1) << 31))
+        return false;
+    const int64_t tiles = seg_row_tiles(p.rows, p.groups, bm) * cdiv64(p.n, bn);
+    return tiles > cus && tiles <= (int64_t)cus * kWalkTiles;
+}
+
+// Kernel of a product: a block tile (SegTileId), and whether its tiles are
+// walked.
+struct SegPlan {
+    int tile;
+    bool walk;
+};
+
+// The plan with the smallest modelled time (us)
+//     c + a rounds k_tiles + b tiles / cus,
+// rounds of one workgroup per CU, over the row tiles to expect (half a tile
+// more per segment than the rows fill; the sizes are on the GPU).  For the
+// walking kernels a last round in small tiles counts as 0.42 (256 x 256) or
+// 0.66 of a round.  The coefficients are least-squares fits, in relative
+// error, to sweeps of every tile over 500 shapes (rows 1 to 16384, 1 to 64
+// segments, N and K from 64 to 4096, inputs cold in the caches) on MI355X.
+// On those shapes the plan's time was 1.03 (nt, nn) to 1.04 (tn) of the
+// fastest tile's in the geometric mean and at most 1.5 of it.  With tiles to
+// walk, walking measured 0.88 to 0.97 of the one-tile kernel's time on most
+// shapes (nt, 256 x 128, 1 to 2 rounds: 0.91) and up to 1.15 on few.  The
+// 32-row ring serves few rows per segment, where B's bytes bound the
+// product.
+static SegPlan pick_plan(int kind, bool f32, const SegParams &p, int cus) {
     struct Cand {
         int id, bm, bn;
-        double c, a, b;
+        double c, a, b;     // one tile per workgroup
+        double wc, wa, wb;  // walked
     };
-    static const Cand cands[] = {
-        {kSeg256x256, 256, 256, 8.280, 1.115, 6.212}, {kSeg256x128, 256, 128, 5.825, 0.663, 3.036},
-        {kSeg128x256, 128, 256, 5.856, 0.661, 2.886}, {kSeg128x128, 128, 128, 4.492, 0.436, 1.517},
-        {kSeg64x128, 64, 128, 3.545, 0.391, 0.780},   {kSeg32x128, 32, 128, 3.3, 0.30, 0.45},
+    static const Cand nt[] = {
+        {kSeg256x256, 256, 256, 6.85, 1.054, 14.80, 2.0, 1.330, 10.0},
+        {kSeg256x128, 256, 128, 4.42, 0.675, 9.38, 6.4, 0.888, 5.2},
+        {kSeg128x256, 128, 256, 4.46, 0.685, 9.56, 6.5, 0.909, 5.2},
+        {kSeg128x128, 128, 128, 3.42, 0.461, 5.81, 0, 0, 0},
+        {kSeg64x128, 64, 128, 2.84, 0.375, 3.87, 0, 0, 0},
+        {kSeg32x128, 32, 128, 2.67, 0.315, 2.72, 0, 0, 0},
+        {kSegRing, 32, 64, 3.57, 0.180, 0.55, 0, 0, 0},
     };
-#ifdef GEMM_F16_SEG_TUNE
-    if (const char *force = std::getenv("SEG_TILE")) return std::atoi(force);
-#endif
+    static const Cand nn[] = {
+        {kSeg256x256, 256, 256, 6.97, 1.070, 11.80, 2.0, 1.360, 10.0},
+        {kSeg256x128, 256, 128, 4.36, 0.687, 7.40, 2.2, 0.887, 7.1},
+        {kSeg128x256, 128, 256, 5.00, 0.632, 8.36, 1.0, 0.813, 9.5},
+        {kSeg128x128, 128, 128, 3.50, 0.468, 5.00, 0, 0, 0},
+        {kSeg64x128, 64, 128, 3.03, 0.405, 3.13, 0, 0, 0},
+        {kSeg32x128, 32, 128, 2.73, 0.343, 2.27, 0, 0, 0},
+        {kSegRing, 32, 128, 3.59, 0.284, 1.14, 0, 0, 0},
+    };
+    static const Cand tn[] = {
+        {kSeg256x256, 256, 256, 10.0, 1.390, 8.20, 0, 0, 0},
+        {kSeg256x128, 256, 128, 6.40, 0.800, 5.75, 0, 0, 0},
+        {kSeg128x256, 128, 256, 6.66, 0.770, 5.87, 0, 0, 0},
+        {kSeg128x128, 128, 128, 4.76, 0.520, 3.95, 0, 0, 0},
+    };
+    const Cand *first = kind == kSegNT ? nt : kind == kSegNN ? nn : tn;
+    const Cand *last = kind == kSegNT ? std::end(nt) : kind == kSegNN ? std::end(nn) : std::end(tn);
     const int64_t segments = std::min<int64_t>(p.groups, p.rows);
-    int best = kSeg128x128;
+    SegPlan best = {kSeg128x128, false};
     double best_t = 1e300;
-    for (const Cand &c : cands) {
-        if (kind == kSegTN && c.bm < 128) continue;
-        double m_tiles;
-        int64_t k_tiles;
+    for (const Cand *c = first; c != last; ++c) {
+        if (p.order && c->id == kSegRing) continue;  // no adapters there
+        double m_tiles, k_tiles;
         if (kind == kSegTN) {
-            m_tiles = (double)(cdiv64(p.k, c.bm) * p.groups);
-            k_tiles = cdiv64(cdiv64(p.rows, p.groups), 64);
+            m_tiles = (double)(cdiv64(p.k, c->bm) * p.groups);
+            k_tiles = (double)std::max<int64_t>(1, cdiv64(cdiv64(p.rows, p.groups), 64));
         } else {
-            m_tiles = p.order || p.groups == 1 ? (double)cdiv64(p.rows, c.bm)
-                                               : (double)p.rows / c.bm + 0.5 * (double)segments;
-            k_tiles = cdiv64(p.k, 64);
+            m_tiles = p.order || segments == 1 ? (double)cdiv64(p.rows, c->bm)
+                                               : (double)p.rows / c->bm + 0.5 * (double)segments;
+            k_tiles = (double)cdiv64(p.k, 64);
         }
-        const double tiles = m_tiles * (double)cdiv64(p.n, c.bn), rounds = (double)(int64_t)((tiles + cus - 1) / cus);
-        const double t = c.c + c.a * rounds * (double)k_tiles + c.b * tiles / cus;
+        const double share = m_tiles * (double)cdiv64(p.n, c->bn) / cus;
+        const bool walk = can_walk(kind, c->bm, c->bn, f32, p, cus) && c->wa > 0 && share > 1;
+        double t;
+        if (walk) {
+            const double whole = std::floor(share), rest = share - whole;
+            const bool large = c->id == kSeg256x256;
+            const double small_rounds = std::ceil(rest * (large ? 4 : 2));
+            const double tail = small_rounds <= (large ? 2 : 1) ? small_rounds * (large ? 0.42 : 0.66) : 1;
+            t = c->wc + c->wa * (whole + tail) * k_tiles + c->wb * share;
+        } else {
+            t = c->c + c->a * std::ceil(share) * k_tiles + c->b * share;
+        }
         if (t < best_t) {
             best_t = t;
-            best = c.id;
+            best = {c->id, walk};
         }
     }
+#ifdef GEMM_F16_SEG_TUNE
+    if (const char *f = std::getenv("SEG_TILE")) {
+        best.tile = std::atoi(f);
+        static const int bms[] = {256, 256, 128}, bns[] = {256, 128, 256};
+        const char *w = std::getenv("SEG_WALK");
+        best.walk = best.tile < 3 && can_walk(kind, bms[best.tile], bns[best.tile], f32, p, cus) && !(w && !std::atoi(w));
+    }
+#endif
     return best;
+}
+
+// Whether a grouped NT product takes the few-row kernel: up to 16 rows per
+// segment, and too few 32 x 64 tiles to fill the CUs, where its waves'
+// share of K is what keeps loads in flight (1 row, 904 x 3280: 6.3 us
+// against the ring's 12.6; 10 rows over 10 segments of 608 x 2032: 8.4
+// against 10.8).  With more tiles the ring is level or faster (45 rows, 4
+// segments of 3056 x 2520: 13.1 against 19.5), except for a handful of rows
+// where every wave has whole passes of 256 elements and two workgroups share
+// a CU (16 rows over 8 segments of 4096 x 2048: 31 against 35.5).
+static bool few_rows(const SegParams &p) {
+    const int64_t segments = std::min<int64_t>(p.groups, p.rows);
+    if (p.k < 8 || p.rows > 16 * segments) return false;
+    return segments * cdiv64(p.n, 64) <= 176 ||
+           (p.rows <= 4 * segments && p.k % 256 == 0 && p.k >= 1024 && p.k <= 2048);
 }
 
 static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a, int64_t a_rows,
@@ -146,13 +229,30 @@ static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k,
     p.k = (int32_t)k;
     p.fan = (int32_t)fan;
 #ifdef GEMM_F16_SEG_TUNE
-    if (kind == kSegNT && std::getenv("SEG_TILE") && std::atoi(std::getenv("SEG_TILE")) == kSegTiles)
-        return status(launch_seg_thin(out_f32 != 0, p, (hipStream_t)stream));
+    const char *force = std::getenv("SEG_TILE");
+    const bool thin = kind == kSegNT && (force ? std::atoi(force) == kSegTiles : few_rows(p));
+#else
+    const bool thin = kind == kSegNT && few_rows(p);
 #endif
-    if (kind == kSegNT && k >= 8 && rows <= 16 * std::min(groups, rows)) return status(launch_seg_thin(out_f32 != 0, p, (hipStream_t)stream));
+    if (thin || (kind == kSegNT && k >= 8 && rows <= 16 * std::min(groups, rows) && !direct_rows(kind, p)))
+        return status(launch_seg_thin(out_f32 != 0, p, (hipStream_t)stream));
     if (direct_rows(kind, p)) {
-        const int tile = pick_tile(kind, p, cus);
+        const SegPlan plan = pick_plan(kind, out_f32 != 0, p, cus);
+        const int tile = plan.tile;
         hipError_t e;
+        if (plan.walk) {
+            // cache policy of the stores: see c_store_policy in gemm_f16.hip
+            const int64_t bytes = (a_rows * k + (kind == kSegTN ? rows * n : groups * n * k)) * 2 + out * es;
+            bool dev = bytes <= (int64_t(256) << 20) || (n * es) % 128 != 0 || (uintptr_t)c % 128 != 0;
+#ifdef GEMM_F16_SEG_TUNE
+            if (const char *f = std::getenv("SEG_DEV")) dev = std::atoi(f);
+#endif
+            switch (kind) {
+                case kSegNT: e = launch_seg_walk_nt(tile, out_f32 != 0, dev, cus, p, (hipStream_t)stream); break;
+                default: e = launch_seg_walk_nn(tile, out_f32 != 0, dev, cus, p, (hipStream_t)stream); break;
+            }
+            return status(e);
+        }
         switch (kind) {
             case kSegNT: e = launch_seg_nt(tile, out_f32 != 0, p, (hipStream_t)stream); break;
             case kSegNN: e = launch_seg_nn(tile, out_f32 != 0, p, (hipStream_t)stream); break;
@@ -315,7 +415,7 @@ int gemm_f16_lora_nt(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64
     // x W^T + h U_s^T
     p.order = order;
     if (direct && rank % 4 == 0)
-        return status(launch_seg_lora(pick_tile(kSegNT, p, cus), p, (hipStream_t)stream));
+        return status(launch_seg_lora(pick_plan(kSegNT, false, p, cus).tile, p, (hipStream_t)stream));
     return status(launch_seg_staged(kSegNT, false, true, p, (hipStream_t)stream));
 }
 

@@ -12,6 +12,29 @@ struct RowsAsCols : C {
     static constexpr int BN = C::BM, FN = C::FM;
 };
 
+// Bytes of K-tile t of an operand with `cols` columns a row, from column n0
+// of its first row to the last row inside the contraction (k_count rows);
+// 0 past it.  No branch: this sits between the MFMAs.
+template <class C>
+__device__ __forceinline__ uint32_t nmajor_bytes(int k_count, int t, int cols, int n0) {
+    const int rows = max(min(k_count - t * C::BK, C::BK), 0);  // rows * cols < 2^30
+    return (uint32_t)max(rows * cols - n0, 0) * 2u;
+}
+
+// The segment of the given rank by falling size (equal sizes in order); more
+// than 64 segments stay in order.
+__device__ __forceinline__ int seg_by_size(const SegParams &p, int rank, int lane) {
+    if (p.groups > kWave) return rank;
+    int size = -1, mine = 0;
+    if (lane < p.groups) size = max(seg_bound(p.offsets, lane + 1, p.rows) - seg_bound(p.offsets, lane, p.rows), 0);
+    for (int g = 0; g < p.groups; ++g) {
+        const int other = __builtin_amdgcn_readlane(size, g);
+        mine += other > size || (other == size && g < lane);
+    }
+    const uint64_t hit = __ballot(lane < p.groups && mine == rank);
+    return __builtin_ctzll(hit);
+}
+
 // A tile's place in the product and its operands' first rows.
 template <int KIND, class C, bool LORA>
 struct SegWork {
@@ -23,8 +46,9 @@ struct SegWork {
         live = true;
         if constexpr (KIND == kSegTN) {
             const uint32_t per = (uint32_t)p.num_m * (uint32_t)p.num_n;
-            g = (int)(pid / per);
-            const TileCoord tc = tile_coord<uint32_t>(pid % per, p.num_m, p.num_n, 4, false);
+            // long segments first, so that the last tiles to start are short
+            g = seg_by_size(p, (int)(pid / per), lane);
+            const TileCoord tc = tile_coord<uint32_t>(pid % per, p.num_m, p.num_n, 4, true);
             row0 = (int)tc.m_block * C::BM;
             n0 = (int)tc.n_block * C::BN;
             valid = min(C::BM, p.k - row0);
@@ -54,42 +78,41 @@ struct SegWork {
     }
 };
 
-// One workgroup per tile.  The K loop is gemm_f16_direct_ahead_kernel's:
-// two LDS stages, both k steps' fragments of K-tile t+1 read during K-tile
-// t, a release and an acquire barrier per K-tile.
+// LDS of seg_tile's operands, and behind it the votes of lora_tiles.
+template <int KIND, class C>
+constexpr int seg_tile_lds() {
+    return 2 * C::BK * 2 * (C::BM + C::BN);
+}
+
+// One tile.  The K loop is gemm_f16_direct_ahead_kernel's: two LDS stages,
+// both k steps' fragments of K-tile t+1 read during K-tile t, a release and
+// an acquire barrier per K-tile.  smem: the kernel's one LDS array (with
+// two, the compiler waits for every load in flight before each fragment
+// read).
 template <int KIND, class C, bool F32, bool LORA>
-__global__ __launch_bounds__(C::kThreads)
-__attribute__((amdgpu_waves_per_eu(C::kMinWavesPerEU, C::kMinWavesPerEU)))
-void seg_tile_kernel(const SegParams p) {
-#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
+__device__ __forceinline__ void seg_tile(const SegParams &p, char *smem, const SegWork<KIND, C, LORA> &w, int tid) {
     constexpr int TM = C::TM, TN = C::TN, FM = C::FM, FN = C::FN;
     static_assert(C::MB == 16 && C::KS == 2, "two 32-wide k steps per K-tile");
-    using OpA = std::conditional_t<KIND == kSegTN, NMajorDirect<RowsAsCols<C>, false>, KMajorDirect<C, C::BM, false>>;
-    using OpB = std::conditional_t<KIND == kSegNT, KMajorDirect<C, C::BN, false>, NMajorDirect<C, false>>;
+    using OpA = std::conditional_t<KIND == kSegTN, NMajorDirect<RowsAsCols<C>, true>, KMajorDirect<C, C::BM, false>>;
+    using OpB = std::conditional_t<KIND == kSegNT, KMajorDirect<C, C::BN, false>, NMajorDirect<C, true>>;
     constexpr int kLdsB = OpA::kLdsBytes, kLds = OpA::kLdsBytes + OpB::kLdsBytes;
     constexpr int LA = OpA::kLoads, L = OpA::kLoads + OpB::kLoads;
-    // one LDS array: with two, the compiler waits for every load in flight
-    // before each fragment read
-    constexpr int kVotes = LORA ? 64 : 0;
-    static_assert(kLds + kVotes <= 160 * 1024, "LDS budget");
+    static_assert(kLds == seg_tile_lds<KIND, C>(), "LDS of the operands");
     static_assert(2 * L < 64, "vmcnt range");
-    __shared__ __attribute__((aligned(1024))) char smem[kLds + kVotes];
-    GEMM_POISON_LDS(smem);
-
-    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int lane = tid & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int wm = wave / C::WN, wn = wave % C::WN;
-
-    SegWork<KIND, C, LORA> w;
-    if (!w.find(p, blockIdx.x, lane)) return;
     const int kt_count = (w.k_count + C::BK - 1) / C::BK;
 
     OpA opa;
     OpB opb;
+    const _Float16 *a_tile = p.a, *b_tile = p.b;  // operands read along N: the tile's first element
     if constexpr (KIND == kSegTN) {
         const int64_t lo = seg_bound(p.offsets, w.g, p.rows);
-        opa.init(p.a + lo * p.k, w.row0, p.k, w.k_count, kt_count, wave, lane, wm * TM, 0);
-        opb.init(p.b + lo * p.n, w.n0, p.n, w.k_count, kt_count, wave, lane, wn * TN, kLdsB);
+        a_tile = p.a + lo * p.k + w.row0;
+        b_tile = p.b + lo * p.n + w.n0;
+        opa.init(p.a, 0, p.k, w.k_count, kt_count, wave, lane, wm * TM, 0);
+        opb.init(p.b, 0, p.n, w.k_count, kt_count, wave, lane, wn * TN, kLdsB);
     } else {
         const int32_t *from = LORA ? p.order : p.index;
         if (from) {
@@ -114,7 +137,8 @@ void seg_tile_kernel(const SegParams p) {
         if constexpr (KIND == kSegNT)
             opb.init(b + (int64_t)w.n0 * p.k, min(C::BN, p.n - w.n0), p.k, kt_count, wave, lane, wn * TN, kLdsB);
         else
-            opb.init(b, w.n0, p.n, p.k, kt_count, wave, lane, wn * TN, kLdsB);
+            opb.init(p.b, 0, p.n, p.k, kt_count, wave, lane, wn * TN, kLdsB);
+        b_tile = b + w.n0;
     }
 
     floatx4 acc[FN][FM];
@@ -138,10 +162,17 @@ void seg_tile_kernel(const SegParams p) {
     };
     auto load = [&](auto s_c, int t, int i) {
         constexpr int S = decltype(s_c)::value;
-        if (i < LA)
-            opa.template load<S>(smem, t, i);
-        else
-            opb.template load<S>(smem, t, i - LA);
+        if (i < LA) {
+            if constexpr (KIND == kSegTN)
+                opa.template load_tile<S>(smem, a_tile, w.row0, nmajor_bytes<C>(w.k_count, t, p.k, w.row0), t, i);
+            else
+                opa.template load<S>(smem, t, i);
+        } else {
+            if constexpr (KIND == kSegNT)
+                opb.template load<S>(smem, t, i - LA);
+            else
+                opb.template load_tile<S>(smem, b_tile, w.n0, nmajor_bytes<C>(w.k_count, t, p.n, w.n0), t, i - LA);
+        }
     };
     using S0 = std::integral_constant<int, 0>;
     using S1 = std::integral_constant<int, 1>;
@@ -244,6 +275,21 @@ void seg_tile_kernel(const SegParams p) {
         Out *c = static_cast<Out *>(p.c) + (KIND == kSegTN ? (int64_t)w.g * p.k * p.n : 0);
         seg_store<C, F32, kWaveBytes>(acc, stg, c, valid, p.n, n0, wm, wn, l, [&](int r) { return row0 + r; });
     }
+}
+
+// One workgroup per tile.
+template <int KIND, class C, bool F32, bool LORA>
+__global__ __launch_bounds__(C::kThreads)
+__attribute__((amdgpu_waves_per_eu(C::kMinWavesPerEU, C::kMinWavesPerEU)))
+void seg_tile_kernel(const SegParams p) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
+    constexpr int kLds = seg_tile_lds<KIND, C>() + (LORA ? 64 : 0);
+    static_assert(kLds <= 160 * 1024, "LDS budget");
+    __shared__ __attribute__((aligned(1024))) char smem[kLds];
+    GEMM_POISON_LDS(smem);
+    SegWork<KIND, C, LORA> w;
+    if (!w.find(p, blockIdx.x, (int)threadIdx.x & (kWave - 1))) return;
+    seg_tile<KIND, C, F32, LORA>(p, smem, w, (int)threadIdx.x);
 #endif
 }
 
@@ -260,7 +306,7 @@ __global__ __launch_bounds__(C::kThreads) void seg_ring_kernel(const SegParams p
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
     constexpr int TM = C::TM, TN = C::TN, FM = C::FM, FN = C::FN;
     using OpA = KMajorDirect<C, C::BM, false>;
-    using OpB = std::conditional_t<KIND == kSegNT, KMajorDirect<C, C::BN, false>, NMajorDirect<C, false>>;
+    using OpB = std::conditional_t<KIND == kSegNT, KMajorDirect<C, C::BN, false>, NMajorDirect<C, true>>;
     constexpr int kStage = OpA::kStage + OpB::kStage;
     constexpr int LA = OpA::kLoads, L = OpA::kLoads + OpB::kLoads;
     constexpr int kLds = S * kStage;
@@ -300,7 +346,7 @@ __global__ __launch_bounds__(C::kThreads) void seg_ring_kernel(const SegParams p
     if constexpr (KIND == kSegNT)
         opb.init(b + (int64_t)w.n0 * p.k, max(min(C::BN, p.n - w.n0), 0), p.k, kt1, wave, lane, wn * TN, OpA::kStage);
     else
-        opb.init(b, w.n0, p.n, p.k, kt1, wave, lane, wn * TN, OpA::kStage);
+        opb.init(p.b, 0, p.n, p.k, kt1, wave, lane, wn * TN, OpA::kStage);
 
     floatx4 acc[FN][FM];
 #pragma unroll
@@ -313,8 +359,10 @@ __global__ __launch_bounds__(C::kThreads) void seg_ring_kernel(const SegParams p
         for (int i = 0; i < L; ++i) {
             if (i < LA)
                 opa.template load<0>(to, t, i);
-            else
+            else if constexpr (KIND == kSegNT)
                 opb.template load<0>(to, t, i - LA);
+            else
+                opb.template load_tile<0>(to, b + w.n0, w.n0, nmajor_bytes<C>(w.k_count, t, p.n, w.n0), t, i - LA);
         }
     };
     if (kt0 < kt1) {
