@@ -61,7 +61,6 @@ EXPORTS = (
     "gemm_f16_grouped_nt",
     "gemm_f16_grouped_nn",
     "gemm_f16_grouped_tn",
-    "gemm_f16_grouped_workspace",
     "gemm_f16_lora_nt",
     "gemm_f16_lora_workspace",
 )
@@ -113,13 +112,11 @@ def lib() -> ctypes.CDLL:
     L.gemm_f16_group_rows.restype = ctypes.c_int
     L.gemm_f16_group_rows_workspace.argtypes = [i64, i64]
     L.gemm_f16_group_rows_workspace.restype = i64
-    L.gemm_f16_grouped_nt.argtypes = [i64, i64, i64, i64, p, i64, p, p, p, i64, p, i32, p, i64, p]
+    L.gemm_f16_grouped_nt.argtypes = [i64, i64, i64, i64, p, i64, p, p, p, i64, p, i32, p]
     L.gemm_f16_grouped_nt.restype = ctypes.c_int
     for f in (L.gemm_f16_grouped_nn, L.gemm_f16_grouped_tn):
-        f.argtypes = [i64, i64, i64, i64, p, p, p, p, i32, p, i64, p]
+        f.argtypes = [i64, i64, i64, i64, p, p, p, p, i32, p]
         f.restype = ctypes.c_int
-    L.gemm_f16_grouped_workspace.argtypes = [i32, i64, i64, i64, i64]
-    L.gemm_f16_grouped_workspace.restype = i64
     L.gemm_f16_lora_nt.argtypes = [i64, i64, i64, i64, i64, p, p, p, p, p, p, p, p, p, p, i64, p]
     L.gemm_f16_lora_nt.restype = ctypes.c_int
     L.gemm_f16_lora_workspace.argtypes = [i64, i64, i64, i64, i64]
@@ -236,5 +233,4 @@ def select_xcd(num_m: int, num_n: int, swizzle: int = 4, cus: int = 256) -> int:
 
 
 from .segments import (  # noqa: E402
-    GROUPED_NN, GROUPED_NT, GROUPED_TN, gemm_f16_grouped_nn, gemm_f16_grouped_nt, gemm_f16_grouped_tn,
-    gemm_f16_lora_nt, group_rows)
+    gemm_f16_grouped_nn, gemm_f16_grouped_nt, gemm_f16_grouped_tn, gemm_f16_lora_nt, group_rows)

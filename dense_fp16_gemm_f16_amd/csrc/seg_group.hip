@@ -16,10 +16,10 @@
 
 namespace gemm_f16 {
 
-// keys per lane group: counters of every wave and of the chunk
+// Waves whose counters of every key, and two more arrays, fit 64 KB of LDS.
 static int group_waves(int groups) {
     const int keys = groups + 1;
-    return 17 * keys * 4 <= 65536 ? 16 : 9 * keys * 4 <= 65536 ? 8 : 4;
+    return 18 * keys * 4 <= 65536 ? 16 : 10 * keys * 4 <= 65536 ? 8 : 4;
 }
 
 static int group_chunk(int64_t rows) {
@@ -63,36 +63,44 @@ __global__ __launch_bounds__(1024) void group_place_kernel(const GroupParams p) 
     extern __shared__ int lds[];
     const int keys = p.groups + 1, tid = threadIdx.x, threads = blockDim.x;
     const int waves = threads / kWave, wave = tid / kWave, lane = tid % kWave;
-    int *const start = lds;              // [keys] first place of each key
-    int *const mine = lds + keys;        // [waves][keys] counts, then next places
-    for (int x = tid; x < waves * keys; x += threads) mine[x] = 0;
+    int *const start = lds;          // [keys] rows of each key, then its first place
+    int *const before = lds + keys;  // [keys] rows of each key in the chunks before
+    int *const mine = before + keys; // [waves][keys] counts, then next places
+    for (int x = tid; x < (waves + 2) * keys; x += threads) lds[x] = 0;
     __syncthreads();
     const int first = (int)blockIdx.x * p.chunk, last = min(p.rows, first + p.chunk);
     // a wave's part: a whole number of 64-row steps
     const int part = ((p.chunk + waves * kWave - 1) / (waves * kWave)) * kWave;
     const int w0 = min(last, first + wave * part), w1 = min(last, w0 + part);
     for (int r = w0 + lane; r < w1; r += kWave) atomicAdd(&mine[wave * keys + group_key<Id>(p.ids, r, p.groups)], 1);
-    __syncthreads();
-    // totals of each key, and the rows of it before this chunk
-    for (int k = tid; k < keys; k += threads) {
-        int total = 0, before = 0;
-        if (p.blocks > 1) {
+    if (p.blocks > 1) {
+        // totals of each key, and the rows of it before this chunk: the
+        // threads share the chunks, so that few loads follow each other
+        // (one thread per key took 9.8 us over 128 chunks)
+        const int shares = max(1, threads / keys);
+        for (int x = tid; x < shares * keys; x += threads) {
+            const int k = x % keys;
+            int total = 0, below = 0;
 #pragma unroll 8
-            for (int b = 0; b < p.blocks; ++b) {
+            for (int b = x / keys; b < p.blocks; b += shares) {
                 const int v = p.counts[(int64_t)b * keys + k];
                 total += v;
-                before += b < (int)blockIdx.x ? v : 0;
+                below += b < (int)blockIdx.x ? v : 0;
             }
-        } else {
-            for (int w = 0; w < waves; ++w) total += mine[w * keys + k];
+            atomicAdd(&start[k], total);
+            atomicAdd(&before[k], below);
         }
-        start[k] = total;
+    }
+    __syncthreads();
+    for (int k = tid; k < keys; k += threads) {
         // each wave's first place, relative to the key's first
+        int at = before[k];
         for (int w = 0; w < waves; ++w) {
             const int v = mine[w * keys + k];
-            mine[w * keys + k] = before;
-            before += v;
+            mine[w * keys + k] = at;
+            at += v;
         }
+        if (p.blocks == 1) start[k] = at;
     }
     __syncthreads();
     // exclusive scan of the totals over the keys
@@ -143,7 +151,7 @@ static hipError_t launch_group(GroupParams p, hipStream_t s) {
         if (e != hipSuccess) return e;
     }
     return hipLaunchKernel(reinterpret_cast<const void *>(group_place_kernel<Id>), dim3(p.blocks), dim3(waves * kWave),
-                           args, (size_t)(waves + 1) * keys * 4, s);
+                           args, (size_t)(waves + 2) * keys * 4, s);
 }
 
 hipError_t launch_group_rows(int64_t rows, int groups, const void *ids, int id_bytes, int32_t *order, int32_t *inverse,

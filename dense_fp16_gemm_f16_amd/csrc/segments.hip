@@ -193,19 +193,16 @@ static bool few_rows(const SegParams &p) {
 
 static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a, int64_t a_rows,
                    const void *b, const int32_t *offsets, const int32_t *index, int64_t fan, void *c, int32_t out_f32,
-                   void *workspace, int64_t workspace_bytes, void *stream) {
+                   void *stream) {
     int rc = check_grouped(kind, rows, groups, n, k);
     if (rc != GEMM_F16_OK) return rc;
     if (a_rows < 0 || a_rows >= kMaxRows || fan < 1 || fan >= kMaxRows || out_f32 < 0 || out_f32 > 1)
         return GEMM_F16_EINVAL;
     if (!index && a_rows < rows) return GEMM_F16_EINVAL;
-    const int64_t need = gemm_f16_grouped_workspace(kind, rows, groups, n, k);
-    if (workspace_bytes < need) return GEMM_F16_EINVAL;
     const int64_t out = kind == kSegTN ? groups * n * k : rows * n;
     if (out == 0) return GEMM_F16_OK;
     const int es = out_f32 ? 4 : 2;
     const Buffer bufs[] = {{c, out * es, es, true},
-                           {workspace, need, 16, true},
                            {a, a_rows * k * 2, 2, false},
                            {b, (kind == kSegTN ? rows * n : groups * n * k) * 2, 2, false},
                            {offsets, (groups + 1) * 4, 4, false},
@@ -323,30 +320,20 @@ int gemm_f16_group_rows(int64_t rows, int64_t groups, const void *ids, int32_t i
                                     static_cast<int32_t *>(workspace), (hipStream_t)stream));
 }
 
-int64_t gemm_f16_grouped_workspace(int32_t kind, int64_t rows, int64_t groups, int64_t n, int64_t k) {
-    const int rc = check_grouped(kind, rows, groups, n, k);
-    return rc != GEMM_F16_OK ? rc : 0;
-}
-
 int gemm_f16_grouped_nt(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a, int64_t a_rows,
                         const void *b, const int32_t *offsets, const int32_t *index, int64_t fan, void *c,
-                        int32_t out_f32, void *workspace, int64_t workspace_bytes, void *stream) {
-    return grouped(kSegNT, rows, groups, n, k, a, a_rows, b, offsets, index, fan, c, out_f32, workspace,
-                   workspace_bytes, stream);
+                        int32_t out_f32, void *stream) {
+    return grouped(kSegNT, rows, groups, n, k, a, a_rows, b, offsets, index, fan, c, out_f32, stream);
 }
 
 int gemm_f16_grouped_nn(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a, const void *b,
-                        const int32_t *offsets, void *c, int32_t out_f32, void *workspace, int64_t workspace_bytes,
-                        void *stream) {
-    return grouped(kSegNN, rows, groups, n, k, a, rows, b, offsets, nullptr, 1, c, out_f32, workspace, workspace_bytes,
-                   stream);
+                        const int32_t *offsets, void *c, int32_t out_f32, void *stream) {
+    return grouped(kSegNN, rows, groups, n, k, a, rows, b, offsets, nullptr, 1, c, out_f32, stream);
 }
 
 int gemm_f16_grouped_tn(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a, const void *b,
-                        const int32_t *offsets, void *c, int32_t out_f32, void *workspace, int64_t workspace_bytes,
-                        void *stream) {
-    return grouped(kSegTN, rows, groups, n, k, a, rows, b, offsets, nullptr, 1, c, out_f32, workspace, workspace_bytes,
-                   stream);
+                        const int32_t *offsets, void *c, int32_t out_f32, void *stream) {
+    return grouped(kSegTN, rows, groups, n, k, a, rows, b, offsets, nullptr, 1, c, out_f32, stream);
 }
 
 int64_t gemm_f16_lora_workspace(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64_t rank) {

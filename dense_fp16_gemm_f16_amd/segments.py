@@ -17,63 +17,57 @@ status of the library raises ``GemmError``.
 from __future__ import annotations
 
 import contextlib
+import functools
 
 import dense_fp16_gemm_f16_amd as _g
 
-GROUPED_NT = 0
-GROUPED_NN = 1
-GROUPED_TN = 2
-
-_ON = contextlib.nullcontext()
+_HERE = contextlib.nullcontext()
 
 
 def _operand(name, t, dtype, shape, device):
-    """t is a contiguous tensor of dtype on device; a None in shape takes any size."""
+    """t must be a contiguous tensor of this dtype and shape on this GPU."""
+    if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        return
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if t.device != device or not t.is_cuda:
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
         raise ValueError(f"{name} must be on the same GPU as the other operands")
-    if len(t.shape) != len(shape) or any(w is not None and w != v for v, w in zip(t.shape, shape)):
-        raise ValueError(f"{name}: expected shape {tuple('any' if w is None else w for w in shape)}, "
-                         f"got {tuple(t.shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous (row-major)")
+    raise ValueError(f"{name} must be contiguous (row-major)")
+
+
+def _gpu(name, t):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU")
+    return t.device
 
 
 def _on(device, stream):
     """(context, stream handle): allocations inside the context belong to the stream."""
     import torch
 
-    if stream is None:
-        handle = torch.cuda.current_stream(device).cuda_stream
-        return (_ON if torch.cuda.current_device() == device.index else torch.cuda.device(device)), handle
-    return torch.cuda.stream(stream), stream.cuda_stream
-
-
-def _out(out, shape, dtype, device):
-    import torch
-
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _operand("out", out, dtype, shape, device)
-    return out
-
-
-def _workspace(size, device):
-    import torch
-
-    if size < 0:
-        raise _g.GemmError(size)
-    return torch.empty(size, dtype=torch.uint8, device=device) if size else None
+    if stream is not None:
+        return torch.cuda.stream(stream), stream.cuda_stream or None
+    handle = torch._C._cuda_getCurrentRawStream(device.index)
+    return (_HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)), handle or None
 
 
 def _ptr(t):
-    return None if t is None else (t.data_ptr() or None)
+    return t.data_ptr() or None
 
 
 def _check(rc):
     if rc != _g.OK:
         raise _g.GemmError(rc)
+
+
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(name, *sizes):
+    size = getattr(_g.lib(), name)(*sizes)
+    if size < 0:
+        raise _g.GemmError(size)
+    return size
 
 
 def group_rows(ids, groups: int, *, stream=None):
@@ -94,63 +88,48 @@ def group_rows(ids, groups: int, *, stream=None):
         raise ValueError("ids must be on a GPU")
     if not ids.is_contiguous():
         raise ValueError("ids must be contiguous")
-    L, rows, device = _g.lib(), ids.numel(), ids.device
+    rows, device = ids.numel(), ids.device
+    size = _workspace_bytes("gemm_f16_group_rows_workspace", rows, groups)
     context, handle = _on(device, stream)
     with context:
-        ws = _workspace(L.gemm_f16_group_rows_workspace(rows, groups), device)
         order = torch.empty(rows, dtype=torch.int32, device=device)
         inverse = torch.empty(rows, dtype=torch.int32, device=device)
         offsets = torch.empty(groups + 1, dtype=torch.int32, device=device)
-        _check(L.gemm_f16_group_rows(rows, groups, _ptr(ids), ids.element_size(), _ptr(order), _ptr(inverse),
-                                     _ptr(offsets), _ptr(ws), ws.numel() if ws is not None else 0, handle or None))
+        ws = torch.empty(size, dtype=torch.uint8, device=device) if size else None
+        _check(_g.lib().gemm_f16_group_rows(rows, groups, _ptr(ids), ids.element_size(), _ptr(order), _ptr(inverse),
+                                            _ptr(offsets), _ptr(ws) if size else None, size, handle))
     return order, inverse, offsets
 
 
-def _grouped(kind, a, b, offsets, index, fan, out_dtype, out, stream):
+def _output(out, shape, dtype, device):
     import torch
 
-    if a.dim() != 2 or b.dim() != (2 if kind == GROUPED_TN else 3):
-        raise ValueError("expected a [rows,K] and b [rows,N]" if kind == GROUPED_TN
-                         else "expected a [rows,K] and b of three dimensions")
-    if out_dtype not in (torch.float16, torch.float32):
-        raise TypeError("out_dtype must be float16 or float32")
-    device = a.device
-    a_rows, k = a.shape
-    rows = a_rows if index is None else index.numel()
-    _operand("a", a, torch.float16, (None, None), device)
-    if kind == GROUPED_NT:
-        _operand("b", b, torch.float16, (None, None, k), device)
-    elif kind == GROUPED_NN:
-        _operand("b", b, torch.float16, (None, k, None), device)
-    else:
-        _operand("b", b, torch.float16, (a_rows, None), device)
-    groups = offsets.numel() - 1 if kind == GROUPED_TN else b.shape[0]
-    n = b.shape[1] if kind != GROUPED_NN else b.shape[2]
-    _operand("offsets", offsets, torch.int32, (groups + 1,), device)
-    if index is not None:
-        _operand("index", index, torch.int32, (rows,), device)
-    L = _g.lib()
-    size = L.gemm_f16_grouped_workspace(kind, rows, groups, n, k)
-    context, handle = _on(device, stream)
-    with context:
-        ws = _workspace(size, device)
-        out = _out(out, (groups, k, n) if kind == GROUPED_TN else (rows, n), out_dtype, device)
-        f32 = int(out_dtype == torch.float32)
-        if kind == GROUPED_NT:
-            rc = L.gemm_f16_grouped_nt(rows, groups, n, k, _ptr(a), a_rows, _ptr(b), _ptr(offsets), _ptr(index), fan,
-                                       _ptr(out), f32, _ptr(ws), size, handle or None)
-        else:
-            call = L.gemm_f16_grouped_nn if kind == GROUPED_NN else L.gemm_f16_grouped_tn
-            rc = call(rows, groups, n, k, _ptr(a), _ptr(b), _ptr(offsets), _ptr(out), f32, _ptr(ws), size,
-                      handle or None)
-        _check(rc)
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _operand("out", out, dtype, shape, device)
     return out
 
 
-def _f16(dtype):
+def _out_type(out_dtype):
     import torch
 
-    return torch.float16 if dtype is None else dtype
+    if out_dtype is None:
+        return torch.float16
+    if out_dtype is not torch.float16 and out_dtype is not torch.float32:
+        raise TypeError("out_dtype must be float16 or float32")
+    return out_dtype
+
+
+def _pair(a, b, b_dims, what):
+    import torch
+
+    if a.dim() != 2 or b.dim() != b_dims:
+        raise ValueError("expected " + what)
+    if a.dtype is not torch.float16:
+        raise TypeError("a must be float16")
+    device = _gpu("a", a)
+    _operand("a", a, torch.float16, a.shape, device)
+    return device
 
 
 def gemm_f16_grouped_nt(a, b, offsets, *, index=None, fan: int = 1, out_dtype=None, out=None, stream=None):
@@ -162,14 +141,42 @@ def gemm_f16_grouped_nt(a, b, offsets, *, index=None, fan: int = 1, out_dtype=No
     gathers each routed row's token.  ``out_dtype`` float16 (default) or
     float32; rows behind offsets[-1] are zeros.
     """
-    return _grouped(GROUPED_NT, a, b, offsets, index, fan, _f16(out_dtype), out, stream)
+    import torch
+
+    dtype = _out_type(out_dtype)
+    device = _pair(a, b, 3, "a [rows,K] and b [groups,N,K]")
+    (a_rows, k), (groups, n, _) = a.shape, b.shape
+    rows = a_rows if index is None else index.numel()
+    _operand("b", b, torch.float16, (groups, n, k), device)
+    _operand("offsets", offsets, torch.int32, (groups + 1,), device)
+    if index is not None:
+        _operand("index", index, torch.int32, (rows,), device)
+    context, handle = _on(device, stream)
+    with context:
+        out = _output(out, (rows, n), dtype, device)
+        _check(_g.lib().gemm_f16_grouped_nt(rows, groups, n, k, _ptr(a), a_rows, _ptr(b), _ptr(offsets),
+                                            None if index is None else _ptr(index), fan, _ptr(out),
+                                            dtype is torch.float32, handle))
+    return out
 
 
 def gemm_f16_grouped_nn(a, b, offsets, *, out_dtype=None, out=None, stream=None):
     """out[r] = a[r] @ b[g] for each row r of segment g: a float16 [rows,K],
     b float16 [groups,K,N].  With a the gradient of gemm_f16_grouped_nt's
     output and b its weights, the gradient of its rows."""
-    return _grouped(GROUPED_NN, a, b, offsets, None, 1, _f16(out_dtype), out, stream)
+    import torch
+
+    dtype = _out_type(out_dtype)
+    device = _pair(a, b, 3, "a [rows,K] and b [groups,K,N]")
+    (rows, k), (groups, _, n) = a.shape, b.shape
+    _operand("b", b, torch.float16, (groups, k, n), device)
+    _operand("offsets", offsets, torch.int32, (groups + 1,), device)
+    context, handle = _on(device, stream)
+    with context:
+        out = _output(out, (rows, n), dtype, device)
+        _check(_g.lib().gemm_f16_grouped_nn(rows, groups, n, k, _ptr(a), _ptr(b), _ptr(offsets), _ptr(out),
+                                            dtype is torch.float32, handle))
+    return out
 
 
 def gemm_f16_grouped_tn(a, b, offsets, *, out_dtype=None, out=None, stream=None):
@@ -177,7 +184,19 @@ def gemm_f16_grouped_tn(a, b, offsets, *, out_dtype=None, out=None, stream=None)
     [rows,N], out [groups,K,N], zeros for an empty segment.  With a the
     gradient of gemm_f16_grouped_nt's output and b its rows, the gradient of
     its weights."""
-    return _grouped(GROUPED_TN, a, b, offsets, None, 1, _f16(out_dtype), out, stream)
+    import torch
+
+    dtype = _out_type(out_dtype)
+    device = _pair(a, b, 2, "a [rows,K] and b [rows,N]")
+    (rows, k), n, groups = a.shape, b.shape[1], offsets.numel() - 1
+    _operand("b", b, torch.float16, (rows, n), device)
+    _operand("offsets", offsets, torch.int32, (groups + 1,), device)
+    context, handle = _on(device, stream)
+    with context:
+        out = _output(out, (groups, k, n), dtype, device)
+        _check(_g.lib().gemm_f16_grouped_tn(rows, groups, n, k, _ptr(a), _ptr(b), _ptr(offsets), _ptr(out),
+                                            dtype is torch.float32, handle))
+    return out
 
 
 def gemm_f16_lora_nt(x, w, down, up, ids, order, offsets, scale=None, *, out=None, stream=None):
@@ -192,25 +211,23 @@ def gemm_f16_lora_nt(x, w, down, up, ids, order, offsets, scale=None, *, out=Non
 
     if x.dim() != 2 or w.dim() != 2 or down.dim() != 3:
         raise ValueError("expected x [rows,K], w [N,K] and down [adapters,rank,K]")
-    device = x.device
-    rows, k = x.shape
-    n = w.shape[0]
-    adapters, rank = down.shape[:2]
-    _operand("x", x, torch.float16, (None, None), device)
-    _operand("w", w, torch.float16, (None, k), device)
-    _operand("down", down, torch.float16, (None, None, k), device)
+    device = _gpu("x", x)
+    (rows, k), n, (adapters, rank, _) = x.shape, w.shape[0], down.shape
+    _operand("x", x, torch.float16, (rows, k), device)
+    _operand("w", w, torch.float16, (n, k), device)
+    _operand("down", down, torch.float16, (adapters, rank, k), device)
     _operand("up", up, torch.float16, (adapters, n, rank), device)
     _operand("ids", ids, torch.int32, (rows,), device)
     _operand("order", order, torch.int32, (rows,), device)
     _operand("offsets", offsets, torch.int32, (adapters + 1,), device)
     if scale is not None:
         _operand("scale", scale, torch.float32, (adapters,), device)
-    L = _g.lib()
-    size = L.gemm_f16_lora_workspace(rows, n, k, adapters, rank)
+    size = _workspace_bytes("gemm_f16_lora_workspace", rows, n, k, adapters, rank)
     context, handle = _on(device, stream)
     with context:
-        ws = _workspace(size, device)
-        out = _out(out, (rows, n), torch.float16, device)
-        _check(L.gemm_f16_lora_nt(rows, n, k, adapters, rank, _ptr(x), _ptr(w), _ptr(down), _ptr(up), _ptr(ids),
-                                  _ptr(order), _ptr(offsets), _ptr(scale), _ptr(out), _ptr(ws), size, handle or None))
+        out = _output(out, (rows, n), torch.float16, device)
+        ws = torch.empty(size, dtype=torch.uint8, device=device)
+        _check(_g.lib().gemm_f16_lora_nt(rows, n, k, adapters, rank, _ptr(x), _ptr(w), _ptr(down), _ptr(up),
+                                         _ptr(ids), _ptr(order), _ptr(offsets), None if scale is None else _ptr(scale),
+                                         _ptr(out), _ptr(ws), size, handle))
     return out

@@ -204,7 +204,7 @@ int gemm_f16_select_xcd(int64_t num_m, int64_t num_n, int32_t swizzle, int32_t c
  * clamped to [0, rows].  Offsets, ids, indices and orders that break these
  * rules give unspecified outputs but no access out of range.  An output
  * must not overlap any input or the workspace (GEMM_F16_EOVERLAP).
- * workspace: device memory of at least the bytes that the matching
+ * workspace (where a call has one): device memory of at least the bytes that the matching
  * *_workspace function returns (0: may be NULL), 16-byte aligned, its
  * content free to be overwritten until the call's work is done; too few
  * bytes give GEMM_F16_EINVAL.
@@ -251,23 +251,13 @@ int64_t gemm_f16_group_rows_workspace(int64_t rows, int64_t groups);
 int gemm_f16_grouped_nt(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a,
                         int64_t a_rows, const void *b, const int32_t *offsets,
                         const int32_t *index, int64_t fan, void *c, int32_t out_f32,
-                        void *workspace, int64_t workspace_bytes, void *stream);
+                        void *stream);
 int gemm_f16_grouped_nn(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a,
                         const void *b, const int32_t *offsets, void *c, int32_t out_f32,
-                        void *workspace, int64_t workspace_bytes, void *stream);
+                        void *stream);
 int gemm_f16_grouped_tn(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a,
                         const void *b, const int32_t *offsets, void *c, int32_t out_f32,
-                        void *workspace, int64_t workspace_bytes, void *stream);
-
-enum {
-    GEMM_F16_GROUPED_NT = 0,
-    GEMM_F16_GROUPED_NN = 1,
-    GEMM_F16_GROUPED_TN = 2
-};
-/* Workspace bytes of a grouped product (kind: GEMM_F16_GROUPED_*), or a
- * negative status for invalid sizes. */
-int64_t gemm_f16_grouped_workspace(int32_t kind, int64_t rows, int64_t groups, int64_t n,
-                                   int64_t k);
+                        void *stream);
 
 /*
  * A projection shared by requests that each have a low-rank adapter of
