@@ -1,41 +1,25 @@
 // Segmented products of few rows (see segments.h): decoding, and the
-// adapters' inner product there.  The time is B's bytes, so what matters is
-// how many of them are in flight.
-//
-// A workgroup owns a segment and 16 columns.  Its waves share K evenly, in
-// 32-wide steps, each taking up to kThinSteps at a time; a wave's part of B
-// goes straight from memory to registers in the MFMA's layout (lane l: row
-// l % 16, 8 elements at 8 (l / 16)), all of it in flight at once, and stays
-// there for all of the segment's rows, 16 at a time, if that is all.  No LDS and no barrier
-// until the waves' sums meet, in wave order.  Any K, N and alignment: global
-// loads take 2-byte aligned addresses, and the part past K is masked.
+// adapters there.  The time is the weights' bytes, so what matters is how
+// many of them are in flight.
 #include <algorithm>
 
 #include "segments.h"
 
 namespace gemm_f16 {
 
-constexpr int kThinSteps = 8;  // 32-wide steps of K that a wave takes at a time
-
-struct ThinParams {
-    SegParams main;       // rows against main.b
-    SegParams down;       // kThinLora: the adapters' inner product
-    float *sums;          // kThinLora: fp32 [rows, n]
-    int32_t down_blocks;  // kThinLora: workgroups of the inner product
-};
-
-// `count` steps of a row (K >= 8), 32 elements each, from the one that ends
-// a wave's part downwards; 8 elements at kl of each.  The first one, where
+// Up to N steps of a row (K >= 8), 32 elements each, `count` of them from
+// step top - 1 downwards; 8 elements at kl of each.  The first one, where
 // `partial`, reaches past K: its chunks past K become zeros, and the chunk
 // across K is loaded from the row's last 8 elements and shifted, so every
 // load stays inside the row.
-__device__ __forceinline__ void thin_load(half8 (&v)[kThinSteps], const _Float16 *row, int top, int count, bool partial,
+template <int N>
+__device__ __forceinline__ void thin_load(half8 (&v)[N], const _Float16 *row, int top, int count, bool partial,
                                           int kl, int k_elems) {
     const int k0 = 32 * (top - 1) + kl;
 #pragma unroll
-    for (int s = 0; s < kThinSteps; ++s) {
+    for (int s = 0; s < N; ++s) {
         if (s >= count) continue;
-        const int k = s == 0 ? min(k0, k_elems - 8) : k0 - 32 * s;
+        const int k = s == 0 && partial ? min(k0, k_elems - 8) : k0 - 32 * s;
         v[s] = __builtin_bit_cast(half8, (int4v)*reinterpret_cast<const int4u *>(row + k));
     }
     if (partial) {
@@ -46,57 +30,40 @@ __device__ __forceinline__ void thin_load(half8 (&v)[kThinSteps], const _Float16
     }
 }
 
-enum ThinMode : int { kThinPlain = 0, kThinLora = 1, kThinDown = 2 };
-
-// MODE kThinPlain: C of a grouped NT product.  kThinLora: h, each row in its
-// own place, by the first down_blocks workgroups, and x W^T in fp32, one
-// segment of every row, by the others.  kThinDown: h in adapter order, a
-// segment's rows shared by gridDim.y workgroups.
-template <bool F32, int MODE>
-__global__ __launch_bounds__(1024) void seg_thin_kernel(const ThinParams tp) {
-#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
-    __shared__ floatx4 red[2][16][kWave];
-    const int tid = threadIdx.x, lane = tid % kWave, waves = blockDim.x / kWave;
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const bool is_down = MODE == kThinDown || (MODE == kThinLora && (int)blockIdx.x < tp.down_blocks);
-    const SegParams &p = MODE == kThinLora && is_down ? tp.down : tp.main;
-    const uint32_t pid = MODE == kThinLora && !is_down ? blockIdx.x - tp.down_blocks : blockIdx.x;
-
-    const int g = (int)(pid / (uint32_t)p.num_n), n0 = (int)(pid % (uint32_t)p.num_n) * 16;
-    int lo = 0, hi = p.rows;
-    bool live = true;  // false: the rows behind the last segment
-    if (MODE != kThinLora || is_down) {
-        live = g < p.groups;
-        lo = seg_bound(p.offsets, g, p.rows);
-        hi = live ? seg_bound(p.offsets, g + 1, p.rows) : p.rows;
-    }
-    const int step = MODE == kThinDown ? 16 * (int)gridDim.y : 16;
-    if (MODE == kThinDown) lo += 16 * (int)blockIdx.y;
-    if (lo >= hi) return;
-
-    using Out = std::conditional_t<F32, float, _Float16>;
-    if (!live) {
-        for (int r = lo + tid / 16; r < hi; r += (int)blockDim.x / 16)
-            if (n0 + tid % 16 < p.n) static_cast<Out *>(p.c)[(int64_t)r * p.n + n0 + tid % 16] = (Out)0.0f;
-        return;
-    }
+// ---- a segment's rows against 16 rows of B ---------------------------------------
+//
+// The waves share the steps [s0, s1) of K evenly, each taking up to NB at a
+// time; a wave's part of B goes straight from memory to registers in the
+// MFMA's layout (lane l: row l % 16, 8 elements at 8 (l / 16)), all of it in
+// flight at once, and stays there for all of the segment's rows, 16 at a
+// time, if that is all.  No LDS and no barrier until the waves' sums meet, in
+// wave order.  Any K >= 8, N and alignment: global loads take 2-byte aligned
+// addresses, and the part past K is masked.
+//
+// Rows lo, lo + step, .. (16 from each) below hi, columns n0 .. n0 + 15 of
+// segment g.  store(r, n, sum): sum holds columns n .. n + 3 of row r, zeros
+// where the row's index lies outside A.
+template <int NB, int NA, int W, class Store>
+__device__ __forceinline__ void thin_rows(const SegParams &p, floatx4 (*red)[W][kWave], int g, int n0, int lo, int hi,
+                                          int step, int s0, int s1, Store store) {
+    const int lane = threadIdx.x % kWave, waves = blockDim.x / kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     // Lanes past the segment's rows or B's columns read the last one again:
     // their results are never stored.
     const int kl = 8 * (lane / 16);
     const _Float16 *br = p.b + ((int64_t)g * p.n + min(n0 + lane % 16, p.n - 1)) * p.k;
     // this wave's steps, [part0, part1)
-    const int steps = (p.k + 31) / 32;
-    const int part0 = (int)((int64_t)steps * wave / waves), part1 = (int)((int64_t)steps * (wave + 1) / waves);
-    const bool one_pass = part1 - part0 <= kThinSteps;
-    const float f = is_down && p.scale ? p.scale[g] : 1.0f;
-    half8 bf[kThinSteps], af[kThinSteps];
+    const int part0 = s0 + (int)((int64_t)(s1 - s0) * wave / waves);
+    const int part1 = s0 + (int)((int64_t)(s1 - s0) * (wave + 1) / waves);
+    const bool one_pass = part1 - part0 <= NB;
+    half8 bf[NB], af[NA];
     int parity = 0;
     for (int r0 = lo; r0 < hi; r0 += step, parity ^= 1) {
         floatx4 acc = {};
         bool found = true;  // an index outside A: a row of zeros
         const _Float16 *ar = nullptr;
-        for (int top = part1; top > part0; top -= kThinSteps) {
-            const int count = min(top - part0, kThinSteps);
+        for (int top = part1; top > part0; top -= NB) {
+            const int count = min(top - part0, NB);
             const bool partial = 32 * top > p.k;
             if (!one_pass || r0 == lo) thin_load(bf, br, top, count, partial, kl, p.k);
             if (top == part1) {  // behind B's loads
@@ -109,10 +76,14 @@ __global__ __launch_bounds__(1024) void seg_thin_kernel(const ThinParams tp) {
                 found = src >= 0 && src < p.a_rows;
                 ar = p.a + (found ? src : 0) * p.k;
             }
-            thin_load(af, ar, top, count, partial, kl, p.k);
 #pragma unroll
-            for (int s = 0; s < kThinSteps; ++s)
-                if (s < count) acc = Mfma<16>::run(bf[s], af[s], acc);
+            for (int q = 0; q < NB; q += NA) {
+                if (q >= count) continue;
+                thin_load(af, ar, top - q, count - q, partial && q == 0, kl, p.k);
+#pragma unroll
+                for (int s = 0; s < NA; ++s)
+                    if (q + s < count) acc = Mfma<16>::run(bf[q + s], af[s], acc);
+            }
         }
         red[parity][wave][lane] = acc;
         lds_barrier();
@@ -121,21 +92,43 @@ __global__ __launch_bounds__(1024) void seg_thin_kernel(const ThinParams tp) {
         // lane l holds row l % 16, columns 4 (l / 16) ..
         floatx4 sum = red[parity][0][lane];
         for (int w = 1; w < waves; ++w) sum += red[parity][w][lane];
-        const int r = r0 + lane % 16, n = n0 + 4 * (lane / 16);
-        if (r >= hi) continue;
-        if (!found) sum = floatx4{};
-        if (is_down) {
-            // zeros in the columns past the rank, up to h_ld
+        const int r = r0 + lane % 16;
+        if (r < hi) store(r, n0 + 4 * (lane / 16), found ? sum : floatx4{});
+    }
+}
+
+// Zeros in h's columns past the rank, up to h_ld; the others times f.
+__device__ __forceinline__ void store_h(const SegParams &p, float *h, int n, floatx4 sum, float f) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[e] = n + e < p.n ? sum[e] * f : 0.0f;
-            const int to = MODE == kThinDown ? r : min(max(p.index[r], 0), p.rows - 1);
-            if (n < p.h_ld)
-                *reinterpret_cast<floatx4 *>(static_cast<float *>(p.c) + (int64_t)to * p.h_ld + n) = sum;
-        } else if (MODE == kThinLora) {
-            float *c = tp.sums + (int64_t)r * p.n + n;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (n + e < p.n) c[e] = sum[e];
+    for (int e = 0; e < 4; ++e) sum[e] = n + e < p.n ? sum[e] * f : 0.0f;
+    if (n < p.h_ld) *reinterpret_cast<floatx4 *>(h + n) = sum;
+}
+
+// A grouped NT product (DOWN false), or h in adapter order (DOWN), a
+// segment's rows shared by gridDim.y workgroups.
+constexpr int kThinSteps = 8, kThinWaves = 16;
+template <bool F32, bool DOWN>
+__global__ __launch_bounds__(kThinWaves *kWave) void seg_thin_kernel(const SegParams p) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
+    __shared__ floatx4 red[2][kThinWaves][kWave];
+    const int tid = threadIdx.x;
+    const int g = (int)(blockIdx.x / (uint32_t)p.num_n), n0 = (int)(blockIdx.x % (uint32_t)p.num_n) * 16;
+    const bool live = g < p.groups;  // false: the rows behind the last segment
+    int lo = seg_bound(p.offsets, g, p.rows);
+    const int hi = live ? seg_bound(p.offsets, g + 1, p.rows) : p.rows;
+    const int step = DOWN ? 16 * (int)gridDim.y : 16;
+    if (DOWN) lo += 16 * (int)blockIdx.y;
+    if (lo >= hi) return;
+    using Out = std::conditional_t<F32, float, _Float16>;
+    if (!live) {
+        for (int r = lo + tid / 16; r < hi; r += (int)blockDim.x / 16)
+            if (n0 + tid % 16 < p.n) static_cast<Out *>(p.c)[(int64_t)r * p.n + n0 + tid % 16] = (Out)0.0f;
+        return;
+    }
+    const float f = DOWN && p.scale ? p.scale[g] : 1.0f;
+    thin_rows<kThinSteps, kThinSteps, kThinWaves>(p, red, g, n0, lo, hi, step, 0, (p.k + 31) / 32, [&](int r, int n, floatx4 sum) {
+        if constexpr (DOWN) {
+            store_h(p, static_cast<float *>(p.c) + (int64_t)r * p.h_ld, n, sum, f);
         } else {
             typedef Out out4 __attribute__((ext_vector_type(4)));
             Out *c = static_cast<Out *>(p.c) + (int64_t)r * p.n + n;
@@ -150,55 +143,153 @@ __global__ __launch_bounds__(1024) void seg_thin_kernel(const ThinParams tp) {
                     if (n + e < p.n) c[e] = (Out)sum[e];
             }
         }
+    });
+#endif
+}
+
+// ---- adapters, up to kLoraFewRows rows --------------------------------------------
+//
+// One launch for both products by x, whose sums meet in lora_join_kernel:
+//  * x W^T: a workgroup takes 64 rows of W and a slice of K, 512 elements at
+//    a time: its 4 waves hold 16 rows of W each in registers, and x's rows
+//    go through LDS, everything of a step in flight at once.  Slicing K and
+//    not N keeps what each CU reads of x at 64 rows by a slice (all of x per
+//    CU took 4 us more for each 16 rows);
+//  * h = scale_s x D_s^T: 16 ranks of an adapter and a slice of K a
+//    workgroup, by thin_rows.
+constexpr int kFewWaves = 4, kFewCols = 16 * kFewWaves, kFewSteps = 16, kFewK = 32 * kFewSteps;
+constexpr int kFewPitch = kFewK * 2 + 16;  // bytes of a row of x in LDS: 16 rows at one chunk on 16 banks of 16 bytes
+
+struct FewParams {
+    SegParams main, down;
+    float *sums;                    // fp32 [main_parts][rows, n]
+    int32_t down_blocks;            // workgroups of h: (adapter, 16 ranks, part)
+    int32_t main_parts, main_steps; // slices of K, and steps of a slice (a multiple of kFewSteps)
+    int32_t down_parts, down_steps;
+};
+
+// x's elements k .. k + 7 of a row, zeros past K (K >= 8).
+__device__ __forceinline__ int4v few_chunk(const _Float16 *row, int k, int k_elems) {
+    const int4v v = *reinterpret_cast<const int4u *>(row + min(k, k_elems - 8));
+    const int past = k + 8 - k_elems;
+    if (past <= 0) return v;
+    const unsigned __int128 w = __builtin_bit_cast(unsigned __int128, v);
+    return __builtin_bit_cast(int4v, past < 8 ? w >> (16 * past) : (unsigned __int128)0);
+}
+
+// T: tiles of 16 rows
+template <int T>
+__global__ __launch_bounds__(kFewWaves *kWave) __attribute__((amdgpu_waves_per_eu(3, 3)))
+void lora_few_kernel(const FewParams fp) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
+    constexpr int kRed = 2 * kFewWaves * kWave * 16;
+    __shared__ __attribute__((aligned(1024))) char smem[16 * T * kFewPitch > kRed ? 16 * T * kFewPitch : kRed];
+    const int tid = threadIdx.x, lane = tid % kWave;
+    if ((int)blockIdx.x < fp.down_blocks) {
+        const SegParams &p = fp.down;
+        const int part = (int)blockIdx.x % fp.down_parts, x = (int)blockIdx.x / fp.down_parts;
+        const int g = x / p.num_n, n0 = x % p.num_n * 16;
+        const int lo = seg_bound(p.offsets, g, p.rows), hi = seg_bound(p.offsets, g + 1, p.rows);
+        if (lo >= hi) return;
+        const int steps = (p.k + 31) / 32, s0 = min(steps, part * fp.down_steps), s1 = min(steps, s0 + fp.down_steps);
+        const float f = p.scale ? p.scale[g] : 1.0f;
+        float *h = static_cast<float *>(p.c) + (int64_t)part * p.rows * p.h_ld;
+        thin_rows<kFewSteps, 8, kFewWaves>(p, reinterpret_cast<floatx4(*)[kFewWaves][kWave]>(smem), g, n0, lo, hi, 16, s0, s1,
+                                           [&](int r, int n, floatx4 sum) {
+                                               // each row in its own place
+                                               const int to = min(max(p.index[r], 0), p.rows - 1);
+                                               store_h(p, h + (int64_t)to * p.h_ld, n, sum, f);
+                                           });
+        return;
+    }
+    const SegParams &p = fp.main;
+    const int pid = (int)blockIdx.x - fp.down_blocks, part = pid / p.num_n;
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int n0 = pid % p.num_n * kFewCols + 16 * wave;
+    const int steps = (p.k + 31) / 32, s0 = min(steps, part * fp.main_steps), s1 = min(steps, s0 + fp.main_steps);
+    const int kl = 8 * (lane / 16);
+    const _Float16 *wr = p.b + (int64_t)min(n0 + lane % 16, p.n - 1) * p.k;
+    floatx4 acc[T];
+#pragma unroll
+    for (int t = 0; t < T; ++t) acc[t] = floatx4{};
+    for (int at = s0; at < s1; at += kFewSteps) {
+        const int count = min(s1 - at, kFewSteps), top = at + count;
+        half8 bf[kFewSteps];
+        // x: 4 T chunks of 16 bytes a thread, the first 8 of them ahead of W's
+        // loads (loads return in order); rows past the last are never stored
+        constexpr int X = 4 * T, X0 = X < 8 ? X : 8;
+        int4v v[X0];
+        auto fetch = [&](int i) {
+            const int c = i * kFewWaves * kWave + tid;
+            return few_chunk(p.a + (int64_t)min(c / 64, p.rows - 1) * p.k, 32 * at + 8 * (c % 64), p.k);
+        };
+        auto put = [&](int i, int4v u) {
+            const int c = i * kFewWaves * kWave + tid;
+            *reinterpret_cast<int4v *>(smem + c / 64 * kFewPitch + c % 64 * 16) = u;
+        };
+#pragma unroll
+        for (int i = 0; i < X0; ++i) v[i] = fetch(i);
+        thin_load(bf, wr, top, count, 32 * top > p.k, kl, p.k);
+        if (at != s0) lds_barrier();  // the last step's reads are done
+#pragma unroll
+        for (int i = 0; i < X0; ++i) put(i, v[i]);
+#pragma unroll
+        for (int i = X0; i < X; ++i) v[i - X0] = fetch(i);
+#pragma unroll
+        for (int i = X0; i < X; ++i) put(i, v[i - X0]);
+        lds_barrier();
+#pragma unroll
+        for (int s = 0; s < kFewSteps; ++s) {
+            if (s >= count) continue;
+            const char *from = smem + lane % 16 * kFewPitch + (count - 1 - s) * 64 + kl * 2;
+#pragma unroll
+            for (int t = 0; t < T; ++t)
+                acc[t] = Mfma<16>::run(bf[s], *reinterpret_cast<const half8 *>(from + 16 * t * kFewPitch), acc[t]);
+        }
+    }
+    const int n = n0 + 4 * (lane / 16);
+#pragma unroll
+    for (int t = 0; t < T; ++t) {
+        const int r = 16 * t + lane % 16;
+        if (r >= p.rows) continue;
+        float *c = fp.sums + ((int64_t)part * p.rows + r) * p.n + n;
+        if (n + 3 < p.n && p.n % 4 == 0) {
+            *reinterpret_cast<floatx4 *>(c) = acc[t];
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (n + e < p.n) c[e] = acc[t][e];
+        }
     }
 #endif
 }
 
-// y = fp16(sums + h U_s^T): one workgroup per row and 256 columns, every
-// product and sum in fp32.
-__global__ __launch_bounds__(256) void lora_join_kernel(const SegParams p, const float *sums, const int32_t *ids) {
+// y = fp16(x W^T + h U_s^T) from the sums' parts: one workgroup per row and
+// 256 columns, every product and sum in fp32.
+__global__ __launch_bounds__(256) void lora_join_kernel(const SegParams p, const float *sums, int parts,
+                                                        const int32_t *ids) {
     const int r = blockIdx.y, n = (int)(blockIdx.x * 256 + threadIdx.x);
     if (n >= p.n) return;
     const int s = ids[r];
-    float v = sums[(int64_t)r * p.n + n];
+    float v = 0.0f;
+#pragma unroll 4
+    for (int q = 0; q < parts; ++q) v += sums[((int64_t)q * p.rows + r) * p.n + n];
     if (s >= 0 && s < p.adapters) {
-        const float *h = p.h + (int64_t)r * p.h_ld;
         const _Float16 *u = p.up + ((int64_t)s * p.n + n) * p.rank;
+        auto h = [&](int j) {
+            float x = 0.0f;
+            for (int q = 0; q < p.h_parts; ++q) x += p.h[((int64_t)q * p.rows + r) * p.h_ld + j];
+            return x;
+        };
         int j = 0;
         for (; j + 8 <= p.rank; j += 8) {
             const half8 w = __builtin_bit_cast(half8, (int4v)*reinterpret_cast<const int4u *>(u + j));
 #pragma unroll
-            for (int e = 0; e < 8; ++e) v = __builtin_fmaf(h[j + e], (float)w[e], v);
+            for (int e = 0; e < 8; ++e) v = __builtin_fmaf(h(j + e), (float)w[e], v);
         }
-        for (; j < p.rank; ++j) v = __builtin_fmaf(h[j], (float)u[j], v);
+        for (; j < p.rank; ++j) v = __builtin_fmaf(h(j), (float)u[j], v);
     }
     static_cast<_Float16 *>(p.c)[(int64_t)r * p.n + n] = (_Float16)v;
-}
-
-template <class Kernel>
-static hipError_t launch_thin(Kernel kernel, int64_t grid, int threads, hipStream_t stream, const ThinParams &p,
-                              unsigned grid_y = 1) {
-    if (grid <= 0) return hipSuccess;
-    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-    void *args[] = {const_cast<ThinParams *>(&p)};
-    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3((unsigned)grid, grid_y), dim3((unsigned)threads),
-                           args, 0, stream);
-}
-
-// waves that K keeps busy in one pass
-static int thin_threads(int k) {
-    int w = 1;
-    while (w < 16 && w * kThinSteps * 32 < k) w *= 2;
-    return w * kWave;
-}
-
-hipError_t launch_seg_thin(bool f32, const SegParams &p, hipStream_t s) {
-    ThinParams t = {};
-    t.main = p;
-    t.main.num_n = (p.n + 15) / 16;
-    const int64_t grid = (int64_t)(p.groups + 1) * t.main.num_n;
-    return f32 ? launch_thin(seg_thin_kernel<true, kThinPlain>, grid, thin_threads(p.k), s, t)
-               : launch_thin(seg_thin_kernel<false, kThinPlain>, grid, thin_threads(p.k), s, t);
 }
 
 // h of K < 8, where no chunk of a row is whole: one lane per element.
@@ -218,36 +309,79 @@ __global__ __launch_bounds__(256) void lora_down_short_kernel(const SegParams p)
     static_cast<float *>(p.c)[x] = sum;
 }
 
+// ---- launches -----------------------------------------------------------------------
+
+template <bool F32, bool DOWN>
+static hipError_t launch_thin(SegParams p, int cols, int64_t groups, int shares, hipStream_t s) {
+    p.num_n = (cols + 15) / 16;
+    const int64_t grid = groups * p.num_n;
+    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    int waves = 1;  // that K keeps busy in one pass
+    while (waves < kThinWaves && waves * kThinSteps * 32 < p.k) waves *= 2;
+    void *args[] = {&p};
+    return hipLaunchKernel(reinterpret_cast<const void *>(seg_thin_kernel<F32, DOWN>),
+                           dim3((unsigned)grid, (unsigned)shares), dim3((unsigned)(waves * kWave)), args, 0, s);
+}
+
+hipError_t launch_seg_thin(bool f32, const SegParams &p, hipStream_t s) {
+    return f32 ? launch_thin<true, false>(p, p.n, p.groups + 1, 1, s)
+               : launch_thin<false, false>(p, p.n, p.groups + 1, 1, s);
+}
+
 hipError_t launch_lora_down_thin(const SegParams &p, hipStream_t s) {
     if (p.k < 8) {
         const int64_t grid = ((int64_t)p.rows * p.h_ld + 255) / 256;
         if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
         return launch_seg(lora_down_short_kernel, grid, 256, s, p);
     }
-    ThinParams t = {};
-    t.main = p;
-    t.main.num_n = (p.h_ld + 15) / 16;
     // some 64 rows a workgroup of an even split
     const int64_t shares = std::min<int64_t>(std::max<int64_t>(p.rows / (64 * (int64_t)p.groups), 1), 1024);
-    return launch_thin(seg_thin_kernel<true, kThinDown>, (int64_t)p.groups * t.main.num_n, thin_threads(p.k), s, t,
-                       (unsigned)shares);
+    return launch_thin<true, true>(p, p.h_ld, p.groups, (int)shares, s);
+}
+
+// Slices of K for steps of `unit` 32-wide steps: at most `most`, equal but
+// for the last.
+static int few_slices(int64_t k, int unit, int most, int32_t *steps) {
+    const int64_t all = (k + 31) / 32, units = (all + unit - 1) / unit;
+    const int64_t parts = std::min<int64_t>(units, most), each = (units + parts - 1) / parts;
+    *steps = (int32_t)(each * unit);
+    return (int)((units + each - 1) / each);
+}
+
+int lora_few_parts(int64_t k) {
+    int32_t steps;
+    return few_slices(k, kFewSteps, 8, &steps);
+}
+int lora_few_h_parts(int64_t k) {
+    int32_t steps;
+    return few_slices(k, kFewSteps * kFewWaves, 4, &steps);
 }
 
 hipError_t launch_lora_few(const SegParams &p, const SegParams &down, float *sums, const int32_t *ids, hipStream_t s) {
-    ThinParams t = {};
-    t.main = p;
-    t.main.num_n = (p.n + 15) / 16;
-    t.down = down;
-    t.down.num_n = (down.h_ld + 15) / 16;
-    t.sums = sums;
-    t.down_blocks = down.groups * t.down.num_n;  // a row without an adapter needs no h
-    hipError_t e = launch_thin(seg_thin_kernel<true, kThinLora>, t.down_blocks + (int64_t)t.main.num_n,
-                               thin_threads(p.k), s, t);
+    FewParams f = {};
+    f.main = p;
+    f.main.num_n = (p.n + kFewCols - 1) / kFewCols;
+    f.main_parts = few_slices(p.k, kFewSteps, 8, &f.main_steps);
+    f.down = down;
+    f.down.num_n = (down.h_ld + 15) / 16;
+    f.down_parts = few_slices(p.k, kFewSteps * kFewWaves, 4, &f.down_steps);
+    f.down_blocks = down.groups * f.down.num_n * f.down_parts;
+    f.sums = sums;
+    const int64_t grid = f.down_blocks + (int64_t)f.main.num_n * f.main_parts;
+    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    void *args[] = {&f};
+    const int tiles = (p.rows + 15) / 16;
+    const void *kernel = tiles <= 1   ? reinterpret_cast<const void *>(lora_few_kernel<1>)
+                         : tiles == 2 ? reinterpret_cast<const void *>(lora_few_kernel<2>)
+                         : tiles == 3 ? reinterpret_cast<const void *>(lora_few_kernel<3>)
+                                      : reinterpret_cast<const void *>(lora_few_kernel<4>);
+    hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)grid), dim3(kFewWaves * kWave), args, 0, s);
     if (e != hipSuccess) return e;
     SegParams j = p;
-    void *args[] = {&j, &sums, &ids};
+    j.h_parts = f.down_parts;
+    void *join[] = {&j, &sums, &f.main_parts, &ids};
     return hipLaunchKernel(reinterpret_cast<const void *>(lora_join_kernel),
-                           dim3((unsigned)((p.n + 255) / 256), (unsigned)p.rows), dim3(256), args, 0, s);
+                           dim3((unsigned)((p.n + 255) / 256), (unsigned)p.rows), dim3(256), join, 0, s);
 }
 
 }  // namespace gemm_f16

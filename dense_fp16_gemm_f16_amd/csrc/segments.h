@@ -706,7 +706,10 @@ hipError_t launch_seg_thin(bool f32, const SegParams &p, hipStream_t s);
 // h in adapter order: direct-to-LDS tiles, K in `splits` slices; or any rows
 hipError_t launch_lora_down(SegParams p, int splits, hipStream_t s);
 hipError_t launch_lora_down_thin(const SegParams &p, hipStream_t s);
-// sums: fp32 [rows, n]; down.c is h with rows in their own order
+// sums: fp32 [lora_few_parts(k)][rows, n]; down.c is h with rows in their own
+// order, lora_few_h_parts(k) arrays
+int lora_few_parts(int64_t k);
+int lora_few_h_parts(int64_t k);
 hipError_t launch_lora_few(const SegParams &p, const SegParams &down, float *sums, const int32_t *ids, hipStream_t s);
 
 hipError_t launch_seg_staged(int kind, bool f32, bool lora, SegParams p, hipStream_t s);

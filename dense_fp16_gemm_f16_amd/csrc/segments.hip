@@ -271,7 +271,7 @@ static int64_t lora_h_ld(int64_t rows, int64_t k, int64_t rank) {
 
 // Slices of K that h is summed in: 64 x 64 tiles alone fill too few CUs.
 static int lora_parts(int64_t rows, int64_t k) {
-    if (lora_few(rows, k)) return 1;
+    if (lora_few(rows, k)) return lora_few_h_parts(k);
 #ifdef GEMM_F16_SEG_TUNE
     if (const char *f = std::getenv("SEG_PARTS")) return std::atoi(f);
 #endif
@@ -340,7 +340,7 @@ int64_t gemm_f16_lora_workspace(int64_t rows, int64_t n, int64_t k, int64_t adap
     const int rc = check_lora(rows, n, k, adapters, rank);
     if (rc != GEMM_F16_OK) return rc;
     // h, and x W^T in fp32 for few rows
-    return rows * lora_h_ld(rows, k, rank) * lora_parts(rows, k) * 4 + (lora_few(rows, k) ? rows * n * 4 : 0);
+    return rows * lora_h_ld(rows, k, rank) * lora_parts(rows, k) * 4 + (lora_few(rows, k) ? rows * n * lora_few_parts(k) * 4 : 0);
 }
 
 int gemm_f16_lora_nt(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64_t rank, const void *x, const void *w,
@@ -393,7 +393,7 @@ int gemm_f16_lora_nt(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64
     p.groups = 1;
     p.n = (int32_t)n;
     if (lora_few(rows, k))
-        return status(launch_lora_few(p, d, static_cast<float *>(workspace) + rows * lora_h_ld(rows, k, rank), ids, (hipStream_t)stream));
+        return status(launch_lora_few(p, d, static_cast<float *>(workspace) + rows * lora_h_ld(rows, k, rank) * lora_parts(rows, k), ids, (hipStream_t)stream));
     const bool direct = direct_rows(kSegNT, d) && direct_rows(kSegNT, p);
     p.h_parts = direct ? lora_parts(rows, k) : 1;
     rc = status(direct ? launch_lora_down(d, p.h_parts, (hipStream_t)stream)
