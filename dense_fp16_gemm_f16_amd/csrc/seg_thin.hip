@@ -104,7 +104,7 @@ __device__ __forceinline__ void store_h(const SegParams &p, float *h, int n, flo
     if (n < p.h_ld) *reinterpret_cast<floatx4 *>(h + n) = sum;
 }
 
-// A grouped NT product (DOWN false), or h in adapter order (DOWN), a
+// A grouped NT product (DOWN false), or h in adapter order as pairs (DOWN), a
 // segment's rows shared by gridDim.y workgroups.
 constexpr int kThinSteps = 8, kThinWaves = 16;
 template <bool F32, bool DOWN>
@@ -128,7 +128,7 @@ __global__ __launch_bounds__(kThinWaves *kWave) void seg_thin_kernel(const SegPa
     const float f = DOWN && p.scale ? p.scale[g] : 1.0f;
     thin_rows<kThinSteps, kThinSteps, kThinWaves>(p, red, g, n0, lo, hi, step, 0, (p.k + 31) / 32, [&](int r, int n, floatx4 sum) {
         if constexpr (DOWN) {
-            store_h(p, static_cast<float *>(p.c) + (int64_t)r * p.h_ld, n, sum, f);
+            if (n < p.h_ld) store_pairs(static_cast<char *>(p.c) + (int64_t)r * p.h_ld * 4, n, sum, f, p.rank);
         } else {
             typedef Out out4 __attribute__((ext_vector_type(4)));
             Out *c = static_cast<Out *>(p.c) + (int64_t)r * p.n + n;
@@ -292,21 +292,25 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const SegParams p, const
     static_cast<_Float16 *>(p.c)[(int64_t)r * p.n + n] = (_Float16)v;
 }
 
-// h of K < 8, where no chunk of a row is whole: one lane per element.
+// h of K < 8, where no chunk of a row is whole: one lane per 4 values.
 __global__ __launch_bounds__(256) void lora_down_short_kernel(const SegParams p) {
-    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, r = x / p.h_ld;
-    const int j = (int)(x % p.h_ld);
+    const int per = p.h_ld / 4;
+    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, r = x / per;
+    const int n = (int)(x % per) * 4;
     if (r >= p.rows) return;
     int g = 0;  // the segment of row r
     while (g < p.groups && r >= seg_bound(p.offsets, g + 1, p.rows)) ++g;
     const int src = p.index[r];
-    float sum = 0.0f;
-    if (g < p.groups && j < p.n && src >= 0 && src < p.a_rows) {
-        for (int k = 0; k < p.k; ++k)
-            sum += (float)p.a[(int64_t)src * p.k + k] * (float)p.b[((int64_t)g * p.n + j) * p.k + k];
-        if (p.scale) sum *= p.scale[g];
+    floatx4 sum = {};
+    if (g < p.groups && src >= 0 && src < p.a_rows) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (n + e >= p.n) continue;
+            for (int k = 0; k < p.k; ++k)
+                sum[e] += (float)p.a[(int64_t)src * p.k + k] * (float)p.b[((int64_t)g * p.n + n + e) * p.k + k];
+        }
     }
-    static_cast<float *>(p.c)[x] = sum;
+    store_pairs(static_cast<char *>(p.c) + r * p.h_ld * 4, n, sum, g < p.groups && p.scale ? p.scale[g] : 1.0f, p.rank);
 }
 
 // ---- launches -----------------------------------------------------------------------
@@ -330,7 +334,7 @@ hipError_t launch_seg_thin(bool f32, const SegParams &p, hipStream_t s) {
 
 hipError_t launch_lora_down_thin(const SegParams &p, hipStream_t s) {
     if (p.k < 8) {
-        const int64_t grid = ((int64_t)p.rows * p.h_ld + 255) / 256;
+        const int64_t grid = ((int64_t)p.rows * (p.h_ld / 4) + 255) / 256;
         if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
         return launch_seg(lora_down_short_kernel, grid, 256, s, p);
     }

@@ -34,11 +34,12 @@ struct SegParams {
     // low-rank adapters (kLora kernels): rows sorted by adapter, row r of
     // C and A is order[r]
     const int32_t *order;
-    const float *h;         // [rows, h_ld] fp32: scale_s (x D_s^T), zeros past the rank
+    const float *h;         // up to kLoraFewRows rows: [h_parts][rows, h_ld] fp32, whose sum is scale_s (x D_s^T)
+    const char *h_pairs;    // more rows: rows of h_ld values, zeros past the rank (store_pairs)
     const _Float16 *up;     // [adapters, n, rank]
     const float *scale;     // [adapters]: multiplies the rows of h (null: 1)
     int32_t adapters, rank, h_ld;
-    int32_t h_parts;        // h is the sum of this many [rows, h_ld] arrays, one after the other
+    int32_t h_parts;
 };
 
 // Segment bounds, clamped so that any content of offsets stays in range.
@@ -311,13 +312,13 @@ __device__ __forceinline__ void seg_store(const floatx4 (&acc)[C::FN][C::FM], ch
 
 // ---- adapters: the low-rank product on top of a tile ---------------------------
 //
-// Adds h U_s^T, h = scale_s x D_s^T in fp32, to a tile of x W^T whose rows
-// are sorted by adapter: for each adapter with rows in the tile and each 32
-// of its ranks, one K-tile whose A is h, zero in rows of other adapters,
-// and whose B is U_s.  h has fp32's range, so it goes through the MFMA as
-// two bf16 parts (h = h0 + h1 to 2^-18 of it) and U_s as two that hold it
-// exactly; the product leaves out h1 u1, at most 2^-18 of h U.  Against the
-// 2^-11 half step of y, one fp16 part would have cost accuracy and range.
+// Adds h U_s^T, h = scale_s x D_s^T, to a tile of x W^T whose rows are
+// sorted by adapter: for each adapter with rows in the tile and each 32 of its
+// ranks, one K-tile whose A is h, zero in rows of other adapters, and whose
+// B is U_s.  h has fp32's range, so it goes through the MFMA as two bf16
+// parts (h = h0 + h1 to 2^-18 of it) and U_s as two that hold it exactly; the
+// product leaves out h1 u1, at most 2^-18 of h U.  Against the 2^-11 half
+// step of y, one fp16 part would have cost accuracy and range.
 //
 // An infinity or NaN in U_s would reach the rows of other adapters as
 // 0 * inf: it is taken as 0 here, and lora_wild adds its products to the
@@ -327,6 +328,23 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ void mfma16_tied_bf16(bf16x8 a, bf16x8 b, floatx4 &c) {
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+
+// h as its consumer's K-tiles: a row holds, for each 32 ranks, 32 values h0
+// and the 32 rests h1, bf16, 128 bytes.  Four values of a row, times f; zeros
+// past the rank (n % 4 == 0, n < h_ld).
+__device__ __forceinline__ void store_pairs(char *row, int n, floatx4 v, float f, int rank) {
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    bf16x4 top, rest;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float x = n + e < rank ? v[e] * f : 0.0f;
+        top[e] = (__bf16)x;
+        rest[e] = (__bf16)(fabsf(x) < __builtin_inff() ? x - (float)top[e] : 0.0f);
+    }
+    char *to = row + n / 32 * 128 + n % 32 * 2;
+    *reinterpret_cast<bf16x4 *>(to) = top;
+    *reinterpret_cast<bf16x4 *>(to + 64) = rest;
 }
 
 // The adapters with rows in [row0, row0 + valid), in order: lane l looks at
@@ -356,35 +374,40 @@ struct LoraWalk {
 };
 
 // Returns (to every thread) whether some U_s of the tile is not finite.
-// votes: one int per wave, in the kernel's one LDS array (a library vote
-// would bring an array of its own, see seg_tile_kernel).  RANK4: the rank is
-// a multiple of 4, so half chunks lie wholly inside a row of U_s; the tails
-// of other ranks cost scalar registers that the 256-wide tiles do not have.
+// w: the first adapter with rows in the tile.  votes: one int per wave, in
+// the kernel's one LDS array (a library vote would bring an array of its own,
+// see seg_tile).  RANK4: the rank is a multiple of 4, so half chunks lie
+// wholly inside a row of U_s; the tails of other ranks cost scalar registers
+// that the 256-wide tiles do not have.
+//
+// Two LDS stages.  h's K-tile comes straight into the other stage under the
+// MFMAs of this one; U_s comes through registers two K-tiles ahead, and is
+// split and written an element at a time between the MFMAs.  (Through
+// registers one K-tile ahead, with h in fp32 and K's slices of it summed
+// here, each K-tile waited 3 us for its loads.)
 template <class C, bool RANK4>
 __device__ __forceinline__ bool lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *smem, int *votes, const SegParams &p,
-                                           int row0, int valid, int n0, int tid, int lane, int wm, int wn) {
-    constexpr int kRow = 128, kB = C::BM * kRow;
+                                           LoraWalk w, int row0, int valid, int n0, int tid, int lane, int wm, int wn) {
+    constexpr int kRow = 128, kB = C::BM * kRow, kStage = (C::BM + C::BN) * kRow;
     auto sw = [](int r) { return (r >> 1) & 7; };
-    // This thread's chunks of one K-tile: h's 8 ranks at 8 (x % 4) of tile
-    // rows x / 4, and U's.  Loaded one K-tile ahead.
-    constexpr int HA = (C::BM * 4 + C::kThreads - 1) / C::kThreads, HB = C::BN * 4 / C::kThreads;
-    static_assert(HB * C::kThreads == C::BN * 4, "whole passes");
-    floatx4 h0[HA], h1[HA];
-    int4v u[HB];
+    constexpr int LA = C::BM * kRow / 1024 / C::kWaves, HB = C::BN * 4 / C::kThreads;
+    static_assert(LA * 1024 * C::kWaves == C::BM * kRow && HB * C::kThreads == C::BN * 4, "whole passes");
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const uint32_t pitch = (uint32_t)p.h_ld * 4u;
+    const __amdgpu_buffer_rsrc_t h_rows = make_rsrc(p.h_pairs + (int64_t)row0 * pitch, (uint32_t)valid * pitch);
     const _Float16 *up_end = p.up + (int64_t)p.adapters * p.n * p.rank;
-    auto fetch = [&](const LoraWalk &w, int c) {
+    int c = 0;  // w's next K-tile starts at rank c
+    auto load_h = [&](int stage) {
 #pragma unroll
-        for (int i = 0; i < HA; ++i) {
-            const int x = i * C::kThreads + tid, r = x >> 2;
-            h0[i] = h1[i] = floatx4{};
-            if (r >= w.lo && r < w.hi) {
-                const float *h = p.h + (int64_t)(row0 + r) * p.h_ld + c + 8 * (x & 3);
-                for (int q = 0; q < p.h_parts; ++q, h += (int64_t)p.rows * p.h_ld) {
-                    h0[i] += *reinterpret_cast<const floatx4 *>(h);
-                    h1[i] += *reinterpret_cast<const floatx4 *>(h + 4);
-                }
-            }
+        for (int i = 0; i < LA; ++i) {
+            const int r = (i * C::kWaves + wave) * 8 + (lane >> 3);
+            const uint32_t off = (uint32_t)r * pitch + (uint32_t)(((lane & 7) ^ sw(r)) << 4);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                h_rows, (__attribute__((address_space(3))) void *)(smem + stage * kStage + (i * C::kWaves + wave) * 1024),
+                16, r >= w.lo && r < w.hi ? off : kOutOfRange, (uint32_t)c * 4u, 0, 0);
         }
+    };
+    auto fetch_u = [&](int4v (&u)[HB]) {
         const _Float16 *up = p.up + (int64_t)w.s * p.n * p.rank;
 #pragma unroll
         for (int i = 0; i < HB; ++i) {
@@ -407,73 +430,83 @@ __device__ __forceinline__ bool lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *s
             }
         }
     };
-
-    int wild = 0, c = 0;
-    LoraWalk w;
-    w.next(p, row0, valid, lane);
-    if (w.s >= 0) fetch(w, 0);
-    while (w.s >= 0) {
-#pragma unroll
-        for (int i = 0; i < HA; ++i) {
-            const int x = i * C::kThreads + tid, r = x >> 2, q = x & 3;
-            if (HA * C::kThreads > C::BM * 4 && r >= C::BM) continue;
-            bf16x8 top, rest;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float v = e < 4 ? h0[i][e & 3] : h1[i][e & 3];
-                top[e] = (__bf16)v;
-                rest[e] = (__bf16)(fabsf(v) < __builtin_inff() ? v - (float)top[e] : 0.0f);
-            }
-            *reinterpret_cast<bf16x8 *>(smem + r * kRow + ((q ^ sw(r)) << 4)) = top;
-            *reinterpret_cast<bf16x8 *>(smem + r * kRow + (((q + 4) ^ sw(r)) << 4)) = rest;
-        }
-#pragma unroll
-        for (int i = 0; i < HB; ++i) {
-            const int x = i * C::kThreads + tid, r = x >> 2, q = x & 3;
-            const half8 v = __builtin_bit_cast(half8, u[i]);
-            bf16x8 top, rest;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                float f = (float)v[e];
-                if (!(fabsf(f) < __builtin_inff())) {
-                    f = 0.0f;
-                    wild = 1;
-                }
-                top[e] = (__bf16)f;
-                rest[e] = (__bf16)(f - (float)top[e]);  // exact: at most 3 bits are left
-            }
-            *reinterpret_cast<bf16x8 *>(smem + kB + r * kRow + ((q ^ sw(r)) << 4)) = top;
-            *reinterpret_cast<bf16x8 *>(smem + kB + r * kRow + (((q + 4) ^ sw(r)) << 4)) = rest;
-        }
-        lds_barrier();
+    auto advance = [&]() {
         c += 32;
         if (c >= p.rank) {
             w.next(p, row0, valid, lane);
             c = 0;
         }
-        if (w.s >= 0) fetch(w, c);
-
-        // u0 h0 and u1 h0, then u0 h1
-#pragma unroll
-        for (int ka = 0; ka < 2; ++ka) {
-            bf16x8 af[C::FM];
-#pragma unroll
-            for (int i = 0; i < C::FM; ++i) {
-                const int r = wm * C::TM + i * 16 + lane % 16;
-                af[i] = *reinterpret_cast<const bf16x8 *>(smem + r * kRow + (((4 * ka + lane / 16) ^ sw(r)) << 4));
-            }
-#pragma unroll
-            for (int kb = 0; kb < 2 - ka; ++kb)
-#pragma unroll
-                for (int j = 0; j < C::FN; ++j) {
-                    const int r = wn * C::TN + j * 16 + lane % 16;
-                    const bf16x8 bf = *reinterpret_cast<const bf16x8 *>(smem + kB + r * kRow +
-                                                                        (((4 * kb + lane / 16) ^ sw(r)) << 4));
-#pragma unroll
-                    for (int i = 0; i < C::FM; ++i) mfma16_tied_bf16(bf, af[i], acc[j][i]);
-                }
+    };
+    // Element e of this thread's chunks of U_s split into its bf16 parts; a
+    // whole chunk goes to LDS.
+    int wild = 0;
+    bf16x8 top, rest;
+    int4v u[HB], ahead[HB];
+    auto split = [&](auto e_c, char *to) {
+        constexpr int i = decltype(e_c)::value / 8, e = decltype(e_c)::value % 8;
+        float v = (float)__builtin_bit_cast(half8, u[i])[e];
+        if (!(fabsf(v) < __builtin_inff())) {
+            v = 0.0f;
+            wild = 1;
         }
-        lds_barrier();
+        top[e] = (__bf16)v;
+        rest[e] = (__bf16)(v - (float)top[e]);  // exact: at most 3 bits are left
+        if constexpr (e == 7) {
+            const int x = i * C::kThreads + tid, r = x >> 2, q = x & 3;
+            *reinterpret_cast<bf16x8 *>(to + kB + r * kRow + ((q ^ sw(r)) << 4)) = top;
+            *reinterpret_cast<bf16x8 *>(to + kB + r * kRow + (((q + 4) ^ sw(r)) << 4)) = rest;
+        }
+    };
+    constexpr int E = HB * 8;
+    // u0 h0, u1 h0, then u0 h1
+    constexpr int NM = C::FM * C::FN, M = 3 * NM;
+
+    int stage = 0;
+    bool more = w.s >= 0;
+#pragma unroll
+    for (int i = 0; i < HB; ++i) ahead[i] = int4v{0, 0, 0, 0};
+    if (more) {
+        load_h(0);
+        fetch_u(u);
+        advance();
+        if (w.s >= 0) fetch_u(ahead);
+        static_range<0, E>([&](auto e_c) { split(e_c, smem); });
+    }
+    vm_barrier<0>();
+    while (more) {
+        // stage holds this K-tile; w and c are at the next one, whose U_s is
+        // in `ahead` (past the last, what is split is never read)
+#pragma unroll
+        for (int i = 0; i < HB; ++i) u[i] = ahead[i];
+        more = w.s >= 0;
+        if (more) {
+            load_h(stage ^ 1);
+            advance();
+            if (w.s >= 0) fetch_u(ahead);
+        }
+        const char *from = smem + stage * kStage;
+        char *to = smem + (stage ^ 1) * kStage;
+        bf16x8 af[C::FM], bf = {};
+        static_range<0, M>([&](auto m_c) {
+            constexpr int m = decltype(m_c)::value;
+            constexpr int ka = m / (2 * NM), kb = m / NM % 2, j = m % NM / C::FM, i = m % C::FM;
+            if constexpr (m % (2 * NM) == 0) {
+#pragma unroll
+                for (int q = 0; q < C::FM; ++q) {
+                    const int r = wm * C::TM + q * 16 + lane % 16;
+                    af[q] = *reinterpret_cast<const bf16x8 *>(from + r * kRow + (((4 * ka + lane / 16) ^ sw(r)) << 4));
+                }
+            }
+            if constexpr (i == 0) {
+                const int r = wn * C::TN + j * 16 + lane % 16;
+                bf = *reinterpret_cast<const bf16x8 *>(from + kB + r * kRow + (((4 * kb + lane / 16) ^ sw(r)) << 4));
+            }
+            mfma16_tied_bf16(bf, af[i], acc[j][i]);
+            static_range<m * E / M, (m + 1) * E / M>([&](auto e_c) { split(e_c, to); });
+            __builtin_amdgcn_sched_barrier(0);
+        });
+        vm_barrier<0>();
+        stage ^= 1;
     }
     acc_fence(acc);
     const uint64_t ballot = __ballot(wild);
@@ -504,9 +537,8 @@ __device__ __forceinline__ void lora_wild(const SegParams &p, int row0, int vali
                 for (int j = 0; j < p.rank; ++j) {
                     const float f = (float)up[j];
                     if (fabsf(f) < __builtin_inff()) continue;
-                    float h = 0.0f;
-                    for (int q = 0; q < p.h_parts; ++q) h += p.h[((int64_t)q * p.rows + r) * p.h_ld + j];
-                    sum += h * f;
+                    const __bf16 *h = reinterpret_cast<const __bf16 *>(p.h_pairs + (int64_t)r * p.h_ld * 4 + j / 32 * 128);
+                    sum += ((float)h[j % 32] + (float)h[32 + j % 32]) * f;
                 }
                 if (!(fabsf(sum) < __builtin_inff())) y[n] = (_Float16)((float)y[n] + sum);
             }
@@ -648,7 +680,9 @@ __global__ __launch_bounds__(C::kThreads) void seg_staged_kernel(const SegParams
     constexpr int kWaveBytes = kLds / C::kWaves;
     char *const stg = smem + wave * kWaveBytes;
     if constexpr (LORA) {
-        const bool wild = lora_tiles<C, false>(acc, smem, reinterpret_cast<int *>(smem + kLds), p, row0, valid, n0, tid, lane, wm, wn);
+        LoraWalk walk;
+        walk.next(p, row0, valid, lane);
+        const bool wild = lora_tiles<C, false>(acc, smem, reinterpret_cast<int *>(smem + kLds), p, walk, row0, valid, n0, tid, lane, wm, wn);
         const int32_t *order = p.order;
         const int rows = p.rows;
         seg_store<C, F32, kWaveBytes>(acc, stg, p.c, valid, p.n, n0, wm, wn, lane, [&](int r) {
@@ -703,8 +737,8 @@ hipError_t launch_seg_lora(int tile, const SegParams &p, hipStream_t s);
 // Few rows (seg_thin.hip).
 constexpr int64_t kLoraFewRows = 64;  // rows up to here: launch_lora_few
 hipError_t launch_seg_thin(bool f32, const SegParams &p, hipStream_t s);
-// h in adapter order: direct-to-LDS tiles, K in `splits` slices; or any rows
-hipError_t launch_lora_down(SegParams p, int splits, hipStream_t s);
+// h as pairs, rows in adapter order: direct-to-LDS tiles, or any rows
+hipError_t launch_lora_down(SegParams p, hipStream_t s);
 hipError_t launch_lora_down_thin(const SegParams &p, hipStream_t s);
 // sums: fp32 [lora_few_parts(k)][rows, n]; down.c is h with rows in their own
 // order, lora_few_h_parts(k) arrays

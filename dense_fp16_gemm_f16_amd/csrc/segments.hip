@@ -263,23 +263,15 @@ static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k,
 // The few-row kernel's loads need a whole chunk of K.
 static bool lora_few(int64_t rows, int64_t k) { return rows <= kLoraFewRows && k >= 8; }
 
-// h's row pitch: whole 16-byte stores, and for lora_tiles whole 32-wide steps
+// Values of h in a row: whole 16-byte stores, or lora_tiles' whole 32 ranks as
+// pairs of 2 bytes
 static int64_t lora_h_ld(int64_t rows, int64_t k, int64_t rank) {
     const int64_t to = lora_few(rows, k) ? 4 : 32;
     return (rank + to - 1) / to * to;
 }
 
-// Slices of K that h is summed in: 64 x 64 tiles alone fill too few CUs.
-static int lora_parts(int64_t rows, int64_t k) {
-    if (lora_few(rows, k)) return lora_few_h_parts(k);
-#ifdef GEMM_F16_SEG_TUNE
-    if (const char *f = std::getenv("SEG_PARTS")) return std::atoi(f);
-#endif
-    const int64_t tiles = (rows + 63) / 64;
-    int parts = 1;
-    while (parts < 4 && tiles * parts < 256 && k >= parts * 1024) parts *= 2;
-    return parts;
-}
+// Arrays whose sum is h.
+static int lora_parts(int64_t rows, int64_t k) { return lora_few(rows, k) ? lora_few_h_parts(k) : 1; }
 
 static int check_lora(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64_t rank) {
     if (rows < 0 || n < 0 || k < 0 || rows >= kMaxRows || n >= kMaxRows || k >= kMaxK) return GEMM_F16_EINVAL;
@@ -389,14 +381,14 @@ int gemm_f16_lora_nt(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64
     p.b = static_cast<const _Float16 *>(w);
     p.c = y;
     p.h = static_cast<const float *>(workspace);
+    p.h_pairs = static_cast<const char *>(workspace);
     p.up = static_cast<const _Float16 *>(up);
     p.groups = 1;
     p.n = (int32_t)n;
     if (lora_few(rows, k))
         return status(launch_lora_few(p, d, static_cast<float *>(workspace) + rows * lora_h_ld(rows, k, rank) * lora_parts(rows, k), ids, (hipStream_t)stream));
     const bool direct = direct_rows(kSegNT, d) && direct_rows(kSegNT, p);
-    p.h_parts = direct ? lora_parts(rows, k) : 1;
-    rc = status(direct ? launch_lora_down(d, p.h_parts, (hipStream_t)stream)
+    rc = status(direct ? launch_lora_down(d, (hipStream_t)stream)
                        : launch_lora_down_thin(d, (hipStream_t)stream));
     if (rc != GEMM_F16_OK) return rc;
     // x W^T + h U_s^T

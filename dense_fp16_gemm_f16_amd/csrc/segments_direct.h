@@ -141,6 +141,10 @@ __device__ __forceinline__ void seg_tile(const SegParams &p, char *smem, const S
         b_tile = b + w.n0;
     }
 
+    // the first adapter of the tile: its offsets arrive under the K loop
+    LoraWalk walk;
+    if constexpr (LORA) walk.next(p, w.row0, w.valid, lane);
+
     floatx4 acc[FN][FM];
 #pragma unroll
     for (int j = 0; j < FN; ++j)
@@ -264,7 +268,7 @@ __device__ __forceinline__ void seg_tile(const SegParams &p, char *smem, const S
     lds_barrier();
     if constexpr (LORA) {
         const bool wild =
-            lora_tiles<C, true>(acc, smem, reinterpret_cast<int *>(smem + kLds), p, row0, valid, n0, t, l, wm, wn);
+            lora_tiles<C, true>(acc, smem, reinterpret_cast<int *>(smem + kLds), p, walk, row0, valid, n0, t, l, wm, wn);
         const int32_t *order = p.order;
         const int rows = p.rows;
         seg_store<C, F32, kWaveBytes>(acc, stg, p.c, valid, p.n, n0, wm, wn, l,
@@ -299,9 +303,8 @@ void seg_tile_kernel(const SegParams p) {
 // next load fills, and has waited for its own loads of the next K-tile).
 // A K-tile of 2 stages in flight leaves a CU waiting for memory most of the
 // time here; the ring keeps S - 1 of them in flight.
-// SPLIT: workgroup x of gridDim.y slices of K writes its fp32 sums to its
-// part of the workspace (h of the adapters, times their scale).
-template <int KIND, class C, int S, bool F32, bool SPLIT>
+// DOWN: h of the adapters, times their scale, as pairs.
+template <int KIND, class C, int S, bool F32, bool DOWN>
 __global__ __launch_bounds__(C::kThreads) void seg_ring_kernel(const SegParams p) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
     constexpr int TM = C::TM, TN = C::TN, FM = C::FM, FN = C::FN;
@@ -319,15 +322,12 @@ __global__ __launch_bounds__(C::kThreads) void seg_ring_kernel(const SegParams p
     const int wm = wave / C::WN, wn = wave % C::WN;
     SegWork<KIND, C, false> w;
     if (!w.find(p, blockIdx.x, lane)) return;
-    // this slice's K-tiles
-    const int all = (w.k_count + C::BK - 1) / C::BK;
-    const int per = SPLIT ? (all + (int)gridDim.y - 1) / (int)gridDim.y : all;
-    const int kt0 = SPLIT ? min(all, (int)blockIdx.y * per) : 0, kt1 = SPLIT ? min(all, kt0 + per) : all;
+    const int kt_count = (w.k_count + C::BK - 1) / C::BK;
 
     OpA opa;
     OpB opb;
     if (p.index) {
-        opa.init(p.a, (int)p.a_rows, p.k, kt1, wave, lane, wm * TM, 0);
+        opa.init(p.a, (int)p.a_rows, p.k, kt_count, wave, lane, wm * TM, 0);
 #pragma unroll
         for (int i = 0; i < OpA::kLoads; ++i) {
             const int r = (i * C::kWaves + wave) * 8 + (lane >> 3);
@@ -340,13 +340,13 @@ __global__ __launch_bounds__(C::kThreads) void seg_ring_kernel(const SegParams p
             opa.voff[i] = off;
         }
     } else {
-        opa.init(p.a + (int64_t)w.row0 * p.k, w.valid, p.k, kt1, wave, lane, wm * TM, 0);
+        opa.init(p.a + (int64_t)w.row0 * p.k, w.valid, p.k, kt_count, wave, lane, wm * TM, 0);
     }
     const _Float16 *b = p.b + (int64_t)(w.live ? w.g : 0) * p.n * p.k;
     if constexpr (KIND == kSegNT)
-        opb.init(b + (int64_t)w.n0 * p.k, max(min(C::BN, p.n - w.n0), 0), p.k, kt1, wave, lane, wn * TN, OpA::kStage);
+        opb.init(b + (int64_t)w.n0 * p.k, max(min(C::BN, p.n - w.n0), 0), p.k, kt_count, wave, lane, wn * TN, OpA::kStage);
     else
-        opb.init(p.b, 0, p.n, p.k, kt1, wave, lane, wn * TN, OpA::kStage);
+        opb.init(p.b, 0, p.n, p.k, kt_count, wave, lane, wn * TN, OpA::kStage);
 
     floatx4 acc[FN][FM];
 #pragma unroll
@@ -365,11 +365,11 @@ __global__ __launch_bounds__(C::kThreads) void seg_ring_kernel(const SegParams p
                 opb.template load_tile<0>(to, b + w.n0, w.n0, nmajor_bytes<C>(w.k_count, t, p.n, w.n0), t, i - LA);
         }
     };
-    if (kt0 < kt1) {
+    if (kt_count > 0) {
 #pragma unroll
-        for (int s = 0; s < S - 1; ++s) load(kt0 + s, s);  // past the last: empty loads, for the count
+        for (int s = 0; s < S - 1; ++s) load(s, s);  // past the last: empty loads, for the count
         int stage = 0;
-        for (int t = kt0; t < kt1; ++t) {
+        for (int t = 0; t < kt_count; ++t) {
             vm_barrier<(S - 2) * L>();
             load(t + S - 1, stage == 0 ? S - 1 : stage - 1);
             const char *from = smem + stage * kStage;
@@ -393,14 +393,19 @@ __global__ __launch_bounds__(C::kThreads) void seg_ring_kernel(const SegParams p
     constexpr int kWaveBytes = kLds / C::kWaves / 1024 * 1024;
     char *const stg = smem + wave * kWaveBytes;
     const int row0 = w.row0;
-    if constexpr (SPLIT) {
+    if constexpr (DOWN) {
         const float f = w.live && p.scale ? p.scale[w.g] : 1.0f;
 #pragma unroll
-        for (int j = 0; j < FN; ++j)
+        for (int i = 0; i < FM; ++i) {
+            const int r = wm * TM + 16 * i + lane % 16;
+            if (r >= w.valid) continue;
+            char *row = static_cast<char *>(p.c) + (int64_t)(row0 + r) * p.h_ld * 4;
 #pragma unroll
-            for (int i = 0; i < FM; ++i) acc[j][i] *= f;
-        float *c = static_cast<float *>(p.c) + (int64_t)blockIdx.y * p.rows * p.h_ld;
-        seg_store<C, true, kWaveBytes>(acc, stg, c, w.valid, p.h_ld, w.n0, wm, wn, lane, [&](int r) { return row0 + r; });
+            for (int j = 0; j < FN; ++j) {
+                const int n = w.n0 + wn * TN + 16 * j + 4 * (lane / 16);
+                if (n < p.h_ld) store_pairs(row, n, acc[j][i], f, p.rank);
+            }
+        }
     } else {
         seg_store<C, F32, kWaveBytes>(acc, stg, p.c, w.valid, p.n, w.n0, wm, wn, lane, [&](int r) { return row0 + r; });
     }
