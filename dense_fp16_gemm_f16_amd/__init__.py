@@ -89,7 +89,12 @@ def lib() -> ctypes.CDLL:
         raise RuntimeError(
             f"{LIB_PATH} is missing: build it with dense_fp16_gemm_f16_amd.build.build() "
             "(there is no fallback path)")
-    L = ctypes.CDLL(LIB_PATH)
+    _lib = _declare(ctypes.CDLL(LIB_PATH))
+    return _lib
+
+
+def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
+    """Argument and result types of every entry point."""
     i64, p, i32 = ctypes.c_int64, ctypes.c_void_p, ctypes.c_int32
     L.gemm_f16_nt.argtypes = [i64, i64, i64, p, p, p, p]
     L.gemm_f16_nt.restype = ctypes.c_int
@@ -121,7 +126,6 @@ def lib() -> ctypes.CDLL:
     L.gemm_f16_lora_nt.restype = ctypes.c_int
     L.gemm_f16_lora_workspace.argtypes = [i64, i64, i64, i64, i64]
     L.gemm_f16_lora_workspace.restype = i64
-    _lib = L
     return L
 
 

@@ -18,12 +18,12 @@ hipError_t launch_seg_lora(int tile, const SegParams &p, hipStream_t s) {
 hipError_t launch_lora_down(SegParams p, hipStream_t s) {
     // 32 x 64 tiles: with 64 rows a tile, 4096 rows fill a quarter of the CUs
     using C = Cfg<32, 64, 1, 4, 16>;
-    constexpr int S = 8;
+    constexpr int S = 6, KG = 2;
     p.num_n = (p.h_ld + C::BN - 1) / C::BN;
     p.num_m = (int32_t)seg_row_tiles(p.rows, p.groups, C::BM);
     const int64_t grid = (int64_t)p.num_m * p.num_n;
     if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-    return launch_seg(seg_ring_kernel<kSegNT, C, S, true, true>, grid, C::kThreads, s, p);
+    return launch_seg(seg_ring_kernel<kSegNT, C, S, KG, true, true>, grid, C::kThreads * KG, s, p);
 }
 
 }  // namespace gemm_f16

@@ -11,7 +11,8 @@ hipError_t launch_seg_nn(int tile, bool f32, const SegParams &p, hipStream_t s) 
         case kSeg128x128: return launch_seg_tile<kSegNN, Cfg<128, 128, 2, 2, 16>>(p, f32, s);
         case kSeg64x128: return launch_seg_tile<kSegNN, Cfg<64, 128, 2, 2, 16>>(p, f32, s);
         case kSeg32x128: return launch_seg_tile<kSegNN, Cfg<32, 128, 1, 4, 16>>(p, f32, s);
-        case kSegRing: return launch_seg_ring<kSegNN, Cfg<32, 128, 1, 4, 16>, 4>(p, f32, s);
+        case kSegRing: return launch_seg_ring<kSegNN, Cfg<32, 128, 1, 4, 16>, 4, 1>(p, f32, s);
+        case kSegRing2: return launch_seg_ring<kSegNN, Cfg<32, 128, 1, 4, 16>, 4, 2>(p, f32, s);
         default: return hipErrorInvalidValue;
     }
 }

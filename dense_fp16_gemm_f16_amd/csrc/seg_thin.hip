@@ -184,6 +184,7 @@ void lora_few_kernel(const FewParams fp) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
     constexpr int kRed = 2 * kFewWaves * kWave * 16;
     __shared__ __attribute__((aligned(1024))) char smem[16 * T * kFewPitch > kRed ? 16 * T * kFewPitch : kRed];
+    GEMM_POISON_LDS(smem);
     const int tid = threadIdx.x, lane = tid % kWave;
     if ((int)blockIdx.x < fp.down_blocks) {
         const SegParams &p = fp.down;

@@ -4,7 +4,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 #include <iterator>
 
 #include "device.h"
@@ -100,7 +99,7 @@ struct SegPlan {
 // fastest tile's in the geometric mean and at most 1.5 of it.  With tiles to
 // walk, walking measured 0.88 to 0.97 of the one-tile kernel's time on most
 // shapes (nt, 256 x 128, 1 to 2 rounds: 0.91) and up to 1.15 on few.  The
-// 32-row ring serves few rows per segment, where B's bytes bound the
+// 32-row rings serve few rows per segment, where B's bytes bound the
 // product.
 static SegPlan pick_plan(int kind, bool f32, const SegParams &p, int cus) {
     struct Cand {
@@ -116,6 +115,7 @@ static SegPlan pick_plan(int kind, bool f32, const SegParams &p, int cus) {
         {kSeg64x128, 64, 128, 2.84, 0.375, 3.87, 0, 0, 0},
         {kSeg32x128, 32, 128, 2.67, 0.315, 2.72, 0, 0, 0},
         {kSegRing, 32, 64, 3.57, 0.180, 0.55, 0, 0, 0},
+        {kSegRing2, 32, 64, 3.30, 0.165, 1.00, 0, 0, 0},
     };
     static const Cand nn[] = {
         {kSeg256x256, 256, 256, 6.97, 1.070, 11.80, 2.0, 1.360, 10.0},
@@ -125,6 +125,7 @@ static SegPlan pick_plan(int kind, bool f32, const SegParams &p, int cus) {
         {kSeg64x128, 64, 128, 3.03, 0.405, 3.13, 0, 0, 0},
         {kSeg32x128, 32, 128, 2.73, 0.343, 2.27, 0, 0, 0},
         {kSegRing, 32, 128, 3.59, 0.284, 1.14, 0, 0, 0},
+        {kSegRing2, 32, 128, 3.40, 0.250, 1.00, 0, 0, 0},
     };
     static const Cand tn[] = {
         {kSeg256x256, 256, 256, 10.0, 1.390, 8.20, 0, 0, 0},
@@ -138,7 +139,7 @@ static SegPlan pick_plan(int kind, bool f32, const SegParams &p, int cus) {
     SegPlan best = {kSeg128x128, false};
     double best_t = 1e300;
     for (const Cand *c = first; c != last; ++c) {
-        if (p.order && c->id == kSegRing) continue;  // no adapters there
+        if (p.order && c->id >= kSegRing) continue;  // no adapters there
         double m_tiles, k_tiles;
         if (kind == kSegTN) {
             m_tiles = (double)(cdiv64(p.k, c->bm) * p.groups);
@@ -150,6 +151,9 @@ static SegPlan pick_plan(int kind, bool f32, const SegParams &p, int cus) {
         }
         const double share = m_tiles * (double)cdiv64(p.n, c->bn) / cus;
         const bool walk = can_walk(kind, c->bm, c->bn, f32, p, cus) && c->wa > 0 && share > 1;
+        // half of K to each half of the waves: where the grid leaves CUs idle
+        // (nt, 64 tiles of 57 K-tiles: 0.77 of the ring's time; 400 tiles: 1.1)
+        if (c->id == kSegRing2 && share > (kind == kSegNT ? 0.7 : 0.4)) continue;
         double t;
         if (walk) {
             const double whole = std::floor(share), rest = share - whole;
@@ -165,14 +169,6 @@ static SegPlan pick_plan(int kind, bool f32, const SegParams &p, int cus) {
             best = {c->id, walk};
         }
     }
-#ifdef GEMM_F16_SEG_TUNE
-    if (const char *f = std::getenv("SEG_TILE")) {
-        best.tile = std::atoi(f);
-        static const int bms[] = {256, 256, 128}, bns[] = {256, 128, 256};
-        const char *w = std::getenv("SEG_WALK");
-        best.walk = best.tile < 3 && can_walk(kind, bms[best.tile], bns[best.tile], f32, p, cus) && !(w && !std::atoi(w));
-    }
-#endif
     return best;
 }
 
@@ -183,11 +179,12 @@ static SegPlan pick_plan(int kind, bool f32, const SegParams &p, int cus) {
 // against 10.8).  With more tiles the ring is level or faster (45 rows, 4
 // segments of 3056 x 2520: 13.1 against 19.5), except for a handful of rows
 // where every wave has whole passes of 256 elements and two workgroups share
-// a CU (16 rows over 8 segments of 4096 x 2048: 31 against 35.5).
-static bool few_rows(const SegParams &p) {
+// a CU (16 rows over 8 segments of 4096 x 2048: 31 against 35.5).  Rows that
+// cannot go straight into LDS have no ring to go to.
+static bool few_rows(const SegParams &p, bool direct) {
     const int64_t segments = std::min<int64_t>(p.groups, p.rows);
     if (p.k < 8 || p.rows > 16 * segments) return false;
-    return segments * cdiv64(p.n, 64) <= 176 ||
+    return !direct || segments * cdiv64(p.n, 64) <= 176 ||
            (p.rows <= 4 * segments && p.k % 256 == 0 && p.k >= 1024 && p.k <= 2048);
 }
 
@@ -225,25 +222,18 @@ static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k,
     p.n = (int32_t)n;
     p.k = (int32_t)k;
     p.fan = (int32_t)fan;
-#ifdef GEMM_F16_SEG_TUNE
-    const char *force = std::getenv("SEG_TILE");
-    const bool thin = kind == kSegNT && (force ? std::atoi(force) == kSegTiles : few_rows(p));
-#else
-    const bool thin = kind == kSegNT && few_rows(p);
-#endif
-    if (thin || (kind == kSegNT && k >= 8 && rows <= 16 * std::min(groups, rows) && !direct_rows(kind, p)))
+    const bool direct = direct_rows(kind, p);
+    // (the few-row kernel reads some row of A even for an index outside it)
+    if (kind == kSegNT && a_rows > 0 && few_rows(p, direct))
         return status(launch_seg_thin(out_f32 != 0, p, (hipStream_t)stream));
-    if (direct_rows(kind, p)) {
+    if (direct) {
         const SegPlan plan = pick_plan(kind, out_f32 != 0, p, cus);
         const int tile = plan.tile;
         hipError_t e;
         if (plan.walk) {
             // cache policy of the stores: see c_store_policy in gemm_f16.hip
             const int64_t bytes = (a_rows * k + (kind == kSegTN ? rows * n : groups * n * k)) * 2 + out * es;
-            bool dev = bytes <= (int64_t(256) << 20) || (n * es) % 128 != 0 || (uintptr_t)c % 128 != 0;
-#ifdef GEMM_F16_SEG_TUNE
-            if (const char *f = std::getenv("SEG_DEV")) dev = std::atoi(f);
-#endif
+            const bool dev = bytes <= (int64_t(256) << 20) || (n * es) % 128 != 0 || (uintptr_t)c % 128 != 0;
             switch (kind) {
                 case kSegNT: e = launch_seg_walk_nt(tile, out_f32 != 0, dev, cus, p, (hipStream_t)stream); break;
                 default: e = launch_seg_walk_nn(tile, out_f32 != 0, dev, cus, p, (hipStream_t)stream); break;

@@ -298,36 +298,46 @@ void seg_tile_kernel(const SegParams p) {
 }
 
 // Small tiles, where the operands' bytes bound the product: one workgroup
-// per tile and K slice, a ring of S LDS stages loaded S - 1 K-tiles ahead,
-// one barrier per K-tile (before it, every wave has read the stage that the
-// next load fills, and has waited for its own loads of the next K-tile).
-// A K-tile of 2 stages in flight leaves a CU waiting for memory most of the
-// time here; the ring keeps S - 1 of them in flight.
+// per tile, a ring of S LDS stages loaded S - 1 K-tiles ahead, one barrier
+// per K-tile (before it, every wave has read the stage that the next load
+// fills, and has waited for its own loads of the next K-tile).  Two stages
+// leave a CU waiting for memory most of the time here; the ring keeps S - 1
+// K-tiles in flight.  KG 2: twice the waves, each half of them with a ring of
+// its own over half of K, the halves' sums meeting in LDS: for grids that
+// leave CUs with one workgroup or none.
 // DOWN: h of the adapters, times their scale, as pairs.
-template <int KIND, class C, int S, bool F32, bool DOWN>
-__global__ __launch_bounds__(C::kThreads) void seg_ring_kernel(const SegParams p) {
+template <int KIND, class C, int S, int KG, bool F32, bool DOWN>
+__global__ __launch_bounds__(C::kThreads *KG) void seg_ring_kernel(const SegParams p) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
     constexpr int TM = C::TM, TN = C::TN, FM = C::FM, FN = C::FN;
     using OpA = KMajorDirect<C, C::BM, false>;
     using OpB = std::conditional_t<KIND == kSegNT, KMajorDirect<C, C::BN, false>, NMajorDirect<C, true>>;
     constexpr int kStage = OpA::kStage + OpB::kStage;
     constexpr int LA = OpA::kLoads, L = OpA::kLoads + OpB::kLoads;
-    constexpr int kLds = S * kStage;
+    constexpr int kRing = S * kStage, kLds = KG * kRing;
     static_assert(kLds <= 160 * 1024 && S >= 3 && (S - 1) * L < 64, "LDS budget, vmcnt range");
     __shared__ __attribute__((aligned(1024))) char smem[kLds];
     GEMM_POISON_LDS(smem);
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int group = __builtin_amdgcn_readfirstlane(tid / C::kThreads);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave) - group * C::kWaves;
+    char *const ring = smem + group * kRing;
     const int wm = wave / C::WN, wn = wave % C::WN;
     SegWork<KIND, C, false> w;
     if (!w.find(p, blockIdx.x, lane)) return;
-    const int kt_count = (w.k_count + C::BK - 1) / C::BK;
+    // this group's K-tiles: `turns` for every group, those past kt1 zeros
+    const int kt_count = (w.k_count + C::BK - 1) / C::BK, turns = (kt_count + KG - 1) / KG;
+    const int kt0 = group * turns, kt1 = min(kt0 + turns, kt_count);
+    // Where this workgroup starts in them: rows a power of two apart put one
+    // K-tile of every row on the same memory channels, so workgroups in step
+    // would all wait for those.
+    const int shift = turns > 0 ? (int)((blockIdx.x * 5u) % (uint32_t)turns) : 0;
 
     OpA opa;
     OpB opb;
     if (p.index) {
-        opa.init(p.a, (int)p.a_rows, p.k, kt_count, wave, lane, wm * TM, 0);
+        opa.init(p.a, (int)p.a_rows, p.k, kt1, wave, lane, wm * TM, 0);
 #pragma unroll
         for (int i = 0; i < OpA::kLoads; ++i) {
             const int r = (i * C::kWaves + wave) * 8 + (lane >> 3);
@@ -340,21 +350,23 @@ __global__ __launch_bounds__(C::kThreads) void seg_ring_kernel(const SegParams p
             opa.voff[i] = off;
         }
     } else {
-        opa.init(p.a + (int64_t)w.row0 * p.k, w.valid, p.k, kt_count, wave, lane, wm * TM, 0);
+        opa.init(p.a + (int64_t)w.row0 * p.k, w.valid, p.k, kt1, wave, lane, wm * TM, 0);
     }
     const _Float16 *b = p.b + (int64_t)(w.live ? w.g : 0) * p.n * p.k;
     if constexpr (KIND == kSegNT)
-        opb.init(b + (int64_t)w.n0 * p.k, max(min(C::BN, p.n - w.n0), 0), p.k, kt_count, wave, lane, wn * TN, OpA::kStage);
+        opb.init(b + (int64_t)w.n0 * p.k, max(min(C::BN, p.n - w.n0), 0), p.k, kt1, wave, lane, wn * TN, OpA::kStage);
     else
-        opb.init(p.b, 0, p.n, p.k, kt_count, wave, lane, wn * TN, OpA::kStage);
+        opb.init(p.b, 0, p.n, p.k, kt1, wave, lane, wn * TN, OpA::kStage);
 
     floatx4 acc[FN][FM];
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
         for (int i = 0; i < FM; ++i) acc[j][i] = floatx4{};
-    auto load = [&](int t, int stage) {
-        char *to = smem + stage * kStage;
+    auto load = [&](int turn, int stage) {  // past the last turn: empty loads, for the count
+        char *to = ring + stage * kStage;
+        const int at = turn + shift < turns ? turn + shift : turn + shift - turns;
+        const int t = turn < turns ? kt0 + at : kt1;
 #pragma unroll
         for (int i = 0; i < L; ++i) {
             if (i < LA)
@@ -362,17 +374,17 @@ __global__ __launch_bounds__(C::kThreads) void seg_ring_kernel(const SegParams p
             else if constexpr (KIND == kSegNT)
                 opb.template load<0>(to, t, i - LA);
             else
-                opb.template load_tile<0>(to, b + w.n0, w.n0, nmajor_bytes<C>(w.k_count, t, p.n, w.n0), t, i - LA);
+                opb.template load_tile<0>(to, b + w.n0, w.n0, nmajor_bytes<C>(min(w.k_count, kt1 * C::BK), t, p.n, w.n0), t, i - LA);
         }
     };
-    if (kt_count > 0) {
+    if (turns > 0) {
 #pragma unroll
-        for (int s = 0; s < S - 1; ++s) load(s, s);  // past the last: empty loads, for the count
+        for (int s = 0; s < S - 1; ++s) load(s, s);
         int stage = 0;
-        for (int t = 0; t < kt_count; ++t) {
+        for (int t = 0; t < turns; ++t) {
             vm_barrier<(S - 2) * L>();
             load(t + S - 1, stage == 0 ? S - 1 : stage - 1);
-            const char *from = smem + stage * kStage;
+            const char *from = ring + stage * kStage;
 #pragma unroll
             for (int ks = 0; ks < C::KS; ++ks) {
                 half8 af[FM], bf[FN];
@@ -389,6 +401,25 @@ __global__ __launch_bounds__(C::kThreads) void seg_ring_kernel(const SegParams p
         }
     }
     vm_barrier<0>();  // no load is still writing LDS when C is staged there
+    if constexpr (KG == 2) {
+        static_assert(C::kThreads * FN * FM * 16 <= kRing, "the second half's sums");
+        floatx4 *const sums = reinterpret_cast<floatx4 *>(smem) + (tid - group * C::kThreads);
+        if (group == 1) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int i = 0; i < FM; ++i) sums[(j * FM + i) * C::kThreads] = acc[j][i];
+        }
+        lds_barrier();
+        if (group == 0) {
+#pragma unroll
+            for (int j = 0; j < FN; ++j)
+#pragma unroll
+                for (int i = 0; i < FM; ++i) acc[j][i] += sums[(j * FM + i) * C::kThreads];
+        }
+        lds_barrier();
+        if (group == 1) return;
+    }
 
     constexpr int kWaveBytes = kLds / C::kWaves / 1024 * 1024;
     char *const stg = smem + wave * kWaveBytes;
@@ -412,14 +443,14 @@ __global__ __launch_bounds__(C::kThreads) void seg_ring_kernel(const SegParams p
 #endif
 }
 
-template <int KIND, class C, int S>
+template <int KIND, class C, int S, int KG>
 hipError_t launch_seg_ring(SegParams p, bool f32, hipStream_t s) {
     p.num_n = (p.n + C::BN - 1) / C::BN;
     p.num_m = (int32_t)seg_row_tiles(p.rows, p.groups, C::BM);
     const int64_t grid = (int64_t)p.num_m * p.num_n;
     if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
-    return f32 ? launch_seg(seg_ring_kernel<KIND, C, S, true, false>, grid, C::kThreads, s, p)
-               : launch_seg(seg_ring_kernel<KIND, C, S, false, false>, grid, C::kThreads, s, p);
+    return f32 ? launch_seg(seg_ring_kernel<KIND, C, S, KG, true, false>, grid, C::kThreads * KG, s, p)
+               : launch_seg(seg_ring_kernel<KIND, C, S, KG, false, false>, grid, C::kThreads * KG, s, p);
 }
 
 // Launch of tile C: the grid holds every tile that any sizes could need.

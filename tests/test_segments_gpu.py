@@ -1,11 +1,15 @@
 """The segmented products on the GPU against their definitions in 64 bits
 (_segments.py derives the bounds): row grouping, products grouped by
 expert, their gradients, and low-rank adapters."""
+import ctypes
+import os
+
 import numpy as np
 import pytest
 import torch
 
 import dense_fp16_gemm_f16_amd as g
+from dense_fp16_gemm_f16_amd import build
 from tests import _segments as ref
 
 pytestmark = pytest.mark.gpu
@@ -74,6 +78,48 @@ def test_grouped_is_exact_on_eighths(kind, sizes, n, k, f32):
     out = CALL[kind](a, b, off, out_dtype=dtype)
     assert out.dtype == dtype and out.shape == want.shape
     assert torch.equal(out, want.to(dtype))
+
+
+# more tiles than CUs (walked tiles, with a last round cut small, rows of no
+# segment, one K-tile), long K on few tiles, and one row against wide weights
+LARGE = [
+    ([3000, 0, 700, 5, 4000], 2048, 1024, 300), ([2500, 1200, 800, 4100], 1544, 1608, 0), ([700, 300] * 8, 4096, 64, 0),
+    ([60, 500, 0, 130], 4096, 4096, 0), ([1, 0, 2], 904, 3280, 1), ([9000], 2304, 200, 0), ([40, 0, 25, 30], 320, 4096, 9),
+]
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("kind", ["nt", "nn", "tn"])
+@pytest.mark.parametrize("sizes, n, k, tail", LARGE)
+def test_grouped_is_exact_at_large_sizes(kind, sizes, n, k, tail, f32):
+    dtype = torch.float32 if f32 else torch.float16
+    gen = _gen(n + k)
+    a, b, off = _inputs(kind, sizes, n, k, gen, tail=tail)
+    want, _, _ = ref.grouped(kind, a, b, off.tolist())
+    assert torch.equal(CALL[kind](a, b, off, out_dtype=dtype), want.to(dtype))
+    if kind == "nt":
+        index = torch.randperm(3 * len(a), generator=gen, device="cuda")[:len(a)].to(torch.int32)
+        want, _, _ = ref.grouped(kind, a, b, off.tolist(), index, 3)
+        assert torch.equal(g.gemm_f16_grouped_nt(a, b, off, index=index, fan=3, out_dtype=dtype), want.to(dtype))
+
+
+@pytest.mark.parametrize("kind", ["nt", "nn", "tn"])
+@pytest.mark.parametrize("sizes, n, k", [SIZES[i] for i in (3, 4, 5, 6, 14, 15)] + [s[:3] for s in LARGE[:5]])
+def test_no_kernel_reads_lds_that_nothing_wrote(kind, sizes, n, k, monkeypatch):
+    """The debug build fills LDS with NaN before the first load."""
+    if not os.path.exists(build.POISON_LIB):
+        pytest.skip("libgemm_f16_poison.so is not built")
+    monkeypatch.setattr(g, "_lib", g._declare(ctypes.CDLL(build.POISON_LIB)))
+    gen = _gen(n)
+    a, b, off = _inputs(kind, sizes, n, k, gen)
+    want, _, _ = ref.grouped(kind, a, b, off.tolist())
+    assert torch.equal(CALL[kind](a, b, off), want.half())
+    if kind == "nt":
+        for rows, runs in ((3, False), (40, False), (300, True)):
+            make = lambda gen, *s: torch.randint(-1, 2, s, generator=gen, device="cuda").half()  # noqa: E731
+            x, w, down, up, ids, order, aoff, scale = _adapters(rows, 4, 16, n, min(k, 512), runs, gen, make)
+            want, _ = ref.lora(x, w, down, up, ids, scale)
+            assert torch.equal(g.gemm_f16_lora_nt(x, w, down, up, ids, order, aoff, scale), want.half())
 
 
 @pytest.mark.parametrize("f32", [False, True])
@@ -177,6 +223,15 @@ def test_an_index_outside_the_rows_reads_zeros(n, k):
     assert not out[[1, 2, 4, 5]].any()
 
 
+def test_an_index_into_no_rows_at_all():
+    h = torch.empty(0, 1024, dtype=torch.float16, device="cuda")
+    b = ref.eighths(_gen(1), 2, 64, 1024)
+    index = torch.zeros(5, dtype=torch.int32, device="cuda")
+    off = torch.tensor([0, 2, 5], dtype=torch.int32, device="cuda")
+    assert not g.gemm_f16_grouped_nt(h, b, off, index=index).any()
+    assert not g.gemm_f16_grouped_nt(h[:, :7].contiguous(), b[:, :, :7].contiguous(), off, index=index).any()
+
+
 def test_empty_extents():
     off = torch.zeros(3, dtype=torch.int32, device="cuda")
     h = lambda *s: torch.zeros(*s, dtype=torch.float16, device="cuda")  # noqa: E731
@@ -234,7 +289,9 @@ ADAPTERS = [
     (1, 4, 16, 256, 256, False), (1, 1, 1, 8, 8, False), (3, 2, 4, 100, 77, False), (48, 32, 16, 512, 512, False),
     (16, 3, 12, 130, 136, False), (17, 5, 24, 264, 1000, True), (64, 64, 8, 128, 4096, False), (130, 6, 33, 300, 129, True),
     (200, 8, 64, 384, 256, False), (600, 5, 64, 520, 328, True), (300, 2, 100, 200, 64, True), (1000, 16, 16, 256, 128, False),
-    (90, 3, 7, 61, 515, False), (2500, 4, 32, 256, 264, True),
+    (90, 3, 7, 61, 515, False), (2500, 4, 32, 256, 264, True), (4096, 8, 64, 1024, 1024, True), (700, 64, 16, 512, 512, False),
+    (65, 2, 160, 300, 4096, False), (33, 3, 9, 100, 7, False), (130, 3, 9, 100, 5, False), (64, 4, 16, 2048, 9000, False),
+    (300, 130, 8, 128, 256, False),
 ]
 
 
