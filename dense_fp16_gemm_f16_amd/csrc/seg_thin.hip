@@ -158,7 +158,7 @@ __global__ __launch_bounds__(kThinWaves *kWave) void seg_thin_kernel(const SegPa
 //  * h = scale_s x D_s^T: 16 ranks of an adapter and a slice of K a
 //    workgroup, by thin_rows.
 constexpr int kFewWaves = 4, kFewCols = 16 * kFewWaves, kFewSteps = 16, kFewK = 32 * kFewSteps;
-constexpr int kFewPitch = kFewK * 2 + 16;  // bytes of a row of x in LDS: 16 rows at one chunk on 16 banks of 16 bytes
+[[maybe_unused]] constexpr int kFewPitch = kFewK * 2 + 16;  // bytes of a row of x in LDS: 16 rows at one chunk on 16 banks of 16 bytes
 
 struct FewParams {
     SegParams main, down;

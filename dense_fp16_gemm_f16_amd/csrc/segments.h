@@ -382,9 +382,7 @@ struct LoraWalk {
 //
 // Two LDS stages.  h's K-tile comes straight into the other stage under the
 // MFMAs of this one; U_s comes through registers two K-tiles ahead, and is
-// split and written an element at a time between the MFMAs.  (Through
-// registers one K-tile ahead, with h in fp32 and K's slices of it summed
-// here, each K-tile waited 3 us for its loads.)
+// split and written an element at a time between the MFMAs.
 template <class C, bool RANK4>
 __device__ __forceinline__ bool lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *smem, int *votes, const SegParams &p,
                                            LoraWalk w, int row0, int valid, int n0, int tid, int lane, int wm, int wn) {

@@ -16,12 +16,9 @@ status of the library raises ``GemmError``.
 """
 from __future__ import annotations
 
-import contextlib
 import functools
 
 import dense_fp16_gemm_f16_amd as _g
-
-_HERE = contextlib.nullcontext()
 
 
 def _operand(name, t, dtype, shape, device):
@@ -37,29 +34,30 @@ def _operand(name, t, dtype, shape, device):
     raise ValueError(f"{name} must be contiguous (row-major)")
 
 
-def _gpu(name, t):
+def _first(name, t, dtype):
+    """The device of a call: that of its first operand, which must be on a GPU."""
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
     if not t.is_cuda:
         raise ValueError(f"{name} must be on a GPU")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous (row-major)")
     return t.device
 
 
-def _on(device, stream):
-    """(context, stream handle): allocations inside the context belong to the stream."""
+def _launch(device, stream, call):
+    """call(stream handle) with that stream current, so that what it allocates
+    belongs to the stream."""
     import torch
 
     if stream is not None:
-        return torch.cuda.stream(stream), stream.cuda_stream or None
-    handle = torch._C._cuda_getCurrentRawStream(device.index)
-    return (_HERE if torch.cuda.current_device() == device.index else torch.cuda.device(device)), handle or None
-
-
-def _ptr(t):
-    return t.data_ptr() or None
-
-
-def _check(rc):
-    if rc != _g.OK:
-        raise _g.GemmError(rc)
+        with torch.cuda.stream(stream):
+            return call(stream.cuda_stream)
+    index = device.index
+    if torch._C._cuda_getDevice() == index:
+        return call(torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(device):
+        return call(torch._C._cuda_getCurrentRawStream(index))
 
 
 @functools.lru_cache(maxsize=1024)
@@ -68,6 +66,15 @@ def _workspace_bytes(name, *sizes):
     if size < 0:
         raise _g.GemmError(size)
     return size
+
+
+def _result(out, shape, dtype, device):
+    import torch
+
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _operand("out", out, dtype, shape, device)
+    return out
 
 
 def group_rows(ids, groups: int, *, stream=None):
@@ -82,32 +89,24 @@ def group_rows(ids, groups: int, *, stream=None):
     """
     import torch
 
-    if ids.dtype not in (torch.int32, torch.int64):
+    if ids.dtype is not torch.int32 and ids.dtype is not torch.int64:
         raise TypeError("ids must be int32 or int64")
-    if not ids.is_cuda:
-        raise ValueError("ids must be on a GPU")
-    if not ids.is_contiguous():
-        raise ValueError("ids must be contiguous")
-    rows, device = ids.numel(), ids.device
+    device, rows = _first("ids", ids, ids.dtype), ids.numel()
     size = _workspace_bytes("gemm_f16_group_rows_workspace", rows, groups)
-    context, handle = _on(device, stream)
-    with context:
+
+    def call(handle):
         order = torch.empty(rows, dtype=torch.int32, device=device)
         inverse = torch.empty(rows, dtype=torch.int32, device=device)
         offsets = torch.empty(groups + 1, dtype=torch.int32, device=device)
         ws = torch.empty(size, dtype=torch.uint8, device=device) if size else None
-        _check(_g.lib().gemm_f16_group_rows(rows, groups, _ptr(ids), ids.element_size(), _ptr(order), _ptr(inverse),
-                                            _ptr(offsets), _ptr(ws) if size else None, size, handle))
-    return order, inverse, offsets
+        rc = _g.lib().gemm_f16_group_rows(
+            rows, groups, ids.data_ptr(), ids.element_size(), order.data_ptr(), inverse.data_ptr(),
+            offsets.data_ptr(), ws.data_ptr() if size else None, size, handle)
+        if rc:
+            raise _g.GemmError(rc)
+        return order, inverse, offsets
 
-
-def _output(out, shape, dtype, device):
-    import torch
-
-    if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    _operand("out", out, dtype, shape, device)
-    return out
+    return _launch(device, stream, call)
 
 
 def _out_type(out_dtype):
@@ -118,18 +117,6 @@ def _out_type(out_dtype):
     if out_dtype is not torch.float16 and out_dtype is not torch.float32:
         raise TypeError("out_dtype must be float16 or float32")
     return out_dtype
-
-
-def _pair(a, b, b_dims, what):
-    import torch
-
-    if a.dim() != 2 or b.dim() != b_dims:
-        raise ValueError("expected " + what)
-    if a.dtype is not torch.float16:
-        raise TypeError("a must be float16")
-    device = _gpu("a", a)
-    _operand("a", a, torch.float16, a.shape, device)
-    return device
 
 
 def gemm_f16_grouped_nt(a, b, offsets, *, index=None, fan: int = 1, out_dtype=None, out=None, stream=None):
@@ -144,20 +131,26 @@ def gemm_f16_grouped_nt(a, b, offsets, *, index=None, fan: int = 1, out_dtype=No
     import torch
 
     dtype = _out_type(out_dtype)
-    device = _pair(a, b, 3, "a [rows,K] and b [groups,N,K]")
+    if a.dim() != 2 or b.dim() != 3:
+        raise ValueError("expected a [rows,K] and b [groups,N,K]")
+    device = _first("a", a, torch.float16)
     (a_rows, k), (groups, n, _) = a.shape, b.shape
     rows = a_rows if index is None else index.numel()
     _operand("b", b, torch.float16, (groups, n, k), device)
     _operand("offsets", offsets, torch.int32, (groups + 1,), device)
     if index is not None:
         _operand("index", index, torch.int32, (rows,), device)
-    context, handle = _on(device, stream)
-    with context:
-        out = _output(out, (rows, n), dtype, device)
-        _check(_g.lib().gemm_f16_grouped_nt(rows, groups, n, k, _ptr(a), a_rows, _ptr(b), _ptr(offsets),
-                                            None if index is None else _ptr(index), fan, _ptr(out),
-                                            dtype is torch.float32, handle))
-    return out
+
+    def call(handle):
+        c = _result(out, (rows, n), dtype, device)
+        rc = _g.lib().gemm_f16_grouped_nt(
+            rows, groups, n, k, a.data_ptr(), a_rows, b.data_ptr(), offsets.data_ptr(),
+            None if index is None else index.data_ptr(), fan, c.data_ptr(), dtype is torch.float32, handle)
+        if rc:
+            raise _g.GemmError(rc)
+        return c
+
+    return _launch(device, stream, call)
 
 
 def gemm_f16_grouped_nn(a, b, offsets, *, out_dtype=None, out=None, stream=None):
@@ -167,16 +160,22 @@ def gemm_f16_grouped_nn(a, b, offsets, *, out_dtype=None, out=None, stream=None)
     import torch
 
     dtype = _out_type(out_dtype)
-    device = _pair(a, b, 3, "a [rows,K] and b [groups,K,N]")
+    if a.dim() != 2 or b.dim() != 3:
+        raise ValueError("expected a [rows,K] and b [groups,K,N]")
+    device = _first("a", a, torch.float16)
     (rows, k), (groups, _, n) = a.shape, b.shape
     _operand("b", b, torch.float16, (groups, k, n), device)
     _operand("offsets", offsets, torch.int32, (groups + 1,), device)
-    context, handle = _on(device, stream)
-    with context:
-        out = _output(out, (rows, n), dtype, device)
-        _check(_g.lib().gemm_f16_grouped_nn(rows, groups, n, k, _ptr(a), _ptr(b), _ptr(offsets), _ptr(out),
-                                            dtype is torch.float32, handle))
-    return out
+
+    def call(handle):
+        c = _result(out, (rows, n), dtype, device)
+        rc = _g.lib().gemm_f16_grouped_nn(
+            rows, groups, n, k, a.data_ptr(), b.data_ptr(), offsets.data_ptr(), c.data_ptr(), dtype is torch.float32, handle)
+        if rc:
+            raise _g.GemmError(rc)
+        return c
+
+    return _launch(device, stream, call)
 
 
 def gemm_f16_grouped_tn(a, b, offsets, *, out_dtype=None, out=None, stream=None):
@@ -187,16 +186,22 @@ def gemm_f16_grouped_tn(a, b, offsets, *, out_dtype=None, out=None, stream=None)
     import torch
 
     dtype = _out_type(out_dtype)
-    device = _pair(a, b, 2, "a [rows,K] and b [rows,N]")
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError("expected a [rows,K] and b [rows,N]")
+    device = _first("a", a, torch.float16)
     (rows, k), n, groups = a.shape, b.shape[1], offsets.numel() - 1
     _operand("b", b, torch.float16, (rows, n), device)
     _operand("offsets", offsets, torch.int32, (groups + 1,), device)
-    context, handle = _on(device, stream)
-    with context:
-        out = _output(out, (groups, k, n), dtype, device)
-        _check(_g.lib().gemm_f16_grouped_tn(rows, groups, n, k, _ptr(a), _ptr(b), _ptr(offsets), _ptr(out),
-                                            dtype is torch.float32, handle))
-    return out
+
+    def call(handle):
+        c = _result(out, (groups, k, n), dtype, device)
+        rc = _g.lib().gemm_f16_grouped_tn(
+            rows, groups, n, k, a.data_ptr(), b.data_ptr(), offsets.data_ptr(), c.data_ptr(), dtype is torch.float32, handle)
+        if rc:
+            raise _g.GemmError(rc)
+        return c
+
+    return _launch(device, stream, call)
 
 
 def gemm_f16_lora_nt(x, w, down, up, ids, order, offsets, scale=None, *, out=None, stream=None):
@@ -211,9 +216,8 @@ def gemm_f16_lora_nt(x, w, down, up, ids, order, offsets, scale=None, *, out=Non
 
     if x.dim() != 2 or w.dim() != 2 or down.dim() != 3:
         raise ValueError("expected x [rows,K], w [N,K] and down [adapters,rank,K]")
-    device = _gpu("x", x)
+    device = _first("x", x, torch.float16)
     (rows, k), n, (adapters, rank, _) = x.shape, w.shape[0], down.shape
-    _operand("x", x, torch.float16, (rows, k), device)
     _operand("w", w, torch.float16, (n, k), device)
     _operand("down", down, torch.float16, (adapters, rank, k), device)
     _operand("up", up, torch.float16, (adapters, n, rank), device)
@@ -223,11 +227,16 @@ def gemm_f16_lora_nt(x, w, down, up, ids, order, offsets, scale=None, *, out=Non
     if scale is not None:
         _operand("scale", scale, torch.float32, (adapters,), device)
     size = _workspace_bytes("gemm_f16_lora_workspace", rows, n, k, adapters, rank)
-    context, handle = _on(device, stream)
-    with context:
-        out = _output(out, (rows, n), torch.float16, device)
+
+    def call(handle):
+        y = _result(out, (rows, n), torch.float16, device)
         ws = torch.empty(size, dtype=torch.uint8, device=device)
-        _check(_g.lib().gemm_f16_lora_nt(rows, n, k, adapters, rank, _ptr(x), _ptr(w), _ptr(down), _ptr(up),
-                                         _ptr(ids), _ptr(order), _ptr(offsets), None if scale is None else _ptr(scale),
-                                         _ptr(out), _ptr(ws), size, handle))
-    return out
+        rc = _g.lib().gemm_f16_lora_nt(
+            rows, n, k, adapters, rank, x.data_ptr(), w.data_ptr(), down.data_ptr(), up.data_ptr(), ids.data_ptr(),
+            order.data_ptr(), offsets.data_ptr(), None if scale is None else scale.data_ptr(), y.data_ptr(),
+            ws.data_ptr(), size, handle)
+        if rc:
+            raise _g.GemmError(rc)
+        return y
+
+    return _launch(device, stream, call)
