@@ -61,6 +61,8 @@ EXPORTS = (
     "gemm_f16_grouped_nt",
     "gemm_f16_grouped_nn",
     "gemm_f16_grouped_tn",
+    "gemm_f16_grouped_tn_workspace",
+    "gemm_f16_grouped_tn_ws",
     "gemm_f16_lora_nt",
     "gemm_f16_lora_workspace",
 )
@@ -122,6 +124,10 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     for f in (L.gemm_f16_grouped_nn, L.gemm_f16_grouped_tn):
         f.argtypes = [i64, i64, i64, i64, p, p, p, p, i32, p]
         f.restype = ctypes.c_int
+    L.gemm_f16_grouped_tn_ws.argtypes = [i64, i64, i64, i64, p, p, p, p, i32, p, i64, p]
+    L.gemm_f16_grouped_tn_ws.restype = ctypes.c_int
+    L.gemm_f16_grouped_tn_workspace.argtypes = [i64, i64, i64, i64]
+    L.gemm_f16_grouped_tn_workspace.restype = i64
     L.gemm_f16_lora_nt.argtypes = [i64, i64, i64, i64, i64, p, p, p, p, p, p, p, p, p, p, i64, p]
     L.gemm_f16_lora_nt.restype = ctypes.c_int
     L.gemm_f16_lora_workspace.argtypes = [i64, i64, i64, i64, i64]

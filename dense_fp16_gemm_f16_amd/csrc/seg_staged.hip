@@ -27,8 +27,8 @@ hipError_t launch_seg_staged(int kind, bool f32, bool lora, SegParams p, hipStre
             return f32 ? launch_seg(seg_staged_kernel<kSegNN, C, true, false>, grid, C::kThreads, s, p)
                        : launch_seg(seg_staged_kernel<kSegNN, C, false, false>, grid, C::kThreads, s, p);
         default:
-            return f32 ? launch_seg(seg_staged_kernel<kSegTN, C, true, false>, grid, C::kThreads, s, p)
-                       : launch_seg(seg_staged_kernel<kSegTN, C, false, false>, grid, C::kThreads, s, p);
+            return f32 ? launch_seg(seg_staged_kernel<kSegTN, C, true, false>, grid, C::kThreads, s, p, p.splits)
+                       : launch_seg(seg_staged_kernel<kSegTN, C, false, false>, grid, C::kThreads, s, p, p.splits);
     }
 }
 

@@ -31,10 +31,14 @@ struct SegParams {
     int32_t rows, groups, n, k, fan;
     int32_t num_m;          // TN: tiles along k; otherwise the most row tiles there can be
     int32_t num_n;          // tiles along n
+    // TN: each segment's rows in `splits` parts of whole K-tiles, part s in
+    // fp32 at c + s part_elems (1: C itself)
+    int32_t splits;
+    int64_t part_elems;
     // low-rank adapters (kLora kernels): rows sorted by adapter, row r of
     // C and A is order[r]
     const int32_t *order;
-    const float *h;         // up to kLoraFewRows rows: [h_parts][rows, h_ld] fp32, whose sum is scale_s (x D_s^T)
+    const float *h;         // TN: the parts; adapters: up to kLoraFewRows rows: [h_parts][rows, h_ld] fp32, whose sum is scale_s (x D_s^T)
     const char *h_pairs;    // more rows: rows of h_ld values, zeros past the rank (store_pairs)
     const _Float16 *up;     // [adapters, n, rank]
     const float *scale;     // [adapters]: multiplies the rows of h (null: 1)
@@ -45,6 +49,17 @@ struct SegParams {
 // Segment bounds, clamped so that any content of offsets stays in range.
 __device__ __forceinline__ int seg_bound(const int32_t *offsets, int g, int rows) {
     return g <= 0 ? 0 : min(max(offsets[g], 0), rows);
+}
+
+// Rows [lo, lo + count) of part s of segment g (TN).
+struct SegPart {
+    int lo, count;
+};
+
+__device__ __forceinline__ SegPart seg_part(const SegParams &p, int g, int s, int bk) {
+    const int lo = seg_bound(p.offsets, g, p.rows), len = max(seg_bound(p.offsets, g + 1, p.rows) - lo, 0);
+    const int part = ((len + bk - 1) / bk + p.splits - 1) / p.splits * bk, at = min(s * part, len);
+    return {lo + at, min(part, len - at)};
 }
 
 struct SegTile {
@@ -571,14 +586,15 @@ __global__ __launch_bounds__(C::kThreads) void seg_staged_kernel(const SegParams
 
     OpA opa;
     OpB opb;
-    int g, row0, valid, n0, kt_count;
+    int g, row0, valid, n0, kt_count, split = 0;
     if constexpr (KIND == kSegTN) {
         const uint32_t per = (uint32_t)p.num_m * (uint32_t)p.num_n;
         g = (int)(blockIdx.x / per);
+        split = (int)blockIdx.y;
         const TileCoord tc = tile_coord<uint32_t>(blockIdx.x % per, p.num_m, p.num_n, 4, false);
         const int m0 = (int)tc.m_block * C::BM;
         n0 = (int)tc.n_block * C::BN;
-        const int lo = seg_bound(p.offsets, g, p.rows), cnt = max(seg_bound(p.offsets, g + 1, p.rows) - lo, 0);
+        const auto [lo, cnt] = seg_part(p, g, split, C::BK);
         row0 = m0;
         valid = min(C::BM, p.k - m0);
         kt_count = (cnt + C::BK - 1) / C::BK;
@@ -689,7 +705,7 @@ __global__ __launch_bounds__(C::kThreads) void seg_staged_kernel(const SegParams
         if (wild) lora_wild<C>(p, row0, valid, n0, tid, lane);
     } else if constexpr (KIND == kSegTN) {
         using Out = std::conditional_t<F32, float, _Float16>;
-        Out *c = static_cast<Out *>(p.c) + (int64_t)g * p.k * p.n;
+        Out *c = static_cast<Out *>(p.c) + split * p.part_elems + (int64_t)g * p.k * p.n;
         seg_store<C, F32, kWaveBytes>(acc, stg, c, valid, p.n, n0, wm, wn, lane, [&](int r) { return row0 + r; });
     } else {
         seg_store<C, F32, kWaveBytes>(acc, stg, p.c, valid, p.n, n0, wm, wn, lane, [&](int r) { return row0 + r; });
@@ -697,10 +713,11 @@ __global__ __launch_bounds__(C::kThreads) void seg_staged_kernel(const SegParams
 }
 
 template <class Kernel>
-inline hipError_t launch_seg(Kernel kernel, int64_t grid, int threads, hipStream_t stream, const SegParams &p) {
+inline hipError_t launch_seg(Kernel kernel, int64_t grid, int threads, hipStream_t stream, const SegParams &p,
+                             int parts = 1) {
     if (grid <= 0) return hipSuccess;
     void *args[] = {const_cast<SegParams *>(&p)};
-    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3((unsigned)grid), dim3((unsigned)threads), args,
+    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3((unsigned)grid, (unsigned)parts), dim3((unsigned)threads), args,
                            0, stream);
 }
 
@@ -743,6 +760,9 @@ hipError_t launch_lora_down_thin(const SegParams &p, hipStream_t s);
 int lora_few_parts(int64_t k);
 int lora_few_h_parts(int64_t k);
 hipError_t launch_lora_few(const SegParams &p, const SegParams &down, float *sums, const int32_t *ids, hipStream_t s);
+
+// C = the sum of the parts at p.h, in their order
+hipError_t launch_seg_join(bool f32, const SegParams &p, hipStream_t s);
 
 hipError_t launch_seg_staged(int kind, bool f32, bool lora, SegParams p, hipStream_t s);
 

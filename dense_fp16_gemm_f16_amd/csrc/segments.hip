@@ -12,6 +12,8 @@
 namespace gemm_f16 {
 
 constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxK = int64_t(1) << 22, kMaxNMajor = int64_t(1) << 25;
+// gfx950's CUs (the sizes alone say what workspace a call takes), and the most parts
+constexpr int kTnCus = 256, kTnSplits = 64;
 constexpr int64_t kMaxElems = int64_t(1) << 47, kMaxGroups = int64_t(1) << 20;
 
 // One buffer of a call, for the checks on pointers.
@@ -85,6 +87,7 @@ static bool can_walk(int kind, int bm, int bn, bool f32, const SegParams &p, int
 struct SegPlan {
     int tile;
     bool walk;
+    double us;  // modelled
 };
 
 // The plan with the smallest modelled time (us)
@@ -136,8 +139,7 @@ static SegPlan pick_plan(int kind, bool f32, const SegParams &p, int cus) {
     const Cand *first = kind == kSegNT ? nt : kind == kSegNN ? nn : tn;
     const Cand *last = kind == kSegNT ? std::end(nt) : kind == kSegNN ? std::end(nn) : std::end(tn);
     const int64_t segments = std::min<int64_t>(p.groups, p.rows);
-    SegPlan best = {kSeg128x128, false};
-    double best_t = 1e300;
+    SegPlan best = {kSeg128x128, false, 1e300};
     for (const Cand *c = first; c != last; ++c) {
         if (p.order && c->id >= kSegRing) continue;  // no adapters there
         double m_tiles, k_tiles;
@@ -164,13 +166,44 @@ static SegPlan pick_plan(int kind, bool f32, const SegParams &p, int cus) {
         } else {
             t = c->c + c->a * std::ceil(share) * k_tiles + c->b * share;
         }
-        if (t < best_t) {
-            best_t = t;
-            best = {c->id, walk};
-        }
+        if (t < best.us) best = {c->id, walk, t};
     }
     return best;
 }
+
+// Parts of each segment's rows for a TN product whose 128 x 128 tiles leave
+// CUs idle (1: not split): the parts' sums go to the workspace in fp32 and
+// a second launch adds them, in their order.  The model of pick_plan with the
+// longest segment, taken as twice the mean, as the least time of a round, and
+// the second launch's.  (16384 rows in one segment of 512 x 512, 16 tiles:
+// 159 us unsplit, 24 in 16 parts; 4 uneven segments of 1024 x 768, 192 tiles:
+// 76 and, in 2 parts, 53; 1024 rows of 512 x 512: 10.7 and 12, not split.)
+static int tn_splits(int64_t rows, int64_t groups, int64_t n, int64_t k) {
+    const int64_t tiles = groups * cdiv64(n, 128) * cdiv64(k, 128);
+    if (tiles >= kTnCus || rows < 4 * 64) return 1;
+    const int64_t longest = groups > 1 ? rows * 2 : rows;  // times groups
+    const int64_t mean_kt = cdiv64(cdiv64(rows, groups), 64), long_kt = cdiv64(cdiv64(longest, groups), 64);
+    SegParams p = {};
+    p.rows = (int32_t)std::min<int64_t>(longest, kMaxRows);
+    p.groups = (int32_t)groups;
+    p.n = (int32_t)n;
+    p.k = (int32_t)k;
+    double best = pick_plan(kSegTN, true, p, kTnCus).us;
+    int splits = 1;
+    for (int s = 2; s <= kTnSplits && s <= long_kt && tiles * s <= 2 * kTnCus; ++s) {
+        const double share = (double)(tiles * s) / kTnCus;
+        const double round = std::max((double)cdiv64(long_kt, s), std::ceil(share) * (double)cdiv64(mean_kt, s));
+        const double t = 4.76 + 0.52 * round + 3.95 * share + 7.0 + 6.0 * share;
+        if (t < best) {
+            best = t;
+            splits = s;
+        }
+    }
+    return splits;
+}
+
+// fp32 elements of a part: whole 16-byte chunks.
+static int64_t tn_part_elems(int64_t groups, int64_t n, int64_t k) { return cdiv64(groups * n * k, 4) * 4; }
 
 // Whether a grouped NT product takes the few-row kernel: up to 16 rows per
 // segment, and too few 32 x 64 tiles to fill the CUs, where its waves'
@@ -190,7 +223,7 @@ static bool few_rows(const SegParams &p, bool direct) {
 
 static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a, int64_t a_rows,
                    const void *b, const int32_t *offsets, const int32_t *index, int64_t fan, void *c, int32_t out_f32,
-                   void *stream) {
+                   void *stream, void *workspace = nullptr, int64_t workspace_bytes = 0, int splits = 1) {
     int rc = check_grouped(kind, rows, groups, n, k);
     if (rc != GEMM_F16_OK) return rc;
     if (a_rows < 0 || a_rows >= kMaxRows || fan < 1 || fan >= kMaxRows || out_f32 < 0 || out_f32 > 1)
@@ -199,7 +232,10 @@ static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k,
     const int64_t out = kind == kSegTN ? groups * n * k : rows * n;
     if (out == 0) return GEMM_F16_OK;
     const int es = out_f32 ? 4 : 2;
+    const int64_t part = tn_part_elems(groups, n, k), need = splits > 1 ? splits * part * 4 : 0;
+    if (workspace_bytes < need) return GEMM_F16_EINVAL;
     const Buffer bufs[] = {{c, out * es, es, true},
+                           {workspace, need, 16, true},
                            {a, a_rows * k * 2, 2, false},
                            {b, (kind == kSegTN ? rows * n : groups * n * k) * 2, 2, false},
                            {offsets, (groups + 1) * 4, 4, false},
@@ -222,10 +258,23 @@ static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k,
     p.n = (int32_t)n;
     p.k = (int32_t)k;
     p.fan = (int32_t)fan;
+    p.splits = 1;
     const bool direct = direct_rows(kind, p);
     // (the few-row kernel reads some row of A even for an index outside it)
     if (kind == kSegNT && a_rows > 0 && few_rows(p, direct))
         return status(launch_seg_thin(out_f32 != 0, p, (hipStream_t)stream));
+    if (splits > 1) {
+        SegParams q = p;
+        q.c = workspace;
+        q.splits = splits;
+        q.part_elems = part;
+        rc = status(direct ? launch_seg_tn(kSeg128x128, true, q, (hipStream_t)stream)
+                           : launch_seg_staged(kind, true, false, q, (hipStream_t)stream));
+        if (rc != GEMM_F16_OK) return rc;
+        q.c = c;
+        q.h = static_cast<const float *>(workspace);
+        return status(launch_seg_join(out_f32 != 0, q, (hipStream_t)stream));
+    }
     if (direct) {
         const SegPlan plan = pick_plan(kind, out_f32 != 0, p, cus);
         const int tile = plan.tile;
@@ -316,6 +365,22 @@ int gemm_f16_grouped_nn(int64_t rows, int64_t groups, int64_t n, int64_t k, cons
 int gemm_f16_grouped_tn(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a, const void *b,
                         const int32_t *offsets, void *c, int32_t out_f32, void *stream) {
     return grouped(kSegTN, rows, groups, n, k, a, rows, b, offsets, nullptr, 1, c, out_f32, stream);
+}
+
+int64_t gemm_f16_grouped_tn_workspace(int64_t rows, int64_t groups, int64_t n, int64_t k) {
+    const int rc = check_grouped(kSegTN, rows, groups, n, k);
+    if (rc != GEMM_F16_OK) return rc;
+    const int splits = tn_splits(rows, groups, n, k);
+    return splits > 1 ? splits * tn_part_elems(groups, n, k) * 4 : 0;
+}
+
+int gemm_f16_grouped_tn_ws(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a, const void *b,
+                           const int32_t *offsets, void *c, int32_t out_f32, void *workspace, int64_t workspace_bytes,
+                           void *stream) {
+    const int rc = check_grouped(kSegTN, rows, groups, n, k);
+    if (rc != GEMM_F16_OK) return rc;
+    return grouped(kSegTN, rows, groups, n, k, a, rows, b, offsets, nullptr, 1, c, out_f32, stream, workspace,
+                   workspace_bytes, tn_splits(rows, groups, n, k));
 }
 
 int64_t gemm_f16_lora_workspace(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64_t rank) {

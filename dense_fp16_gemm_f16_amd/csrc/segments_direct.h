@@ -39,6 +39,7 @@ __device__ __forceinline__ int seg_by_size(const SegParams &p, int rank, int lan
 template <int KIND, class C, bool LORA>
 struct SegWork {
     int g, row0, valid, n0, k_count;  // k_count: length of the contraction
+    int lo, split;                    // TN: its first row, its part
     bool live;
 
     // false: past the last tile
@@ -48,11 +49,14 @@ struct SegWork {
             const uint32_t per = (uint32_t)p.num_m * (uint32_t)p.num_n;
             // long segments first, so that the last tiles to start are short
             g = seg_by_size(p, (int)(pid / per), lane);
+            split = (int)blockIdx.y;
             const TileCoord tc = tile_coord<uint32_t>(pid % per, p.num_m, p.num_n, 4, true);
             row0 = (int)tc.m_block * C::BM;
             n0 = (int)tc.n_block * C::BN;
             valid = min(C::BM, p.k - row0);
-            k_count = max(seg_bound(p.offsets, g + 1, p.rows) - seg_bound(p.offsets, g, p.rows), 0);
+            const SegPart part = seg_part(p, g, split, C::BK);
+            lo = part.lo;
+            k_count = part.count;
             return true;
         }
         TileCoord tc;
@@ -108,9 +112,8 @@ __device__ __forceinline__ void seg_tile(const SegParams &p, char *smem, const S
     OpB opb;
     const _Float16 *a_tile = p.a, *b_tile = p.b;  // operands read along N: the tile's first element
     if constexpr (KIND == kSegTN) {
-        const int64_t lo = seg_bound(p.offsets, w.g, p.rows);
-        a_tile = p.a + lo * p.k + w.row0;
-        b_tile = p.b + lo * p.n + w.n0;
+        a_tile = p.a + (int64_t)w.lo * p.k + w.row0;
+        b_tile = p.b + (int64_t)w.lo * p.n + w.n0;
         opa.init(p.a, 0, p.k, w.k_count, kt_count, wave, lane, wm * TM, 0);
         opb.init(p.b, 0, p.n, w.k_count, kt_count, wave, lane, wn * TN, kLdsB);
     } else {
@@ -276,7 +279,7 @@ __device__ __forceinline__ void seg_tile(const SegParams &p, char *smem, const S
         if (wild) lora_wild<C>(p, row0, valid, n0, t, l);
     } else {
         using Out = std::conditional_t<F32, float, _Float16>;
-        Out *c = static_cast<Out *>(p.c) + (KIND == kSegTN ? (int64_t)w.g * p.k * p.n : 0);
+        Out *c = static_cast<Out *>(p.c) + (KIND == kSegTN ? w.split * p.part_elems + (int64_t)w.g * p.k * p.n : 0);
         seg_store<C, F32, kWaveBytes>(acc, stg, c, valid, p.n, n0, wm, wn, l, [&](int r) { return row0 + r; });
     }
 }
@@ -467,11 +470,12 @@ hipError_t launch_seg_tile(SegParams p, bool f32, hipStream_t s) {
         grid = m_tiles * p.num_n;
     }
     if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    const int parts = KIND == kSegTN ? p.splits : 1;
     if constexpr (LORA)
         return launch_seg(seg_tile_kernel<KIND, C, false, LORA>, grid, C::kThreads, s, p);
     else
-        return f32 ? launch_seg(seg_tile_kernel<KIND, C, true, LORA>, grid, C::kThreads, s, p)
-                   : launch_seg(seg_tile_kernel<KIND, C, false, LORA>, grid, C::kThreads, s, p);
+        return f32 ? launch_seg(seg_tile_kernel<KIND, C, true, LORA>, grid, C::kThreads, s, p, parts)
+                   : launch_seg(seg_tile_kernel<KIND, C, false, LORA>, grid, C::kThreads, s, p, parts);
 }
 
 }  // namespace gemm_f16

@@ -192,11 +192,19 @@ def gemm_f16_grouped_tn(a, b, offsets, *, out_dtype=None, out=None, stream=None)
     (rows, k), n, groups = a.shape, b.shape[1], offsets.numel() - 1
     _operand("b", b, torch.float16, (rows, n), device)
     _operand("offsets", offsets, torch.int32, (groups + 1,), device)
+    size = _workspace_bytes("gemm_f16_grouped_tn_workspace", rows, groups, n, k)
 
     def call(handle):
         c = _result(out, (groups, k, n), dtype, device)
-        rc = _g.lib().gemm_f16_grouped_tn(
-            rows, groups, n, k, a.data_ptr(), b.data_ptr(), offsets.data_ptr(), c.data_ptr(), dtype is torch.float32, handle)
+        if size:
+            ws = torch.empty(size, dtype=torch.uint8, device=device)
+            rc = _g.lib().gemm_f16_grouped_tn_ws(
+                rows, groups, n, k, a.data_ptr(), b.data_ptr(), offsets.data_ptr(), c.data_ptr(),
+                dtype is torch.float32, ws.data_ptr(), size, handle)
+        else:
+            rc = _g.lib().gemm_f16_grouped_tn(
+                rows, groups, n, k, a.data_ptr(), b.data_ptr(), offsets.data_ptr(), c.data_ptr(),
+                dtype is torch.float32, handle)
         if rc:
             raise _g.GemmError(rc)
         return c

@@ -260,6 +260,17 @@ int gemm_f16_grouped_tn(int64_t rows, int64_t groups, int64_t n, int64_t k, cons
                         void *stream);
 
 /*
+ * grouped_tn with a workspace: where C has few tiles and the segments many
+ * rows, each segment's rows are split among workgroups, whose fp32 sums meet
+ * in the workspace and are added in their order.  The workspace is at most
+ * 512 tiles of 64 KB; where its size is 0, the call is gemm_f16_grouped_tn.
+ */
+int gemm_f16_grouped_tn_ws(int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a,
+                           const void *b, const int32_t *offsets, void *c, int32_t out_f32,
+                           void *workspace, int64_t workspace_bytes, void *stream);
+int64_t gemm_f16_grouped_tn_workspace(int64_t rows, int64_t groups, int64_t n, int64_t k);
+
+/*
  * A projection shared by requests that each have a low-rank adapter of
  * their own (or none):
  *

@@ -51,6 +51,31 @@ def test_grouped_gradient_checks(kind, change, expect):
     assert call(v["rows"], v["groups"], v["n"], v["k"], v["a"], v["b"], v["offsets"], v["c"], v["f32"], None) == expect
 
 
+def _tn_ws(rows=9000, groups=2, n=64, k=128, a=A, b=B, offsets=O, c=C, f32=0, ws=W, size=BIG):
+    return g.lib().gemm_f16_grouped_tn_ws(rows, groups, n, k, a, b, offsets, c, f32, ws, size, None)
+
+
+@pytest.mark.parametrize("change, expect", [
+    ({"rows": -1}, g.EINVAL), ({"groups": 0}, g.EINVAL), ({"n": 1 << 25}, g.EINVAL), ({"f32": 2}, g.EINVAL),
+    ({"size": 4}, g.EINVAL), ({"ws": None}, g.ENULL), ({"a": None}, g.ENULL), ({"ws": W + 4}, g.EALIGN),
+    ({"c": W}, g.EOVERLAP), ({"ws": A}, g.EOVERLAP), ({"ws": O}, g.EOVERLAP), ({"n": 0, "size": 0, "ws": None}, g.OK),
+])
+def test_grouped_tn_ws_checks(change, expect):
+    assert _tn_ws(**change) == expect
+
+
+def test_grouped_tn_workspace_sizes():
+    size = g.lib().gemm_f16_grouped_tn_workspace
+    assert size(16384, 1, 512, 512) >= 2 * 512 * 512 * 4           # few tiles, many rows: split
+    for whole in ((100, 1, 512, 512), (16384, 8, 2048, 4096), (0, 4, 64, 64), (16384, 4, 0, 64), (16384, 4, 64, 0)):
+        assert size(*whole) == 0
+    for rows in (256, 5000, (1 << 30) - 1):
+        for groups, n, k in ((1, 1, 1), (3, 61, 75), (7, 700, 500), (1 << 20, 8, 8), (1, 100000, 64)):
+            assert 0 <= size(rows, groups, n, k) <= 512 * 65536
+    for bad in ((-1, 1, 8, 8), (1 << 30, 1, 8, 8), (8, 0, 8, 8), (8, 1, 1 << 25, 8), (8, 1, 8, 1 << 22)):
+        assert size(*bad) == g.EINVAL
+
+
 @pytest.mark.parametrize("change, expect", [
     ({"rows": -1}, g.EINVAL), ({"rows": 1 << 30}, g.EINVAL), ({"groups": 0}, g.EINVAL), ({"groups": 2049}, g.EINVAL),
     ({"id_bytes": 2}, g.EINVAL), ({"size": 3}, g.EINVAL),

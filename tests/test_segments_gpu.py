@@ -134,6 +134,79 @@ def test_grouped_on_random_operands(kind, sizes, n, k, f32):
     assert ref.worst(out, want, mag * terms * 2.0**-23, dtype) <= 1.0
 
 
+# ---- weight gradients of few tiles: each segment's rows in parts ------------------
+
+SPLIT = [([9000], 256, 200, 0), ([16000], 64, 64, 5), ([0, 6000, 1, 63, 3000], 136, 264, 70), ([5000, 0, 4000], 61, 75, 0),
+         ([2600, 2500], 513, 130, 3), ([64, 8000, 65], 8, 8, 0), ([3000, 900, 2000, 4000], 1024, 768, 0)]
+
+
+@pytest.mark.parametrize("poisoned", [False, True])
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("sizes, n, k, tail", SPLIT)
+def test_split_weight_gradient_is_exact(sizes, n, k, tail, f32, poisoned, monkeypatch):
+    if poisoned and not os.path.exists(build.POISON_LIB):
+        pytest.skip("libgemm_f16_poison.so is not built")
+    if poisoned:
+        monkeypatch.setattr(g, "_lib", g._declare(ctypes.CDLL(build.POISON_LIB)))
+    dtype = torch.float32 if f32 else torch.float16
+    a, b, off = _inputs("tn", sizes, n, k, _gen(n + k), tail=tail)
+    assert g.lib().gemm_f16_grouped_tn_workspace(len(a), len(sizes), n, k) >= 2 * 4 * len(sizes) * n * k
+    want, _, _ = ref.grouped("tn", a, b, off.tolist())
+    for offset in (0, 1, 8):  # the result at any alignment, nothing written beside it
+        whole = torch.full((want.numel() + 600,), 7.0, dtype=dtype, device="cuda")
+        out = whole[offset + 256:][:want.numel()].view(want.shape)
+        g.gemm_f16_grouped_tn(a, b, off, out_dtype=dtype, out=out)
+        assert torch.equal(out, want.to(dtype))
+        assert (whole[:offset + 256] == 7).all() and (whole[offset + 256 + want.numel():] == 7).all()
+
+
+@pytest.mark.parametrize("f32", [False, True])
+@pytest.mark.parametrize("n, k", [(264, 136), (75, 61)])
+def test_split_weight_gradient_on_random_operands(n, k, f32):
+    dtype = torch.float32 if f32 else torch.float16
+    a, b, off = _inputs("tn", [4000, 31, 7000], n, k, _gen(k), ref.normal)
+    want, mag, terms = ref.grouped("tn", a, b, off.tolist())
+    out = g.gemm_f16_grouped_tn(a, b, off, out_dtype=dtype)
+    assert ref.worst(out, want, mag * terms * 2.0**-23, dtype) <= 1.0
+    assert torch.equal(out, g.gemm_f16_grouped_tn(a, b, off, out_dtype=dtype))  # the same bits again
+
+
+def test_split_weight_gradient_keeps_segments_apart():
+    sizes = [3000, 5000, 2000]
+    a, b, off = _inputs("tn", sizes, 128, 72, _gen(3), tail=500)
+    want, _, _ = ref.grouped("tn", a, b, off.tolist())
+    a[3000:8000] = float("nan")
+    b[10000:] = float("inf")
+    out = g.gemm_f16_grouped_tn(a, b, off)
+    assert torch.equal(out[[0, 2]], want[[0, 2]].half()) and torch.isnan(out[1]).all()
+
+
+@pytest.mark.parametrize("offsets", [[0, 5000, 20, 9000], [0, -5, 1 << 30, 3], [7, 7, 7, 7], [9000, 6000, 3000, 0]])
+def test_split_weight_gradient_with_offsets_that_break_the_rules(offsets):
+    a, b, _ = _inputs("tn", [3000] * 3, 96, 80, _gen(1))
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    whole = torch.full((3 * 80 * 96 + 4096,), 7.0, dtype=torch.float16, device="cuda")
+    g.gemm_f16_grouped_tn(a, b, off, out=whole[2048:][:3 * 80 * 96].view(3, 80, 96))
+    assert (whole[:2048] == 7).all() and (whole[2048 + 3 * 80 * 96:] == 7).all()
+
+
+def test_split_weight_gradient_in_a_graph():
+    a, b, off = _inputs("tn", [3000, 6000], 128, 256, _gen(9))
+    g.gemm_f16_grouped_tn(a, b, off)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = g.gemm_f16_grouped_tn(a, b, off)
+    for sizes in ([3000, 6000], [0, 9000], [8999, 1], [4000, 2000]):
+        off.copy_(ref.offsets_of(sizes))
+        a.copy_(ref.eighths(_gen(sizes[0]), *a.shape))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, g.gemm_f16_grouped_tn(a, b, off))
+        want, _, _ = ref.grouped("tn", a, b, off.tolist())
+        assert torch.equal(out, want.half())
+
+
 @pytest.mark.parametrize("fan", [1, 2, 3, 8])
 @pytest.mark.parametrize("tokens, groups, n, k", [(1, 8, 64, 64), (50, 8, 136, 200), (333, 5, 257, 99), (700, 3, 256, 256),
                                                   (8, 8, 512, 2048)])
