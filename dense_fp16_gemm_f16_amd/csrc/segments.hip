@@ -98,8 +98,8 @@ struct SegPlan {
 // 0.66 of a round.  The coefficients are least-squares fits, in relative
 // error, to sweeps of every tile over 500 shapes (rows 1 to 16384, 1 to 64
 // segments, N and K from 64 to 4096, inputs cold in the caches) on MI355X.
-// On those shapes the plan's time was 1.03 (nt, nn) to 1.04 (tn) of the
-// fastest tile's in the geometric mean and at most 1.5 of it.  With tiles to
+// On 350 other shapes of that range the plan's time was 1.03 (tn) to 1.05 (nn)
+// of the fastest tile's in the geometric mean and at most 1.7 of it.  With tiles to
 // walk, walking measured 0.88 to 0.97 of the one-tile kernel's time on most
 // shapes (nt, 256 x 128, 1 to 2 rounds: 0.91) and up to 1.15 on few.  The
 // 32-row rings serve few rows per segment, where B's bytes bound the

@@ -27,6 +27,10 @@ using TailCfg = Cfg<128, 128, 2, 2, 16>;
 //  * fp16 results: v_permlane16_swap joins two blocks' 8-byte quarters into
 //    16-byte stores, so no operand layout is bent for the stores; fp32
 //    results leave a block at a time.
+// Bound by the MFMAs at the clock that the power limit leaves: 16384 rows in
+// 8 uneven segments, 4096 x 2048, take 240-253 us (1090-1145 TFLOP/s), in equal
+// segments 196, as long as the dense kernel; the rest is half a row tile lost
+// per segment and a last round that does not fill the CUs.
 template <int KIND, class C, bool F32, int POL>
 __global__ __launch_bounds__(C::kThreads)
 __attribute__((amdgpu_waves_per_eu(C::kMinWavesPerEU, C::kMinWavesPerEU)))
