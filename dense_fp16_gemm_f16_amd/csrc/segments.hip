@@ -94,8 +94,8 @@ struct SegPlan {
 //     c + a rounds k_tiles + b tiles / cus,
 // rounds of one workgroup per CU, over the row tiles to expect (half a tile
 // more per segment than the rows fill; the sizes are on the GPU).  For the
-// walking kernels a last round in small tiles counts as 0.42 (256 x 256) or
-// 0.66 of a round.  The coefficients are least-squares fits, in relative
+// walking kernels a last round in small tiles counts as 0.42 or 0.5 (256 x
+// 256) or 0.66 of a round.  The coefficients are least-squares fits, in relative
 // error, to sweeps of every tile over 500 shapes (rows 1 to 16384, 1 to 64
 // segments, N and K from 64 to 4096, inputs cold in the caches) on MI355X.
 // On 350 other shapes of that range the plan's time was 1.03 (tn) to 1.05 (nn)
@@ -160,8 +160,7 @@ static SegPlan pick_plan(int kind, bool f32, const SegParams &p, int cus) {
         if (walk) {
             const double whole = std::floor(share), rest = share - whole;
             const bool large = c->id == kSeg256x256;
-            const double small_rounds = std::ceil(rest * (large ? 4 : 2));
-            const double tail = small_rounds <= (large ? 2 : 1) ? small_rounds * (large ? 0.42 : 0.66) : 1;
+            const double tail = rest == 0 ? 0 : large && rest <= 0.25 ? 0.42 : rest <= 0.5 ? (large ? 0.5 : 0.66) : 1;
             t = c->wc + c->wa * (whole + tail) * k_tiles + c->wb * share;
         } else {
             t = c->c + c->a * std::ceil(share) * k_tiles + c->b * share;

@@ -13,6 +13,7 @@ struct WalkTile {
 };
 
 using TailCfg = Cfg<128, 128, 2, 2, 16>;
+using HalfCfg = Cfg<128, 256, 2, 2, 16>;
 
 // As gemm_f16_stream_kernel: the K-tile stream runs on across tiles (the
 // last two K-tiles of a tile load the next tile's first two), and a tile's C
@@ -22,8 +23,8 @@ using TailCfg = Cfg<128, 128, 2, 2, 16>;
 //    a load of offsets or indices inside the K loop would wait, in order,
 //    for every operand load before it;
 //  * rows behind the last segment take two K-tiles of zeros;
-//  * a last round that would leave three of four CUs idle is cut
-//    into 128 x 128 tiles, one per workgroup (TailCfg);
+//  * a last round that would leave half the CUs idle is cut into 128 x 128
+//    tiles, or halves of a 256 x 256 tile, one per workgroup;
 //  * fp16 results: v_permlane16_swap joins two blocks' 8-byte quarters into
 //    16-byte stores, so no operand layout is bent for the stores; fp32
 //    results leave a block at a time.
@@ -45,7 +46,9 @@ void seg_walk_kernel(const SegParams p) {
     constexpr int LA = OpA::kLoads, L = OpA::kLoads + OpB::kLoads;
     constexpr int kList = kLds, kRows = kList + kWalkTiles * (int)sizeof(WalkTile);
     constexpr int kAll = kRows + (KIND == kSegNT ? kWalkTiles * C::BM * 4 : 0);
-    static_assert(seg_tile_lds<KIND, TailCfg>() <= kAll, "LDS of the last round's tiles");
+    constexpr bool kLarge = C::BM == 256 && C::BN == 256;
+    static_assert(seg_tile_lds<KIND, TailCfg>() <= kAll && (!kLarge || seg_tile_lds<KIND, HalfCfg>() <= kAll),
+                  "LDS of the last round's tiles");
     constexpr int NM = FM * FN;            // MFMAs per k step
     constexpr int U = F32 ? NM : NM / 2;   // 16-byte store units per wave and tile
     constexpr int ES = F32 ? 4 : 2;
@@ -61,18 +64,16 @@ void seg_walk_kernel(const SegParams p) {
 
     // ---- this workgroup's tiles --------------------------------------------
     int count = 0;
-    constexpr int kSub = C::BM / TailCfg::BM * (C::BN / TailCfg::BN);
     SegMap<C::BM> map;
-    int total, whole = 0, sub = (int)blockIdx.x, subs = 0;  // subs: small tiles of the last round
+    int total, whole = 0, parts = 0;  // parts: small tiles that a tile of the last round is cut into
     map.init(p, lane);
     total = whole = map.total * p.num_n;
     const int rest = total % G;
-    // rounds of small tiles instead of one of large ones: one takes some 0.42
-    // of a 256 x 256 tile's time, 0.66 of a 256 x 128's
-    if (rest * kSub <= (kSub == 4 ? 2 : 1) * G) {
-        whole = total - rest;
-        subs = rest * kSub;
-    }
+    // One takes 0.42 (a quarter) or 0.5 (half) of a 256 x 256 tile's time,
+    // 0.66 (half) of a 256 x 128's (16384 rows, 8 segments, 4096 x 2048, 80 tiles
+    // in the last round: 229 us in two rounds of quarters, 220 in halves).
+    parts = kLarge && rest * 4 <= G ? 4 : rest * 2 <= G ? 2 : 0;
+    if (parts > 0) whole = total - rest;
     for (int round = 0; round * G < whole && count < kWalkTiles; ++round) {
         const int pid = round * G + (int)blockIdx.x;
         if (pid >= whole) break;
@@ -355,19 +356,33 @@ void seg_walk_kernel(const SegParams p) {
         // before the workgroup ends
         __builtin_amdgcn_s_waitcnt(0);
     }
-    for (; sub < subs; sub += G) {
+    // at most one small tile per workgroup
+    auto small = [&](auto cfg) {
+        using T = decltype(cfg);
+        constexpr int kCols = C::BN / T::BN, kParts = C::BM / T::BM * kCols;
+        const int at = (int)blockIdx.x;
         __syncthreads();  // every wave is done with the stages
-        SegWork<KIND, TailCfg, false> w;
-        const TileCoord tc = tile_coord<uint32_t>((uint32_t)(whole + sub / kSub), map.total, p.num_n, 4, true);
+        SegWork<KIND, T, false> w;
+        const TileCoord tc = tile_coord<uint32_t>((uint32_t)(whole + at / kParts), map.total, p.num_n, 4, true);
         const SegTile st = map.find(p, (int)tc.m_block, lane);
-        const int sm = sub % kSub / (C::BN / TailCfg::BN) * TailCfg::BM;
+        const int sm = at % kParts / kCols * T::BM;
         w.g = st.g;
         w.row0 = st.row0 + sm;
-        w.valid = min(st.valid - sm, TailCfg::BM);
-        w.n0 = (int)tc.n_block * C::BN + sub % (C::BN / TailCfg::BN) * TailCfg::BN;
+        w.valid = min(st.valid - sm, T::BM);
+        w.n0 = (int)tc.n_block * C::BN + at % kCols * T::BN;
         w.live = st.g < p.groups;
         w.k_count = w.live ? p.k : 0;
-        if (w.valid > 0 && w.n0 < p.n) seg_tile<KIND, TailCfg, F32, false>(p, smem, w, tid);
+        if (w.valid > 0 && w.n0 < p.n) seg_tile<KIND, T, F32, false>(p, smem, w, tid);
+    };
+    if ((int)blockIdx.x < (total - whole) * parts) {
+        if constexpr (kLarge) {
+            if (parts == 4)
+                small(TailCfg{});
+            else
+                small(HalfCfg{});
+        } else {
+            small(TailCfg{});
+        }
     }
 #endif
 }
