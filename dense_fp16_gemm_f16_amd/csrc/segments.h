@@ -744,7 +744,7 @@ int64_t group_blocks(int64_t rows);
 hipError_t launch_group_rows(int64_t rows, int groups, const void *ids, int id_bytes, int32_t *order, int32_t *inverse,
                              int32_t *offsets, int32_t *counts, hipStream_t s);
 // Direct-to-LDS kernels (segments_direct.h), by block tile.
-enum SegTileId : int { kSeg256x256, kSeg256x128, kSeg128x256, kSeg128x128, kSeg64x128, kSeg32x128, kSegRing, kSegRing2, kSegTiles };
+enum SegTileId : int { kSeg256x256, kSeg256x128, kSeg128x256, kSeg128x128, kSeg64x128, kSeg32x128, kSegRing, kSegRing2 };
 hipError_t launch_seg_nt(int tile, bool f32, const SegParams &p, hipStream_t s);
 hipError_t launch_seg_nn(int tile, bool f32, const SegParams &p, hipStream_t s);
 hipError_t launch_seg_tn(int tile, bool f32, const SegParams &p, hipStream_t s);
