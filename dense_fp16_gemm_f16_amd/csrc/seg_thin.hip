@@ -98,6 +98,24 @@ __device__ __forceinline__ void thin_rows(const SegParams &p, floatx4 (*red)[W][
     }
 }
 
+// The segment that slot `slot` of a grid stands for, and its rows: the grid
+// has a slot for each segment, or (by_row) for each row, of which the first of
+// a segment takes it.  The fewer of the two: one row and 2^20 segments would
+// else start 2^20 slots of workgroups, more threads than a launch can have.
+// false: nothing to do.
+__device__ __forceinline__ bool thin_segment(const SegParams &p, int slot, int lane, int &g, int &lo, int &hi) {
+    g = p.by_row ? seg_of_row(p, slot, lane) : slot;
+    lo = seg_bound(p.offsets, g, p.rows);
+    hi = g < p.groups ? seg_bound(p.offsets, g + 1, p.rows) : p.rows;
+    return lo < hi && (!p.by_row || lo == slot);
+}
+
+// Slots of a grid over `groups` segments.
+static int64_t thin_slots(SegParams &p, int64_t groups) {
+    p.by_row = p.rows < groups;
+    return p.by_row ? p.rows : groups;
+}
+
 // Zeros in h's columns past the rank, up to h_ld; the others times f.
 __device__ __forceinline__ void store_h(const SegParams &p, float *h, int n, floatx4 sum, float f) {
 #pragma unroll
@@ -113,10 +131,11 @@ __global__ __launch_bounds__(kThinWaves *kWave) void seg_thin_kernel(const SegPa
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
     __shared__ floatx4 red[2][kThinWaves][kWave];
     const int tid = threadIdx.x;
-    const int g = (int)(blockIdx.x / (uint32_t)p.num_n), n0 = (int)(blockIdx.x % (uint32_t)p.num_n) * 16;
+    const int n0 = (int)(blockIdx.x % (uint32_t)p.num_n) * 16;
+    int g, lo, hi;
+    if (!thin_segment(p, (int)(blockIdx.x / (uint32_t)p.num_n), tid % kWave, g, lo, hi)) return;
     const bool live = g < p.groups;  // false: the rows behind the last segment
-    int lo = seg_bound(p.offsets, g, p.rows);
-    const int hi = live ? seg_bound(p.offsets, g + 1, p.rows) : p.rows;
+    if (DOWN && !live) return;
     const int step = DOWN ? 16 * (int)gridDim.y : 16;
     if (DOWN) lo += 16 * (int)blockIdx.y;
     if (lo >= hi) return;
@@ -166,7 +185,7 @@ constexpr int kFewWaves = 4, kFewCols = 16 * kFewWaves, kFewSteps = 16, kFewK = 
 struct FewParams {
     SegParams main, down;
     float *sums;                    // fp32 [main_parts][rows, n]
-    int32_t down_blocks;            // workgroups of h: (adapter, 16 ranks, part)
+    int32_t down_blocks;            // workgroups of h: (slot, 16 ranks, part)
     int32_t main_parts, main_steps; // slices of K, and steps of a slice (a multiple of kFewSteps)
     int32_t down_parts, down_steps;
 };
@@ -192,9 +211,9 @@ void lora_few_kernel(const FewParams fp) {
     if ((int)blockIdx.x < fp.down_blocks) {
         const SegParams &p = fp.down;
         const int part = (int)blockIdx.x % fp.down_parts, x = (int)blockIdx.x / fp.down_parts;
-        const int g = x / p.num_n, n0 = x % p.num_n * 16;
-        const int lo = seg_bound(p.offsets, g, p.rows), hi = seg_bound(p.offsets, g + 1, p.rows);
-        if (lo >= hi) return;
+        const int n0 = x % p.num_n * 16;
+        int g, lo, hi;
+        if (!thin_segment(p, x / p.num_n, lane, g, lo, hi) || g >= p.groups) return;
         const int steps = (p.k + 31) / 32, s0 = min(steps, part * fp.down_steps), s1 = min(steps, s0 + fp.down_steps);
         const float f = p.scale ? p.scale[g] : 1.0f;
         float *h = static_cast<float *>(p.c) + (int64_t)part * p.rows * p.h_ld;
@@ -322,7 +341,7 @@ __global__ __launch_bounds__(256) void lora_down_short_kernel(const SegParams p)
 template <bool F32, bool DOWN>
 static hipError_t launch_thin(SegParams p, int cols, int64_t groups, int shares, hipStream_t s) {
     p.num_n = (cols + 15) / 16;
-    const int64_t grid = groups * p.num_n;
+    const int64_t grid = thin_slots(p, groups) * p.num_n;
     if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
     int waves = 1;  // that K keeps busy in one pass
     while (waves < kThinWaves && waves * kThinSteps * 32 < p.k) waves *= 2;
@@ -373,7 +392,7 @@ hipError_t launch_lora_few(const SegParams &p, const SegParams &down, float *sum
     f.down = down;
     f.down.num_n = (down.h_ld + 15) / 16;
     f.down_parts = few_slices(p.k, kFewSteps * kFewWaves, 4, &f.down_steps);
-    f.down_blocks = down.groups * f.down.num_n * f.down_parts;
+    f.down_blocks = (int32_t)(thin_slots(f.down, down.groups) * f.down.num_n * f.down_parts);
     f.sums = sums;
     const int64_t grid = f.down_blocks + (int64_t)f.main.num_n * f.main_parts;
     if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;

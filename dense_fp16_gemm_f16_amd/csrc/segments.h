@@ -44,6 +44,7 @@ struct SegParams {
     const float *scale;     // [adapters]: multiplies the rows of h (null: 1)
     int32_t adapters, rank, h_ld;
     int32_t h_parts;
+    int32_t by_row;         // few-row kernels: workgroups per row, not per segment (thin_segment)
 };
 
 // Segment bounds, clamped so that any content of offsets stays in range.
@@ -60,6 +61,21 @@ __device__ __forceinline__ SegPart seg_part(const SegParams &p, int g, int s, in
     const int lo = seg_bound(p.offsets, g, p.rows), len = max(seg_bound(p.offsets, g + 1, p.rows) - lo, 0);
     const int part = ((len + bk - 1) / bk + p.splits - 1) / p.splits * bk, at = min(s * part, len);
     return {lo + at, min(part, len - at)};
+}
+
+// The segment that row `row` lies in; groups: it lies behind the last one.  A
+// search by the whole wave, 64 segments a step (offsets that decrease give
+// some segment).
+__device__ __forceinline__ int seg_of_row(const SegParams &p, int row, int lane) {
+    int g = 0, span = p.groups + 1;  // one of g .. g + span - 1
+    while (span > 1) {
+        const int stride = (span + kWave - 1) / kWave, at = lane * stride;
+        const uint64_t past = ~__ballot(at < span && seg_bound(p.offsets, g + at, p.rows) <= row);
+        const int step = max((past ? __builtin_ctzll(past) : kWave) - 1, 0) * stride;
+        g += step;
+        span = min(stride, span - step);
+    }
+    return g;
 }
 
 struct SegTile {
