@@ -22,7 +22,6 @@ hipError_t launch_lora_down(SegParams p, hipStream_t s) {
     p.num_n = (p.h_ld + C::BN - 1) / C::BN;
     p.num_m = (int32_t)seg_row_tiles(p.rows, p.groups, C::BM);
     const int64_t grid = (int64_t)p.num_m * p.num_n;
-    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
     return launch_seg(seg_ring_kernel<kSegNT, C, S, KG, true, true>, grid, C::kThreads * KG, s, p);
 }
 

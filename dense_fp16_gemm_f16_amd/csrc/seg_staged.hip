@@ -17,7 +17,6 @@ hipError_t launch_seg_staged(int kind, bool f32, bool lora, SegParams p, hipStre
         p.num_m = (int32_t)m_tiles;
         grid = m_tiles * p.num_n;
     }
-    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
     if (lora) return launch_seg(seg_staged_kernel<kSegNT, C, false, true>, grid, C::kThreads, s, p);
     switch (kind) {
         case kSegNT:

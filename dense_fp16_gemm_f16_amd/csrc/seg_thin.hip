@@ -131,9 +131,10 @@ __global__ __launch_bounds__(kThinWaves *kWave) void seg_thin_kernel(const SegPa
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
     __shared__ floatx4 red[2][kThinWaves][kWave];
     const int tid = threadIdx.x;
-    const int n0 = (int)(blockIdx.x % (uint32_t)p.num_n) * 16;
+    const uint32_t pid = seg_pid(p);
+    const int n0 = (int)(pid % (uint32_t)p.num_n) * 16;
     int g, lo, hi;
-    if (!thin_segment(p, (int)(blockIdx.x / (uint32_t)p.num_n), tid % kWave, g, lo, hi)) return;
+    if (!thin_segment(p, (int)(pid / (uint32_t)p.num_n), tid % kWave, g, lo, hi)) return;
     const bool live = g < p.groups;  // false: the rows behind the last segment
     if (DOWN && !live) return;
     const int step = DOWN ? 16 * (int)gridDim.y : 16;
@@ -208,9 +209,10 @@ void lora_few_kernel(const FewParams fp) {
     __shared__ __attribute__((aligned(1024))) char smem[16 * T * kFewPitch > kRed ? 16 * T * kFewPitch : kRed];
     GEMM_POISON_LDS(smem);
     const int tid = threadIdx.x, lane = tid % kWave;
-    if ((int)blockIdx.x < fp.down_blocks) {
+    const int at = (int)seg_pid(fp.main);
+    if (at < fp.down_blocks) {
         const SegParams &p = fp.down;
-        const int part = (int)blockIdx.x % fp.down_parts, x = (int)blockIdx.x / fp.down_parts;
+        const int part = at % fp.down_parts, x = at / fp.down_parts;
         const int n0 = x % p.num_n * 16;
         int g, lo, hi;
         if (!thin_segment(p, x / p.num_n, lane, g, lo, hi) || g >= p.groups) return;
@@ -226,7 +228,7 @@ void lora_few_kernel(const FewParams fp) {
         return;
     }
     const SegParams &p = fp.main;
-    const int pid = (int)blockIdx.x - fp.down_blocks, part = pid / p.num_n;
+    const int pid = at - fp.down_blocks, part = pid / p.num_n;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int n0 = pid % p.num_n * kFewCols + 16 * wave;
     const int steps = (p.k + 31) / 32, s0 = min(steps, part * fp.main_steps), s1 = min(steps, s0 + fp.main_steps);
@@ -235,8 +237,8 @@ void lora_few_kernel(const FewParams fp) {
     floatx4 acc[T];
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[t] = floatx4{};
-    for (int at = s0; at < s1; at += kFewSteps) {
-        const int count = min(s1 - at, kFewSteps), top = at + count;
+    for (int step = s0; step < s1; step += kFewSteps) {
+        const int count = min(s1 - step, kFewSteps), top = step + count;
         half8 bf[kFewSteps];
         // x: 4 T chunks of 16 bytes a thread, the first 8 of them ahead of W's
         // loads (loads return in order); rows past the last are never stored
@@ -244,7 +246,7 @@ void lora_few_kernel(const FewParams fp) {
         int4v v[X0];
         auto fetch = [&](int i) {
             const int c = i * kFewWaves * kWave + tid;
-            return few_chunk(p.a + (int64_t)min(c / 64, p.rows - 1) * p.k, 32 * at + 8 * (c % 64), p.k);
+            return few_chunk(p.a + (int64_t)min(c / 64, p.rows - 1) * p.k, 32 * step + 8 * (c % 64), p.k);
         };
         auto put = [&](int i, int4v u) {
             const int c = i * kFewWaves * kWave + tid;
@@ -253,7 +255,7 @@ void lora_few_kernel(const FewParams fp) {
 #pragma unroll
         for (int i = 0; i < X0; ++i) v[i] = fetch(i);
         thin_load(bf, wr, top, count, 32 * top > p.k, kl, p.k);
-        if (at != s0) lds_barrier();  // the last step's reads are done
+        if (step != s0) lds_barrier();  // the last step's reads are done
 #pragma unroll
         for (int i = 0; i < X0; ++i) put(i, v[i]);
 #pragma unroll
@@ -318,7 +320,7 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const SegParams p, const
 // h of K < 8, where no chunk of a row is whole: one lane per 4 values.
 __global__ __launch_bounds__(256) void lora_down_short_kernel(const SegParams p) {
     const int per = p.h_ld / 4;
-    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x, r = x / per;
+    const int64_t x = (int64_t)seg_pid(p) * 256 + threadIdx.x, r = x / per;
     const int n = (int)(x % per) * 4;
     if (r >= p.rows) return;
     int g = 0;  // the segment of row r
@@ -342,12 +344,11 @@ template <bool F32, bool DOWN>
 static hipError_t launch_thin(SegParams p, int cols, int64_t groups, int shares, hipStream_t s) {
     p.num_n = (cols + 15) / 16;
     const int64_t grid = thin_slots(p, groups) * p.num_n;
-    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
     int waves = 1;  // that K keeps busy in one pass
     while (waves < kThinWaves && waves * kThinSteps * 32 < p.k) waves *= 2;
     void *args[] = {&p};
-    return hipLaunchKernel(reinterpret_cast<const void *>(seg_thin_kernel<F32, DOWN>),
-                           dim3((unsigned)grid, (unsigned)shares), dim3((unsigned)(waves * kWave)), args, 0, s);
+    return launch_grid(reinterpret_cast<const void *>(seg_thin_kernel<F32, DOWN>), grid, shares, waves * kWave, s, args,
+                       p.first);
 }
 
 hipError_t launch_seg_thin(bool f32, const SegParams &p, hipStream_t s) {
@@ -358,7 +359,6 @@ hipError_t launch_seg_thin(bool f32, const SegParams &p, hipStream_t s) {
 hipError_t launch_lora_down_thin(const SegParams &p, hipStream_t s) {
     if (p.k < 8) {
         const int64_t grid = ((int64_t)p.rows * (p.h_ld / 4) + 255) / 256;
-        if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
         return launch_seg(lora_down_short_kernel, grid, 256, s, p);
     }
     // some 64 rows a workgroup of an even split
@@ -395,14 +395,13 @@ hipError_t launch_lora_few(const SegParams &p, const SegParams &down, float *sum
     f.down_blocks = (int32_t)(thin_slots(f.down, down.groups) * f.down.num_n * f.down_parts);
     f.sums = sums;
     const int64_t grid = f.down_blocks + (int64_t)f.main.num_n * f.main_parts;
-    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
     void *args[] = {&f};
     const int tiles = (p.rows + 15) / 16;
     const void *kernel = tiles <= 1   ? reinterpret_cast<const void *>(lora_few_kernel<1>)
                          : tiles == 2 ? reinterpret_cast<const void *>(lora_few_kernel<2>)
                          : tiles == 3 ? reinterpret_cast<const void *>(lora_few_kernel<3>)
                                       : reinterpret_cast<const void *>(lora_few_kernel<4>);
-    hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)grid), dim3(kFewWaves * kWave), args, 0, s);
+    hipError_t e = launch_grid(kernel, grid, 1, kFewWaves * kWave, s, args, f.main.first);
     if (e != hipSuccess) return e;
     SegParams j = p;
     j.h_parts = f.down_parts;

@@ -15,6 +15,8 @@
 // kernels.h.
 #pragma once
 
+#include <algorithm>
+
 #include "kernels.h"
 
 namespace gemm_f16 {
@@ -45,7 +47,11 @@ struct SegParams {
     int32_t adapters, rank, h_ld;
     int32_t h_parts;
     int32_t by_row;         // few-row kernels: workgroups per row, not per segment (thin_segment)
+    uint32_t first;         // workgroups of this grid that earlier launches hold (launch_seg)
 };
+
+// This workgroup's place in a grid of launch_seg.
+__device__ __forceinline__ uint32_t seg_pid(const SegParams &p) { return p.first + blockIdx.x; }
 
 // Segment bounds, clamped so that any content of offsets stays in range.
 __device__ __forceinline__ int seg_bound(const int32_t *offsets, int g, int rows) {
@@ -611,9 +617,9 @@ __global__ __launch_bounds__(C::kThreads) void seg_staged_kernel(const SegParams
     int g, row0, valid, n0, kt_count, split = 0;
     if constexpr (KIND == kSegTN) {
         const uint32_t per = (uint32_t)p.num_m * (uint32_t)p.num_n;
-        g = (int)(blockIdx.x / per);
+        g = (int)(seg_pid(p) / per);
         split = (int)blockIdx.y;
-        const TileCoord tc = tile_coord<uint32_t>(blockIdx.x % per, p.num_m, p.num_n, 4, false);
+        const TileCoord tc = tile_coord<uint32_t>(seg_pid(p) % per, p.num_m, p.num_n, 4, false);
         const int m0 = (int)tc.m_block * C::BM;
         n0 = (int)tc.n_block * C::BN;
         const auto [lo, cnt] = seg_part(p, g, split, C::BK);
@@ -625,7 +631,7 @@ __global__ __launch_bounds__(C::kThreads) void seg_staged_kernel(const SegParams
         opb.init(p.b + (int64_t)lo * p.n + n0, p.b + (int64_t)p.rows * p.n, p.n, cnt, p.n - n0, wave, lane,
                  wn * C::TN, kLdsB);
     } else {
-        const uint32_t pid = blockIdx.x;
+        const uint32_t pid = seg_pid(p);
         if constexpr (LORA) {
             g = 0;
             const TileCoord tc = tile_coord<uint32_t>(pid, (p.rows + C::BM - 1) / C::BM, p.num_n, 4, true);
@@ -734,13 +740,26 @@ __global__ __launch_bounds__(C::kThreads) void seg_staged_kernel(const SegParams
     }
 }
 
+// A launch holds fewer than 2^32 threads along x, and one of more loses the
+// rest without an error: such a grid (below 2^31 workgroups) goes out in
+// several launches.  args: the kernel's, with `first` inside one of them.
+inline hipError_t launch_grid(const void *kernel, int64_t grid, int parts, int threads, hipStream_t stream, void **args,
+                              uint32_t &first) {
+    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    const int64_t most = ((int64_t(1) << 32) - 1) / threads;
+    for (int64_t at = 0; at < grid; at += most) {
+        first = (uint32_t)at;
+        const hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)std::min(most, grid - at), (unsigned)parts),
+                                             dim3((unsigned)threads), args, 0, stream);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 template <class Kernel>
-inline hipError_t launch_seg(Kernel kernel, int64_t grid, int threads, hipStream_t stream, const SegParams &p,
-                             int parts = 1) {
-    if (grid <= 0) return hipSuccess;
-    void *args[] = {const_cast<SegParams *>(&p)};
-    return hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3((unsigned)grid, (unsigned)parts), dim3((unsigned)threads), args,
-                           0, stream);
+inline hipError_t launch_seg(Kernel kernel, int64_t grid, int threads, hipStream_t stream, SegParams p, int parts = 1) {
+    void *args[] = {&p};
+    return launch_grid(reinterpret_cast<const void *>(kernel), grid, parts, threads, stream, args, p.first);
 }
 
 // Row tiles that the segments can need at most, whatever their sizes: each

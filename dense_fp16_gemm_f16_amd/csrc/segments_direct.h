@@ -298,7 +298,7 @@ void seg_tile_kernel(const SegParams p) {
     __shared__ __attribute__((aligned(1024))) char smem[kLds];
     GEMM_POISON_LDS(smem);
     SegWork<KIND, C, LORA> w;
-    if (!w.find(p, blockIdx.x, (int)threadIdx.x & (kWave - 1))) return;
+    if (!w.find(p, seg_pid(p), (int)threadIdx.x & (kWave - 1))) return;
     seg_tile<KIND, C, F32, LORA>(p, smem, w, (int)threadIdx.x);
 #endif
 }
@@ -333,7 +333,7 @@ __global__ __launch_bounds__(C::kThreads *KG) void seg_ring_kernel(const SegPara
     char *const ring = smem + group * kRing;
     const int wm = wave / C::WN, wn = wave % C::WN;
     SegWork<KIND, C, false> w;
-    if (!w.find(p, blockIdx.x, lane)) return;
+    if (!w.find(p, seg_pid(p), lane)) return;
     // this group's K-tiles: `turns` for every group, those past kt1 zeros
     const int kt_count = (w.k_count + C::BK - 1) / C::BK, turns = (kt_count + KG - 1) / KG;
     const int kt0 = group * turns, kt1 = min(kt0 + turns, kt_count);
@@ -456,7 +456,6 @@ hipError_t launch_seg_ring(SegParams p, bool f32, hipStream_t s) {
     p.num_n = (p.n + C::BN - 1) / C::BN;
     p.num_m = (int32_t)seg_row_tiles(p.rows, p.groups, C::BM);
     const int64_t grid = (int64_t)p.num_m * p.num_n;
-    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
     return f32 ? launch_seg(seg_ring_kernel<KIND, C, S, KG, true, false>, grid, C::kThreads * KG, s, p)
                : launch_seg(seg_ring_kernel<KIND, C, S, KG, false, false>, grid, C::kThreads * KG, s, p);
 }
@@ -474,7 +473,6 @@ hipError_t launch_seg_tile(SegParams p, bool f32, hipStream_t s) {
         p.num_m = (int32_t)m_tiles;
         grid = m_tiles * p.num_n;
     }
-    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
     const int parts = KIND == kSegTN ? p.splits : 1;
     if constexpr (LORA)
         return launch_seg(seg_tile_kernel<KIND, C, false, LORA>, grid, C::kThreads, s, p);
