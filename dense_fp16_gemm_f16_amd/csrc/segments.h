@@ -70,14 +70,14 @@ __device__ __forceinline__ SegPart seg_part(const SegParams &p, int g, int s, in
 }
 
 // The segment that row `row` lies in; groups: it lies behind the last one.  A
-// search by the whole wave, 64 segments a step (offsets that decrease give
-// some segment).
+// search by the whole wave, 65 ways a step (offsets that decrease give some
+// segment).
 __device__ __forceinline__ int seg_of_row(const SegParams &p, int row, int lane) {
     int g = 0, span = p.groups + 1;  // one of g .. g + span - 1
     while (span > 1) {
-        const int stride = (span + kWave - 1) / kWave, at = lane * stride;
+        const int stride = (span + kWave) / (kWave + 1), at = (lane + 1) * stride;
         const uint64_t past = ~__ballot(at < span && seg_bound(p.offsets, g + at, p.rows) <= row);
-        const int step = max((past ? __builtin_ctzll(past) : kWave) - 1, 0) * stride;
+        const int step = (past ? __builtin_ctzll(past) : kWave) * stride;
         g += step;
         span = min(stride, span - step);
     }
