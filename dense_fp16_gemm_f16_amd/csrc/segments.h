@@ -359,12 +359,19 @@ __device__ __forceinline__ void seg_store(const floatx4 (&acc)[C::FN][C::FM], ch
 //
 // An infinity or NaN in U_s would reach the rows of other adapters as
 // 0 * inf: it is taken as 0 here, and lora_wild adds its products to the
-// rows of its adapter afterwards.
+// rows of its adapter afterwards.  An infinity in h stays in h0, and has to
+// give u * inf: both parts of u have its sign, and neither is 0 where u is
+// not (an empty rest becomes 2^-102 u, far below the sum's last bit).
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ void mfma16_tied_bf16(bf16x8 a, bf16x8 b, floatx4 &c) {
     asm volatile("v_mfma_f32_16x16x32_bf16 %0, %1, %2, %0" : "+a"(c) : "v"(a), "v"(b));
+}
+
+// x's upper 16 bits, the rest cut off
+__device__ __forceinline__ __bf16 bf16_cut(float x) {
+    return __builtin_bit_cast(__bf16, (uint16_t)(__builtin_bit_cast(uint32_t, x) >> 16));
 }
 
 // h as its consumer's K-tiles: a row holds, for each 32 ranks, 32 values h0
@@ -376,8 +383,11 @@ __device__ __forceinline__ void store_pairs(char *row, int n, floatx4 v, float f
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float x = n + e < rank ? v[e] * f : 0.0f;
+        const bool finite = fabsf(x) < __builtin_inff();
         top[e] = (__bf16)x;
-        rest[e] = (__bf16)(fabsf(x) < __builtin_inff() ? x - (float)top[e] : 0.0f);
+        // what rounds up to infinity is cut instead
+        if (finite && !(fabsf((float)top[e]) < __builtin_inff())) top[e] = bf16_cut(x);
+        rest[e] = (__bf16)(finite ? x - (float)top[e] : 0.0f);
     }
     char *to = row + n / 32 * 128 + n % 32 * 2;
     *reinterpret_cast<bf16x4 *>(to) = top;
@@ -488,8 +498,8 @@ __device__ __forceinline__ bool lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *s
             v = 0.0f;
             wild = 1;
         }
-        top[e] = (__bf16)v;
-        rest[e] = (__bf16)(v - (float)top[e]);  // exact: at most 3 bits are left
+        top[e] = bf16_cut(v);
+        rest[e] = bf16_cut(__builtin_fmaf(v, 0x1p-102f, v - (float)top[e]));  // at most 3 bits are left: v - top, or 2^-102 v
         if constexpr (e == 7) {
             const int x = i * C::kThreads + tid, r = x >> 2, q = x & 3;
             *reinterpret_cast<bf16x8 *>(to + kB + r * kRow + ((q ^ sw(r)) << 4)) = top;

@@ -1,0 +1,54 @@
+"""What adapters keep of an inner product h = scale (x D^T): its infinities and
+its largest values, at every row count."""
+import pytest
+import torch
+
+import dense_fp16_gemm_f16_amd as g
+from tests import _segments as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def _call(x, w, down, up, ids, scale=None):
+    order, _, off = g.group_rows(ids, down.shape[0])
+    return g.gemm_f16_lora_nt(x, w, down, up, ids, order, off, scale)
+
+
+def _one_adapter(rows, n, k, rank):
+    z = lambda *s: torch.zeros(*s, dtype=torch.float16, device="cuda")  # noqa: E731
+    return z(rows, k), z(n, k), z(1, rank, k), z(1, n, rank), torch.zeros(rows, dtype=torch.int32, device="cuda")
+
+
+# few rows; aligned tiles, rank a multiple of 4 and not; rows that are not 16-byte aligned
+FORMS = [(6, 40, 64, 16), (70, 40, 64, 16), (300, 264, 64, 32), (600, 520, 128, 64), (300, 130, 64, 18), (90, 61, 75, 16)]
+
+
+@pytest.mark.parametrize("rows, n, k, rank", FORMS)
+def test_an_infinite_inner_product_gives_what_fp32_gives(rows, n, k, rank):
+    """h = +-inf in one rank: y = h u there, so +-inf, and NaN where u is 0."""
+    gen = torch.Generator(device="cuda").manual_seed(rank)
+    x, w, down, up, _ = _one_adapter(rows, n, k, rank)
+    down, up = down.repeat(2, 1, 1), up.repeat(2, 1, 1)
+    ids = torch.randint(-1, 2, (rows,), generator=gen, device="cuda", dtype=torch.int32)
+    for t in (x, w, down, up):
+        t.copy_(ref.eighths(gen, *t.shape))
+    x[:, 5] = torch.where(torch.rand(rows, generator=gen, device="cuda") < 0.5, 1.0, -1.0).half()
+    down[1, 3, 5] = float("inf")
+    up[1, :, 3] = (torch.arange(n, device="cuda") % 5 - 2).half() * 0.375  # both signs, of one and two bf16 parts, and 0
+    up[1, n // 2:, 3] *= 1.0009765625
+    out = _call(x, w, down, up, ids).cpu()
+    want, err = ref.lora(*(t.cpu() for t in (x, w, down, up, ids)), None)
+    wild = ~torch.isfinite(want)
+    assert wild[ids.cpu() == 1].all() and not wild[ids.cpu() != 1].any()
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(out[wild].nan_to_num(1.0), want[wild].half().nan_to_num(1.0))
+    assert ref.worst(out[~wild], want[~wild], err[~wild], torch.float16) <= 1.0
+
+
+@pytest.mark.parametrize("rows, n, k, rank", FORMS)
+def test_the_largest_inner_product_times_zero_is_zero(rows, n, k, rank):
+    x, w, down, up, ids = _one_adapter(rows, n, k, rank)
+    x[:, 0], w[:, 0], down[0, :, 0] = 1.0, 2.0, 1.0
+    down[0, 1, 0] = -1.0
+    scale = torch.full((1,), torch.finfo(torch.float32).max, device="cuda")
+    assert (_call(x, w, down, up, ids, scale) == 2.0).all()
