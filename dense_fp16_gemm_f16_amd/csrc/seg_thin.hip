@@ -123,7 +123,7 @@ __device__ __forceinline__ void store_h(const SegParams &p, float *h, int n, flo
     if (n < p.h_ld) *reinterpret_cast<floatx4 *>(h + n) = sum;
 }
 
-// A grouped NT product (DOWN false), or h in adapter order as pairs (DOWN), a
+// A grouped NT product (DOWN false), or h in adapter order in its parts (DOWN), a
 // segment's rows shared by gridDim.y workgroups.
 constexpr int kThinSteps = 8, kThinWaves = 16;
 template <bool F32, bool DOWN>
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(kThinWaves *kWave) void seg_thin_kernel(const SegPa
     const float f = DOWN && p.scale ? p.scale[g] : 1.0f;
     thin_rows<kThinSteps, kThinSteps, kThinWaves>(p, red, g, n0, lo, hi, step, 0, (p.k + 31) / 32, [&](int r, int n, floatx4 sum) {
         if constexpr (DOWN) {
-            if (n < p.h_ld) store_pairs(static_cast<char *>(p.c) + (int64_t)r * p.h_ld * 4, n, sum, f, p.rank);
+            if (n < p.h_ld) store_split(static_cast<char *>(p.c) + (int64_t)r * p.h_ld * kSplitValue, n, sum, f, p.rank);
         } else {
             typedef Out out4 __attribute__((ext_vector_type(4)));
             Out *c = static_cast<Out *>(p.c) + (int64_t)r * p.n + n;
@@ -335,7 +335,7 @@ __global__ __launch_bounds__(256) void lora_down_short_kernel(const SegParams p)
                 sum[e] += (float)p.a[(int64_t)src * p.k + k] * (float)p.b[((int64_t)g * p.n + n + e) * p.k + k];
         }
     }
-    store_pairs(static_cast<char *>(p.c) + r * p.h_ld * 4, n, sum, g < p.groups && p.scale ? p.scale[g] : 1.0f, p.rank);
+    store_split(static_cast<char *>(p.c) + r * p.h_ld * kSplitValue, n, sum, g < p.groups && p.scale ? p.scale[g] : 1.0f, p.rank);
 }
 
 // ---- launches -----------------------------------------------------------------------

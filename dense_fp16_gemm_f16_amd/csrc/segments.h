@@ -41,7 +41,7 @@ struct SegParams {
     // C and A is order[r]
     const int32_t *order;
     const float *h;         // TN: the parts; adapters: up to kLoraFewRows rows: [h_parts][rows, h_ld] fp32, whose sum is scale_s (x D_s^T)
-    const char *h_pairs;    // more rows: rows of h_ld values, zeros past the rank (store_pairs)
+    const char *h_split;    // more rows: rows of h_ld values, zeros past the rank (store_split)
     const _Float16 *up;     // [adapters, n, rank]
     const float *scale;     // [adapters]: multiplies the rows of h (null: 1)
     int32_t adapters, rank, h_ld;
@@ -352,10 +352,12 @@ __device__ __forceinline__ void seg_store(const floatx4 (&acc)[C::FN][C::FM], ch
 // Adds h U_s^T, h = scale_s x D_s^T, to a tile of x W^T whose rows are
 // sorted by adapter: for each adapter with rows in the tile and each 32 of its
 // ranks, one K-tile whose A is h, zero in rows of other adapters, and whose
-// B is U_s.  h has fp32's range, so it goes through the MFMA as two bf16
-// parts (h = h0 + h1 to 2^-18 of it) and U_s as two that hold it exactly; the
-// product leaves out h1 u1, at most 2^-18 of h U.  Against the 2^-11 half
-// step of y, one fp16 part would have cost accuracy and range.
+// B is U_s.  h is an fp32 sum, so it goes through the MFMA as three bf16 parts,
+// which hold it exactly, and U_s as two that do.  Five products of parts
+// make h U: the sixth, h2 u1, is below 2^-23 of it, one step of an fp32 product
+// (|h2| <= 2^-16 |h|, |u1| < 2^-7 |u|).  Two parts of h, with three products, lost
+// 2^-17 of h: 4096 rows, 4096 x 4096, 8 adapters of rank 64 took 143 us with them
+// and take 146.
 //
 // An infinity or NaN in U_s would reach the rows of other adapters as
 // 0 * inf: it is taken as 0 here, and lora_wild adds its products to the
@@ -374,12 +376,15 @@ __device__ __forceinline__ __bf16 bf16_cut(float x) {
     return __builtin_bit_cast(__bf16, (uint16_t)(__builtin_bit_cast(uint32_t, x) >> 16));
 }
 
-// h as its consumer's K-tiles: a row holds, for each 32 ranks, 32 values h0
-// and the 32 rests h1, bf16, 128 bytes.  Four values of a row, times f; zeros
-// past the rank (n % 4 == 0, n < h_ld).
-__device__ __forceinline__ void store_pairs(char *row, int n, floatx4 v, float f, int rank) {
+constexpr int kSplit = 192;  // bytes of 32 values of h
+constexpr int kSplitValue = kSplit / 32;
+
+// h as its consumer's K-tiles: a row holds, for each 32 ranks, 32 values h0,
+// the 32 next parts h1 and the 32 last h2, bf16.  Four values of a row, times
+// f; zeros past the rank (n % 4 == 0, n < h_ld).
+__device__ __forceinline__ void store_split(char *row, int n, floatx4 v, float f, int rank) {
     typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-    bf16x4 top, rest;
+    bf16x4 top, next, last;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const float x = n + e < rank ? v[e] * f : 0.0f;
@@ -387,11 +392,14 @@ __device__ __forceinline__ void store_pairs(char *row, int n, floatx4 v, float f
         top[e] = (__bf16)x;
         // what rounds up to infinity is cut instead
         if (finite && !(fabsf((float)top[e]) < __builtin_inff())) top[e] = bf16_cut(x);
-        rest[e] = (__bf16)(finite ? x - (float)top[e] : 0.0f);
+        const float rest = finite ? x - (float)top[e] : 0.0f;  // both differences are exact
+        next[e] = (__bf16)rest;
+        last[e] = (__bf16)(rest - (float)next[e]);
     }
-    char *to = row + n / 32 * 128 + n % 32 * 2;
+    char *to = row + n / 32 * kSplit + n % 32 * 2;
     *reinterpret_cast<bf16x4 *>(to) = top;
-    *reinterpret_cast<bf16x4 *>(to + 64) = rest;
+    *reinterpret_cast<bf16x4 *>(to + 64) = next;
+    *reinterpret_cast<bf16x4 *>(to + 128) = last;
 }
 
 // The adapters with rows in [row0, row0 + valid), in order: lane l looks at
@@ -420,10 +428,19 @@ struct LoraWalk {
     }
 };
 
+// Bytes of LDS that lora_tiles takes: two stages of the three parts of h, each
+// a plane of 64-byte rows whose 16-byte chunk c sits at c ^ (row / 4) % 4 (so
+// that 16 rows' chunks c lie on different banks), and of U_s.
+template <class C>
+constexpr int lora_lds() {
+    return 2 * (C::BM * kSplit + C::BN * 128);
+}
+
 // Returns (to every thread) whether some U_s of the tile is not finite.
 // w: the first adapter with rows in the tile.  votes: one int per wave, in
 // the kernel's one LDS array (a library vote would bring an array of its own,
-// see seg_tile).  RANK4: the rank is a multiple of 4, so half chunks lie
+// see seg_tile), behind what the epilogue uses: the last stage is done with
+// by then.  RANK4: the rank is a multiple of 4, so half chunks lie
 // wholly inside a row of U_s; the tails of other ranks cost scalar registers
 // that the 256-wide tiles do not have.
 //
@@ -431,29 +448,33 @@ struct LoraWalk {
 // MFMAs of this one; U_s comes through registers two K-tiles ahead, and is
 // split and written an element at a time between the MFMAs.
 //
-// 4096 rows, 4096 x 4096, 8 adapters of rank 64 in runs: 128 us against 104
-// without adapters; a tile across three adapters does six such K-tiles of 3
+// 4096 rows, 4096 x 4096, 8 adapters of rank 64 in runs: 135 us against 104
+// without adapters; a tile across three adapters does six such K-tiles of 5
 // MFMAs per block beside its 64 of 2.
 template <class C, bool RANK4>
 __device__ __forceinline__ bool lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *smem, int *votes, const SegParams &p,
                                            LoraWalk w, int row0, int valid, int n0, int tid, int lane, int wm, int wn) {
-    constexpr int kRow = 128, kB = C::BM * kRow, kStage = (C::BM + C::BN) * kRow;
+    constexpr int kRow = 128, kPlane = C::BM * 64, kB = 3 * kPlane, kStage = kB + C::BN * kRow;
+    static_assert(2 * kStage == lora_lds<C>(), "LDS of the stages");
     auto sw = [](int r) { return (r >> 1) & 7; };
-    constexpr int LA = C::BM * kRow / 1024 / C::kWaves, HB = C::BN * 4 / C::kThreads;
-    static_assert(LA * 1024 * C::kWaves == C::BM * kRow && HB * C::kThreads == C::BN * 4, "whole passes");
+    auto sw_h = [](int r) { return (r >> 2) & 3; };
+    constexpr int BA = kB / 1024, LA = (BA + C::kWaves - 1) / C::kWaves, HB = C::BN * 4 / C::kThreads;  // blocks of 16 rows
+    static_assert(C::BM % 16 == 0 && HB * C::kThreads == C::BN * 4, "whole passes");
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const uint32_t pitch = (uint32_t)p.h_ld * 4u;
-    const __amdgpu_buffer_rsrc_t h_rows = make_rsrc(p.h_pairs + (int64_t)row0 * pitch, (uint32_t)valid * pitch);
+    const uint32_t pitch = (uint32_t)p.h_ld * kSplitValue;
+    const __amdgpu_buffer_rsrc_t h_rows = make_rsrc(p.h_split + (int64_t)row0 * pitch, (uint32_t)valid * pitch);
     const _Float16 *up_end = p.up + (int64_t)p.adapters * p.n * p.rank;
     int c = 0;  // w's next K-tile starts at rank c
     auto load_h = [&](int stage) {
 #pragma unroll
         for (int i = 0; i < LA; ++i) {
-            const int r = (i * C::kWaves + wave) * 8 + (lane >> 3);
-            const uint32_t off = (uint32_t)r * pitch + (uint32_t)(((lane & 7) ^ sw(r)) << 4);
+            const int block = i * C::kWaves + wave;
+            if (BA % C::kWaves != 0 && block >= BA) continue;
+            const int r = block % (C::BM / 16) * 16 + (lane >> 2);
+            const uint32_t off = (uint32_t)r * pitch + (uint32_t)(block / (C::BM / 16) * 64 + (((lane & 3) ^ sw_h(r)) << 4));
             __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                h_rows, (__attribute__((address_space(3))) void *)(smem + stage * kStage + (i * C::kWaves + wave) * 1024),
-                16, r >= w.lo && r < w.hi ? off : kOutOfRange, (uint32_t)c * 4u, 0, 0);
+                h_rows, (__attribute__((address_space(3))) void *)(smem + stage * kStage + block * 1024), 16,
+                r >= w.lo && r < w.hi ? off : kOutOfRange, (uint32_t)c * (uint32_t)kSplitValue, 0, 0);
         }
     };
     auto fetch_u = [&](int4v (&u)[HB]) {
@@ -507,8 +528,8 @@ __device__ __forceinline__ bool lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *s
         }
     };
     constexpr int E = HB * 8;
-    // u0 h0, u1 h0, then u0 h1
-    constexpr int NM = C::FM * C::FN, M = 3 * NM;
+    // u0 h0, u1 h0, u0 h1, u1 h1, then u0 h2
+    constexpr int NM = C::FM * C::FN, M = 5 * NM;
 
     int stage = 0;
     bool more = w.s >= 0;
@@ -543,7 +564,7 @@ __device__ __forceinline__ bool lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *s
 #pragma unroll
                 for (int q = 0; q < C::FM; ++q) {
                     const int r = wm * C::TM + q * 16 + lane % 16;
-                    af[q] = *reinterpret_cast<const bf16x8 *>(from + r * kRow + (((4 * ka + lane / 16) ^ sw(r)) << 4));
+                    af[q] = *reinterpret_cast<const bf16x8 *>(from + ka * kPlane + r * 64 + (((lane / 16) ^ sw_h(r)) << 4));
                 }
             }
             if constexpr (i == 0) {
@@ -586,8 +607,8 @@ __device__ __forceinline__ void lora_wild(const SegParams &p, int row0, int vali
                 for (int j = 0; j < p.rank; ++j) {
                     const float f = (float)up[j];
                     if (fabsf(f) < __builtin_inff()) continue;
-                    const __bf16 *h = reinterpret_cast<const __bf16 *>(p.h_pairs + (int64_t)r * p.h_ld * 4 + j / 32 * 128);
-                    sum += ((float)h[j % 32] + (float)h[32 + j % 32]) * f;
+                    const __bf16 *h = reinterpret_cast<const __bf16 *>(p.h_split + (int64_t)r * p.h_ld * kSplitValue + j / 32 * kSplit);
+                    sum += ((float)h[j % 32] + (float)h[32 + j % 32] + (float)h[64 + j % 32]) * f;
                 }
                 if (!(fabsf(sum) < __builtin_inff())) y[n] = (_Float16)((float)y[n] + sum);
             }
@@ -613,9 +634,9 @@ __global__ __launch_bounds__(C::kThreads) void seg_staged_kernel(const SegParams
     constexpr int kLdsB = 2 * OpA::kStage, kLds = kLdsB + 2 * OpB::kStage;
     // one LDS array: with two, the compiler waits for every load in flight
     // before each fragment read
-    constexpr int kVotes = LORA ? 64 : 0;
-    static_assert(kLds + kVotes <= 160 * 1024, "LDS budget");
-    __shared__ __attribute__((aligned(1024))) char smem[kLds + kVotes];
+    constexpr int kAll = LORA ? lora_lds<C>() : kLds;
+    static_assert(kAll <= 160 * 1024 && (!LORA || kLds + C::kWaves * 4 <= kAll), "LDS budget");
+    __shared__ __attribute__((aligned(1024))) char smem[kAll];
     GEMM_POISON_LDS(smem);
 
     const int tid = threadIdx.x, lane = tid & (kWave - 1);
@@ -803,7 +824,7 @@ hipError_t launch_seg_lora(int tile, const SegParams &p, hipStream_t s);
 // Few rows (seg_thin.hip).
 constexpr int64_t kLoraFewRows = 64;  // rows up to here: launch_lora_few
 hipError_t launch_seg_thin(bool f32, const SegParams &p, hipStream_t s);
-// h as pairs, rows in adapter order: direct-to-LDS tiles, or any rows
+// h in its parts, rows in adapter order: direct-to-LDS tiles, or any rows
 hipError_t launch_lora_down(SegParams p, hipStream_t s);
 hipError_t launch_lora_down_thin(const SegParams &p, hipStream_t s);
 // sums: fp32 [lora_few_parts(k)][rows, n]; down.c is h with rows in their own

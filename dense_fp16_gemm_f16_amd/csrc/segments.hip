@@ -301,8 +301,8 @@ static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k,
 // The few-row kernel's loads need a whole chunk of K.
 static bool lora_few(int64_t rows, int64_t k) { return rows <= kLoraFewRows && k >= 8; }
 
-// Values of h in a row: whole 16-byte stores, or lora_tiles' whole 32 ranks as
-// pairs of 2 bytes
+// Values of h in a row: whole 16-byte stores, or lora_tiles' whole 32 ranks in
+// parts
 static int64_t lora_h_ld(int64_t rows, int64_t k, int64_t rank) {
     const int64_t to = lora_few(rows, k) ? 4 : 32;
     return (rank + to - 1) / to * to;
@@ -385,8 +385,10 @@ int gemm_f16_grouped_tn_ws(int64_t rows, int64_t groups, int64_t n, int64_t k, c
 int64_t gemm_f16_lora_workspace(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64_t rank) {
     const int rc = check_lora(rows, n, k, adapters, rank);
     if (rc != GEMM_F16_OK) return rc;
-    // h, and x W^T in fp32 for few rows
-    return rows * lora_h_ld(rows, k, rank) * lora_parts(rows, k) * 4 + (lora_few(rows, k) ? rows * n * lora_few_parts(k) * 4 : 0);
+    const int64_t h = rows * lora_h_ld(rows, k, rank);
+    if (!lora_few(rows, k)) return h * kSplitValue;
+    // h, and x W^T, in fp32
+    return (h * lora_parts(rows, k) + rows * n * lora_few_parts(k)) * 4;
 }
 
 int gemm_f16_lora_nt(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64_t rank, const void *x, const void *w,
@@ -435,7 +437,7 @@ int gemm_f16_lora_nt(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64
     p.b = static_cast<const _Float16 *>(w);
     p.c = y;
     p.h = static_cast<const float *>(workspace);
-    p.h_pairs = static_cast<const char *>(workspace);
+    p.h_split = static_cast<const char *>(workspace);
     p.up = static_cast<const _Float16 *>(up);
     p.groups = 1;
     p.n = (int32_t)n;

@@ -293,8 +293,8 @@ __global__ __launch_bounds__(C::kThreads)
 __attribute__((amdgpu_waves_per_eu(C::kMinWavesPerEU, C::kMinWavesPerEU)))
 void seg_tile_kernel(const SegParams p) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
-    constexpr int kLds = seg_tile_lds<KIND, C>() + (LORA ? 64 : 0);
-    static_assert(kLds <= 160 * 1024, "LDS budget");
+    constexpr int kOps = seg_tile_lds<KIND, C>(), kLds = LORA ? lora_lds<C>() : kOps;
+    static_assert(kLds <= 160 * 1024 && (!LORA || kOps + C::kWaves * 4 <= kLds), "LDS budget");
     __shared__ __attribute__((aligned(1024))) char smem[kLds];
     GEMM_POISON_LDS(smem);
     SegWork<KIND, C, LORA> w;
@@ -311,7 +311,7 @@ void seg_tile_kernel(const SegParams p) {
 // K-tiles in flight.  KG 2: twice the waves, each half of them with a ring of
 // its own over half of K, the halves' sums meeting in LDS: for grids that
 // leave CUs with one workgroup or none.
-// DOWN: h of the adapters, times their scale, as pairs (4096 rows, K 4096, 8
+// DOWN: h of the adapters, times their scale, in parts (4096 rows, K 4096, 8
 // adapters of rank 64: 16 us, 33 MB of x at 2.1 TB/s, bound by how long 128-byte
 // pieces of rows take to come; 32 x 32 tiles, which read x twice: 25 us).
 template <int KIND, class C, int S, int KG, bool F32, bool DOWN>
@@ -438,11 +438,11 @@ __global__ __launch_bounds__(C::kThreads *KG) void seg_ring_kernel(const SegPara
         for (int i = 0; i < FM; ++i) {
             const int r = wm * TM + 16 * i + lane % 16;
             if (r >= w.valid) continue;
-            char *row = static_cast<char *>(p.c) + (int64_t)(row0 + r) * p.h_ld * 4;
+            char *row = static_cast<char *>(p.c) + (int64_t)(row0 + r) * p.h_ld * kSplitValue;
 #pragma unroll
             for (int j = 0; j < FN; ++j) {
                 const int n = w.n0 + wn * TN + 16 * j + 4 * (lane / 16);
-                if (n < p.h_ld) store_pairs(row, n, acc[j][i], f, p.rank);
+                if (n < p.h_ld) store_split(row, n, acc[j][i], f, p.rank);
             }
         }
     } else {

@@ -284,8 +284,8 @@ int64_t gemm_f16_grouped_tn_workspace(int64_t rows, int64_t groups, int64_t n, i
  *   scale    fp32 [adapters], or NULL for ones
  *   y        fp16 [rows,N]
  *
- * The inner product is kept in fp32 (for many rows its second product takes
- * it as two bf16 parts, off by at most 2^-17 of it) and Y is rounded once.
+ * The inner product is kept in fp32 (past 64 rows its second product takes it
+ * as three bf16 parts, which hold it exactly) and Y is rounded once.
  * rows, n < 2^30; k < 2^22; 1 <= rank <= 4096; 1 <= adapters <= 2^20;
  * rows*n, n*k, adapters*rank*(n+k) < 2^47.
  */

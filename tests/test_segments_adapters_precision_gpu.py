@@ -1,5 +1,5 @@
-"""What adapters keep of an inner product h = scale (x D^T): its infinities and
-its largest values, at every row count."""
+"""What adapters keep of an inner product h = scale (x D^T): all of its fp32
+bits and its infinities, at every row count."""
 import pytest
 import torch
 
@@ -52,3 +52,54 @@ def test_the_largest_inner_product_times_zero_is_zero(rows, n, k, rank):
     down[0, 1, 0] = -1.0
     scale = torch.full((1,), torch.finfo(torch.float32).max, device="cuda")
     assert (_call(x, w, down, up, ids, scale) == 2.0).all()
+
+
+@pytest.mark.parametrize("rows, n, k, rank", FORMS)
+def test_every_bit_of_an_inner_product_counts(rows, n, k, rank):
+    """Pairs of ranks with h and h + d, h of 19 bits, and u = -1 and 1: y is the
+    sum of the d, and every partial sum is a whole number below 2^24."""
+    gen = torch.Generator(device="cuda").manual_seed(rows)
+    x, w, down, up, ids = _one_adapter(rows, n, k, rank)
+    x[:, 0], x[:, 1] = 4096.0, 1.0
+    x[:, 2] = torch.randint(-2, 3, (rows,), generator=gen, device="cuda").half()
+    pairs = min(rank // 2, 8)
+    high = torch.randint(0, 128, (pairs,), generator=gen, device="cuda").half()
+    low = torch.randint(0, 2048, (pairs,), generator=gen, device="cuda").half()
+    d = torch.randint(-3, 4, (pairs,), generator=gen, device="cuda").half()
+    down[0, 0:2 * pairs:2, 0] = down[0, 1:2 * pairs:2, 0] = high
+    down[0, 0:2 * pairs:2, 1] = down[0, 1:2 * pairs:2, 1] = low
+    down[0, 1:2 * pairs:2, 2] = d
+    up[0, :, 0:2 * pairs:2], up[0, :, 1:2 * pairs:2] = -1.0, 1.0
+    want = x[:, 2] * d.sum()
+    assert torch.equal(_call(x, w, down, up, ids), want[:, None].expand(rows, n))
+
+
+def test_every_bit_of_a_single_inner_product():
+    """2^23 + 2^12 + 1 against -2^23 and -2^12."""
+    for rows, n, k, rank in FORMS:
+        x, w, down, up, ids = _one_adapter(rows, n, k, rank)
+        x[:, 0], x[:, 1] = 4096.0, 1.0
+        x[:, 2] = 1.0
+        down[0, 0, 0], down[0, 0, 1], down[0, 0, 2] = 2048.0, 1.0, 4096.0
+        down[0, 1, 0], down[0, 2, 0] = 2048.0, 1.0
+        up[0, :, 0], up[0, :, 1], up[0, :, 2] = 1.0, -1.0, -1.0
+        assert (_call(x, w, down, up, ids) == 1.0).all(), (rows, n, k, rank)
+
+
+@pytest.mark.parametrize("rows, n, k, rank", FORMS)
+def test_adapters_are_as_exact_as_fp32(rows, n, k, rank):
+    """The bound of sums in fp32: k terms and a scale for h, then k + 5 rank
+    terms, and the least product of parts, below 2^-23 of its term."""
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    x, w, down, up, ids = _one_adapter(rows, n, k, rank)
+    for t in (x, w, down, up):
+        t.copy_(ref.normal(gen, *t.shape))
+    up[0, :, 1::2] = -up[0, :, ::2][:, :rank // 2]  # pairs of ranks that nearly cancel
+    down[0, 1::2] = down[0, ::2][:rank // 2]
+    down[0, 1::2, 0] += 2.0**-9
+    w.zero_()
+    scale = torch.full((1,), 0.75, device="cuda")
+    want, _ = ref.lora(x, w, down, up, ids, scale)
+    h = 0.75 * torch.mm(x.double().abs(), down[0].double().abs().T.contiguous())
+    mag = torch.mm(h, up[0].double().abs().T.contiguous())
+    assert ref.worst(_call(x, w, down, up, ids, scale), want, mag * (2 * k + 6 * rank + 4) * 2.0**-23, torch.float16) <= 1.0
