@@ -51,6 +51,8 @@ def _launch(device, stream, call):
     import torch
 
     if stream is not None:
+        if stream.device != device:  # kernels run where the stream is
+            raise ValueError("stream must be on the same GPU as the operands")
         with torch.cuda.stream(stream):
             return call(stream.cuda_stream)
     index = device.index
