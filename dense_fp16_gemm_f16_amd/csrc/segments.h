@@ -354,16 +354,16 @@ __device__ __forceinline__ void seg_store(const floatx4 (&acc)[C::FN][C::FM], ch
 // ranks, one K-tile whose A is h, zero in rows of other adapters, and whose
 // B is U_s.  h is an fp32 sum, so it goes through the MFMA as three bf16 parts,
 // which hold it exactly, and U_s as two that do.  Five products of parts
-// make h U: the sixth, h2 u1, is below 2^-23 of it, one step of an fp32 product
-// (|h2| <= 2^-16 |h|, |u1| < 2^-7 |u|).  Two parts of h, with three products, lost
+// make h U: the sixth, h2 u1, is at most 2^-24 of it, half a step of an fp32
+// product (|h2| <= 2^-16 |h|, |u1| <= 2^-8 |u|).  Two parts of h, with three products, lost
 // 2^-17 of h: 4096 rows, 4096 x 4096, 8 adapters of rank 64 took 143 us with them
 // and take 146.
 //
 // An infinity or NaN in U_s would reach the rows of other adapters as
 // 0 * inf: it is taken as 0 here, and lora_wild adds its products to the
-// rows of its adapter afterwards.  An infinity in h stays in h0, and has to
-// give u * inf: both parts of u have its sign, and neither is 0 where u is
-// not (an empty rest becomes 2^-102 u, far below the sum's last bit).
+// rows of its adapter afterwards.  An infinity in h has to give u * inf, so it
+// travels as h2, which meets u0 alone: u's sign, and 0 where u is 0 (times
+// u1, of 0 or the other sign, it would be a NaN).
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
@@ -389,12 +389,12 @@ __device__ __forceinline__ void store_split(char *row, int n, floatx4 v, float f
     for (int e = 0; e < 4; ++e) {
         const float x = n + e < rank ? v[e] * f : 0.0f;
         const bool finite = fabsf(x) < __builtin_inff();
-        top[e] = (__bf16)x;
+        top[e] = (__bf16)(finite ? x : 0.0f);
         // what rounds up to infinity is cut instead
-        if (finite && !(fabsf((float)top[e]) < __builtin_inff())) top[e] = bf16_cut(x);
+        if (!(fabsf((float)top[e]) < __builtin_inff())) top[e] = bf16_cut(x);
         const float rest = finite ? x - (float)top[e] : 0.0f;  // both differences are exact
         next[e] = (__bf16)rest;
-        last[e] = (__bf16)(rest - (float)next[e]);
+        last[e] = (__bf16)(finite ? rest - (float)next[e] : x);
     }
     char *to = row + n / 32 * kSplit + n % 32 * 2;
     *reinterpret_cast<bf16x4 *>(to) = top;
@@ -519,8 +519,8 @@ __device__ __forceinline__ bool lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *s
             v = 0.0f;
             wild = 1;
         }
-        top[e] = bf16_cut(v);
-        rest[e] = bf16_cut(__builtin_fmaf(v, 0x1p-102f, v - (float)top[e]));  // at most 3 bits are left: v - top, or 2^-102 v
+        top[e] = (__bf16)v;
+        rest[e] = (__bf16)(v - (float)top[e]);  // exact: at most 3 bits are left
         if constexpr (e == 7) {
             const int x = i * C::kThreads + tid, r = x >> 2, q = x & 3;
             *reinterpret_cast<bf16x8 *>(to + kB + r * kRow + ((q ^ sw(r)) << 4)) = top;

@@ -103,3 +103,22 @@ def test_adapters_are_as_exact_as_fp32(rows, n, k, rank):
     h = 0.75 * torch.mm(x.double().abs(), down[0].double().abs().T.contiguous())
     mag = torch.mm(h, up[0].double().abs().T.contiguous())
     assert ref.worst(_call(x, w, down, up, ids, scale), want, mag * (2 * k + 6 * rank + 4) * 2.0**-23, torch.float16) <= 1.0
+
+
+def _many_adapters(rows, adapters, rank, n, k, seed):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    ids = torch.randint(-1, adapters, (rows,), generator=gen, device="cuda", dtype=torch.int32)
+    make = lambda *s: torch.randint(-1, 2, s, generator=gen, device="cuda").half()  # noqa: E731
+    t = [make(rows, k), make(n, k), make(adapters, rank, k), make(adapters, n, rank)]
+    return t, ids
+
+
+@pytest.mark.parametrize("rows, adapters, rank, n, k", [(300, 37, 64, 264, 64), (1000, 200, 32, 512, 64), (500, 40, 100, 136, 72),
+                                                        (260, 100, 48, 130, 33), (60, 64, 64, 200, 72)])
+def test_adapters_many_to_a_tile_are_exact(rows, adapters, rank, n, k):
+    """Sums that are exact in fp32 come out exact: zeros too."""
+    t, ids = _many_adapters(rows, adapters, rank, n, k, rows)
+    order, _, off = g.group_rows(ids, adapters)
+    want, _ = ref.lora(*t, ids, None)
+    assert float(want.abs().max()) <= 2048  # whole numbers that fp16 holds
+    assert torch.equal(g.gemm_f16_lora_nt(*t, ids, order, off), want.half())
