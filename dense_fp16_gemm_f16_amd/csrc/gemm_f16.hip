@@ -1,6 +1,8 @@
 // libgemm_f16 host side: the C ABI of include/gemm_f16.h -- argument
 // checks, the device gate, the block-tile choice and the launch.  The
 // kernels live in kernels.h and are compiled per block tile (tile_*.hip).
+#include <atomic>
+#include <cstdlib>
 #include <hip/hip_runtime.h>
 
 #include <stdint.h>
@@ -8,7 +10,6 @@
 #include <algorithm>
 #include <bitset>
 
-#include "device.h"
 #include "gemm_f16.h"
 #include "kernels.h"
 
@@ -199,6 +200,52 @@ static bool ranges_overlap(const void *p, int64_t pb, const void *q, int64_t qb)
     const uintptr_t a0 = (uintptr_t)p, a1 = a0 + (uintptr_t)pb;
     const uintptr_t b0 = (uintptr_t)q, b1 = b0 + (uintptr_t)qb;
     return pb > 0 && qb > 0 && a0 < b1 && b0 < a1;
+}
+
+// Per-device caches below: host threads may call the library at the same
+// time, so the entries are atomics; a first call on a device in two threads
+// at once computes the same value twice and stores it twice.
+
+// Compute units of the current device (0 if unknown), cached per device.
+static int device_cus() {
+    static std::atomic<int> cached[64];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 0;
+    int n = cached[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (hipDeviceGetAttribute(&n, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || n <= 0) return 0;
+        cached[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// "gfx950", optionally followed by ":" and target features.
+static bool is_gfx950(const char *arch) {
+    return arch[0] == 'g' && arch[1] == 'f' && arch[2] == 'x' && arch[3] == '9' && arch[4] == '5' &&
+           arch[5] == '0' && (arch[6] == '\0' || arch[6] == ':');
+}
+
+// Test hook: when the environment variable GEMM_F16_TEST_ARCH is set as the
+// library loads, its value stands in for every device's architecture name
+// in the gate below (no device is queried), so the refusal path can be
+// exercised on any host.
+static const char *const kTestArch = std::getenv("GEMM_F16_TEST_ARCH");
+
+// gfx950 check, cached per device.
+static int check_device() {
+    if (kTestArch) return is_gfx950(kTestArch) ? GEMM_F16_OK : GEMM_F16_EDEVICE;
+    static std::atomic<int> cached[64];  // 0 = unknown, 1 = gfx950, -1 = other
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return GEMM_F16_EHIP;
+    if (dev < 0 || dev >= 64) return GEMM_F16_EDEVICE;
+    int state = cached[dev].load(std::memory_order_relaxed);
+    if (state == 0) {
+        hipDeviceProp_t prop;
+        if (hipGetDeviceProperties(&prop, dev) != hipSuccess) return GEMM_F16_EHIP;
+        state = is_gfx950(prop.gcnArchName) ? 1 : -1;
+        cached[dev].store(state, std::memory_order_relaxed);
+    }
+    return state == 1 ? GEMM_F16_OK : GEMM_F16_EDEVICE;
 }
 
 // Both contracts: NN == false is C fp16 = A B^T (B [N,K]); NN == true is

@@ -13,7 +13,7 @@ namespace gemm_f16 {
 
 constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxK = int64_t(1) << 22, kMaxNMajor = int64_t(1) << 25;
 // gfx950's CUs (the sizes alone say what workspace a call takes), and the most parts
-constexpr int kCus = 256, kTnSplits = 64;
+constexpr int kTnCus = 256, kTnSplits = 64;
 constexpr int64_t kMaxElems = int64_t(1) << 47, kMaxGroups = int64_t(1) << 20;
 
 // One buffer of a call, for the checks on pointers.
@@ -66,12 +66,6 @@ static bool direct_rows(int kind, const SegParams &p) {
     // (64 rows of B below 2^31 bytes)
     if (kind != kSegNT && (p.n % 8 != 0 || p.n >= (1 << 24))) return false;
     return !(p.index || p.order) || p.a_rows * p.k * 2 < (int64_t(1) << 31);
-}
-
-// Compute units to plan for.
-static int known_cus() {
-    const int cus = device_cus();
-    return cus > 0 ? cus : kCus;
 }
 
 static int64_t cdiv64(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -185,7 +179,7 @@ static SegPlan pick_plan(int kind, bool f32, const SegParams &p, int cus) {
 // 76 and, in 2 parts, 53; 1024 rows of 512 x 512: 10.7 and 12, not split.)
 static int tn_splits(int64_t rows, int64_t groups, int64_t n, int64_t k) {
     const int64_t tiles = groups * cdiv64(n, 128) * cdiv64(k, 128);
-    if (tiles >= kCus || rows < 4 * 64) return 1;
+    if (tiles >= kTnCus || rows < 4 * 64) return 1;
     const int64_t longest = groups > 1 ? rows * 2 : rows;  // times groups
     const int64_t mean_kt = cdiv64(cdiv64(rows, groups), 64), long_kt = cdiv64(cdiv64(longest, groups), 64);
     SegParams p = {};
@@ -193,10 +187,10 @@ static int tn_splits(int64_t rows, int64_t groups, int64_t n, int64_t k) {
     p.groups = (int32_t)groups;
     p.n = (int32_t)n;
     p.k = (int32_t)k;
-    double best = pick_plan(kSegTN, true, p, kCus).us;
+    double best = pick_plan(kSegTN, true, p, kTnCus).us;
     int splits = 1;
-    for (int s = 2; s <= kTnSplits && s <= long_kt && tiles * s <= 2 * kCus; ++s) {
-        const double share = (double)(tiles * s) / kCus;
+    for (int s = 2; s <= kTnSplits && s <= long_kt && tiles * s <= 2 * kTnCus; ++s) {
+        const double share = (double)(tiles * s) / kTnCus;
         const double round = std::max((double)cdiv64(long_kt, s), std::ceil(share) * (double)cdiv64(mean_kt, s));
         const double t = 4.76 + 0.52 * round + 3.95 * share + 7.0 + 6.0 * share;
         if (t < best) {
@@ -247,9 +241,9 @@ static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k,
                            {index, index ? rows * 4 : 0, 4, false}};
     rc = check_buffers(bufs);
     if (rc != GEMM_F16_OK) return rc;
-    rc = check_device();
+    int cus;
+    rc = current_device(&cus);
     if (rc != GEMM_F16_OK) return rc;
-    const int cus = known_cus();
 
     SegParams p = {};
     p.a = static_cast<const _Float16 *>(a);
@@ -349,7 +343,8 @@ int gemm_f16_group_rows(int64_t rows, int64_t groups, const void *ids, int32_t i
                            {ids, rows * id_bytes, id_bytes, false}};
     int rc = check_buffers(bufs);
     if (rc != GEMM_F16_OK) return rc;
-    rc = check_device();
+    int cus;
+    rc = current_device(&cus);
     if (rc != GEMM_F16_OK) return rc;
     return status(launch_group_rows(rows, (int)groups, ids, id_bytes, order, inverse, offsets,
                                     static_cast<int32_t *>(workspace), (hipStream_t)stream));
@@ -417,9 +412,9 @@ int gemm_f16_lora_nt(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64
                            {scale, scale ? adapters * 4 : 0, 4, false}};
     rc = check_buffers(bufs);
     if (rc != GEMM_F16_OK) return rc;
-    rc = check_device();
+    int cus;
+    rc = current_device(&cus);
     if (rc != GEMM_F16_OK) return rc;
-    const int cus = known_cus();
 
     SegParams p = {};
     p.a = static_cast<const _Float16 *>(x);
