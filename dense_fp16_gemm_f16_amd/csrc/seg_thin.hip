@@ -38,8 +38,8 @@ __device__ __forceinline__ void thin_load(half8 (&v)[N], const _Float16 *row, in
 // flight at once, and stays there for all of the segment's rows, 16 at a
 // time, if that is all.  No LDS and no barrier until the waves' sums meet, in
 // wave order.  Any K >= 8, N and alignment: global loads take 2-byte aligned
-// addresses, and the part past K is masked.  Bound by B's bytes: 16 rows over 8
-// segments of 4096 x 2048, 135 MB, in 31 us (4.3 TB/s; a large copy reaches 4.9).
+// addresses, and the part past K is masked.  Bound by B's bytes and a short
+// launch's ramp: 1 row, 904 x 3280, 5.9 MB, in 6.2 us.
 //
 // Rows lo, lo + step, .. (16 from each) below hi, columns n0 .. n0 + 15 of
 // segment g.  store(r, n, sum): sum holds columns n .. n + 3 of row r, zeros

@@ -448,7 +448,7 @@ constexpr int lora_lds() {
 // MFMAs of this one; U_s comes through registers two K-tiles ahead, and is
 // split and written an element at a time between the MFMAs.
 //
-// 4096 rows, 4096 x 4096, 8 adapters of rank 64 in runs: 135 us against 104
+// 4096 rows, 4096 x 4096, 8 adapters of rank 64 in runs: 133 us against 104
 // without adapters; a tile across three adapters does six such K-tiles of 5
 // MFMAs per block beside its 64 of 2.
 template <class C, bool RANK4>

@@ -204,20 +204,22 @@ static int tn_splits(int64_t rows, int64_t groups, int64_t n, int64_t k) {
 // fp32 elements of a part: whole 16-byte chunks.
 static int64_t tn_part_elems(int64_t groups, int64_t n, int64_t k) { return cdiv64(groups * n * k, 4) * 4; }
 
-// Whether a grouped NT product takes the few-row kernel: up to 16 rows per
-// segment, and too few 32 x 64 tiles to fill the CUs, where its waves'
-// share of K is what keeps loads in flight (1 row, 904 x 3280: 6.3 us
-// against the ring's 12.6; 10 rows over 10 segments of 608 x 2032: 8.4
-// against 10.8).  With more tiles the ring is level or faster (45 rows, 4
-// segments of 3056 x 2520: 13.1 against 19.5), except for a handful of rows
-// where every wave has whole passes of 256 elements and two workgroups share
-// a CU (16 rows over 8 segments of 4096 x 2048: 31 against 35.5).  Rows that
-// cannot go straight into LDS have no ring to go to.
+// Up to 16 rows per segment, where B's bytes bound an NT product: the few-row
+// kernel while the ring's 32 x 64 tiles would be too few to fill the CUs, for
+// its waves' share of K is what keeps loads in flight then (1 row, 904 x 3280:
+// 6.3 us against the ring's 12.6; 10 rows over 10 segments of 608 x 2032: 8.4
+// against 10.8), else the ring (16 rows over 8 segments of 4096 x 2048: 28.9
+// against 31.6; 45 rows, 4 segments of 3056 x 2520: 13.1 against 19.5).  On 327
+// shapes of more than 176 tiles (1 to 16 rows in each of 2 to 64 segments, N from 1024 to
+// 8192, K from 256 to 8192) the ring took 1.010 of the fastest kernel's time in
+// the geometric mean and 1.17 at most; pick_plan, whose fit does not tell the ring from a
+// 32 x 128 tile there, 1.06 and 1.38.  Rows that cannot go straight into LDS
+// have no ring to go to.
+static bool byte_bound(const SegParams &p) { return p.rows <= 16 * std::min<int64_t>(p.groups, p.rows); }
+
 static bool few_rows(const SegParams &p, bool direct) {
     const int64_t segments = std::min<int64_t>(p.groups, p.rows);
-    if (p.k < 8 || p.rows > 16 * segments) return false;
-    return !direct || segments * cdiv64(p.n, 64) <= 176 ||
-           (p.rows <= 4 * segments && p.k % 256 == 0 && p.k >= 1024 && p.k <= 2048);
+    return p.k >= 8 && byte_bound(p) && (!direct || segments * cdiv64(p.n, 64) <= 176);
 }
 
 static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k, const void *a, int64_t a_rows,
@@ -274,6 +276,8 @@ static int grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k,
         q.h = static_cast<const float *>(workspace);
         return status(launch_seg_join(out_f32 != 0, q, (hipStream_t)stream));
     }
+    if (direct && kind == kSegNT && byte_bound(p))
+        return status(launch_seg_nt(kSegRing, out_f32 != 0, p, (hipStream_t)stream));
     if (direct) {
         const SegPlan plan = pick_plan(kind, out_f32 != 0, p, cus);
         const int tile = plan.tile;
