@@ -360,8 +360,9 @@ __device__ __forceinline__ void seg_store(const floatx4 (&acc)[C::FN][C::FM], ch
 // and take 146.
 //
 // An infinity or NaN in U_s would reach the rows of other adapters as
-// 0 * inf: it is taken as 0 here, and lora_wild adds its products to the
-// rows of its adapter afterwards.  An infinity in h has to give u * inf, so it
+// 0 * inf: it is taken as 1 of its sign here (not as 0: h may be infinite
+// there), and lora_wild adds its products, none of them finite, to the rows of
+// its adapter afterwards.  An infinity in h has to give u * inf, so it
 // travels as h2, which meets u0 alone: u's sign, and 0 where u is 0 (times
 // u1, of 0 or the other sign, it would be a NaN).
 
@@ -516,7 +517,7 @@ __device__ __forceinline__ bool lora_tiles(floatx4 (&acc)[C::FN][C::FM], char *s
         constexpr int i = decltype(e_c)::value / 8, e = decltype(e_c)::value % 8;
         float v = (float)__builtin_bit_cast(half8, u[i])[e];
         if (!(fabsf(v) < __builtin_inff())) {
-            v = 0.0f;
+            v = copysignf(1.0f, v);
             wild = 1;
         }
         top[e] = (__bf16)v;

@@ -122,3 +122,19 @@ def test_adapters_many_to_a_tile_are_exact(rows, adapters, rank, n, k):
     want, _ = ref.lora(*t, ids, None)
     assert float(want.abs().max()) <= 2048  # whole numbers that fp16 holds
     assert torch.equal(g.gemm_f16_lora_nt(*t, ids, order, off), want.half())
+
+
+@pytest.mark.parametrize("rows, n, k, rank", FORMS)
+def test_an_infinite_inner_product_meets_an_infinite_weight(rows, n, k, rank):
+    """inf * inf is inf: not what 0 or a finite stand-in for either gives."""
+    x, w, down, up, ids = _one_adapter(rows, n, k, rank)
+    x[:, 0], w[:, 0] = 1.0, 2.0
+    down[0, :, 0] = 0.5
+    down[0, 2, 0] = float("inf")
+    up[0] = 0.25
+    up[0, :, 2] = float("inf")
+    up[0, 1::2, 2] = float("-inf")
+    x[rows // 2:, 0] = -1.0
+    out = _call(x, w, down, up, ids)
+    sign = x[:, :1].float() * torch.where(torch.arange(n, device="cuda") % 2 == 0, 1.0, -1.0)
+    assert torch.equal(out.float(), sign * float("inf"))
