@@ -10,7 +10,8 @@ adapter).
 
 Every call is asynchronous on ``stream`` (default: torch's current stream),
 never waits for the GPU and captures into HIP graphs.  Outputs and the
-workspace are allocated on that stream.  The arguments' contracts are those of
+workspace are allocated on that stream; for operands of another one the caller
+orders the streams and keeps the tensors (``record_stream``).  The arguments' contracts are those of
 ``include/gemm_f16.h``; shapes, types and devices are checked here, and a
 status of the library raises ``GemmError``.
 """
