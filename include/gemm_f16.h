@@ -281,6 +281,7 @@ int64_t gemm_f16_grouped_tn_workspace(int64_t rows, int64_t groups, int64_t n, i
  *   down     fp16 [adapters,rank,K]   up  fp16 [adapters,N,rank]
  *   ids      int32 [rows]: the adapter of each row; outside [0, adapters): none
  *   order, offsets   of gemm_f16_group_rows(rows, adapters, ids, ...)
+ *            (past its 2048 groups: any stable sort of the rows by adapter)
  *   scale    fp32 [adapters], or NULL for ones
  *   y        fp16 [rows,N]
  *
