@@ -1,7 +1,9 @@
 """MI355X (gfx950) fp16 GEMM: C = fp16(A @ B^T) with fp32 accumulation, and the
 second contract D = A @ B (B [K,N], fp32 out).  Beside them the segmented
 products (segments.py): row grouping, products grouped by expert with their
-gradients, and low-rank adapters.
+gradients, and low-rank adapters; and the feed-forward layer around them
+(feedforward.py): a product with bias, activation and residual, the routing to
+experts and the way back, with their gradients.
 
 Thin ctypes binding over ``libgemm_f16.so`` (C ABI declared in
 ``include/gemm_f16.h``).  This module only marshals arguments: shapes,
@@ -65,6 +67,14 @@ EXPORTS = (
     "gemm_f16_grouped_tn_ws",
     "gemm_f16_lora_nt",
     "gemm_f16_lora_workspace",
+    "gemm_f16_fused_nt",
+    "gemm_f16_fused_workspace",
+    "gemm_f16_fused_grad",
+    "gemm_f16_fused_grad_workspace",
+    "gemm_f16_route",
+    "gemm_f16_route_grad",
+    "gemm_f16_combine_rows",
+    "gemm_f16_combine_rows_grad",
 )
 
 
@@ -132,6 +142,22 @@ def _declare(L: ctypes.CDLL) -> ctypes.CDLL:
     L.gemm_f16_lora_nt.restype = ctypes.c_int
     L.gemm_f16_lora_workspace.argtypes = [i64, i64, i64, i64, i64]
     L.gemm_f16_lora_workspace.restype = i64
+    L.gemm_f16_fused_nt.argtypes = [i64, i64, i64, p, p, p, p, p, i64, p]
+    L.gemm_f16_fused_nt.restype = ctypes.c_int
+    L.gemm_f16_fused_workspace.argtypes = [i64, i64, i64]
+    L.gemm_f16_fused_workspace.restype = i64
+    L.gemm_f16_fused_grad.argtypes = [i64, i64, p, i32, p, i32, p, p, p, i64, p]
+    L.gemm_f16_fused_grad.restype = ctypes.c_int
+    L.gemm_f16_fused_grad_workspace.argtypes = [i64, i64]
+    L.gemm_f16_fused_grad_workspace.restype = i64
+    L.gemm_f16_route.argtypes = [i64, i64, i64, p, i32, p, p, p, p, p]
+    L.gemm_f16_route.restype = ctypes.c_int
+    L.gemm_f16_route_grad.argtypes = [i64, i64, i64, p, i32, p, p, p, p, p]
+    L.gemm_f16_route_grad.restype = ctypes.c_int
+    L.gemm_f16_combine_rows.argtypes = [i64, i64, i64, i64, p, i32, p, p, p, p, p, i32, p]
+    L.gemm_f16_combine_rows.restype = ctypes.c_int
+    L.gemm_f16_combine_rows_grad.argtypes = [i64, i64, i64, i64, p, i32, p, i32, p, p, p, p, i32, p, p]
+    L.gemm_f16_combine_rows_grad.restype = ctypes.c_int
     return L
 
 
@@ -244,3 +270,5 @@ def select_xcd(num_m: int, num_n: int, swizzle: int = 4, cus: int = 256) -> int:
 
 from .segments import (  # noqa: E402
     gemm_f16_grouped_nn, gemm_f16_grouped_nt, gemm_f16_grouped_tn, gemm_f16_lora_nt, group_rows)
+from .feedforward import (  # noqa: E402
+    combine_rows, combine_rows_grad, gemm_f16_fused_grad, gemm_f16_fused_nt, route, route_grad)

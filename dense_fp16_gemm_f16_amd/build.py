@@ -48,10 +48,13 @@ HIPCC_FLAGS = [
 
 def sources() -> list[str]:
     """Translation units of libgemm_f16.so: the host side, one per block tile, one
-    per block tile of the ring kernel's variants and the segmented products'."""
+    per block tile of the ring kernel's variants, the segmented products' and the
+    feed-forward layer's."""
     return ([os.path.join(CSRC, "gemm_f16.hip")] + sorted(glob.glob(os.path.join(CSRC, "tile_*.hip")))
             + sorted(glob.glob(os.path.join(CSRC, "ring_*.hip")))
-            + [os.path.join(CSRC, "segments.hip")] + sorted(glob.glob(os.path.join(CSRC, "seg_*.hip"))))
+            + [os.path.join(CSRC, "segments.hip")] + sorted(glob.glob(os.path.join(CSRC, "seg_*.hip")))
+            + [os.path.join(CSRC, "feedforward.hip"), os.path.join(CSRC, "route.hip"), os.path.join(CSRC, "combine.hip")]
+            + sorted(glob.glob(os.path.join(CSRC, "fused_*.hip"))))
 
 
 def _hipcc() -> str:

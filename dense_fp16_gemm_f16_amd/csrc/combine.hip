@@ -1,0 +1,162 @@
+// The way back from the experts: their rows, sorted by expert, weighted and summed into their
+// tokens, and the gradient.
+//
+//   y[t] = residual[t] + sum_f gates[t, f] rows[inverse[t, f]]
+//   drows[inverse[t, f]] = gates[t, f] dy[t],   dgates[t, f] = sum_n dy[t, n] rows[inverse[t, f], n]
+//
+// Places from *last on hold the rows of no expert: they add nothing whatever they hold, and
+// have zeros as their gradients.  Sums in fp32, over f in order.  Bound by bytes: every row
+// is read and written once, 16 bytes a lane.
+#include <algorithm>
+
+#include "fused.h"
+#include "route.h"
+
+namespace gemm_f16 {
+
+constexpr int kCombineThreads = 256;
+
+// Place of routed row r: -1 where it is out of range, so no content of inverse leads there.
+__device__ __forceinline__ int64_t place_of(const CombineParams &p, int64_t r) {
+    const int64_t at = p.inverse[r];
+    return at >= 0 && at < p.places ? at : -1;
+}
+
+// 8 columns of a row (n < p.n), those past the last 0.
+__device__ __forceinline__ void load_cols(const CombineParams &p, const void *from, bool f32, int64_t row, int n, float (&v)[8]) {
+    const int64_t at = row * p.n + n;
+    if (p.vec) {
+        load_row(from, f32, at, v);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = n + e < p.n ? load1(from, f32, at + e) : 0.0f;
+    }
+}
+
+__device__ __forceinline__ void store_cols(const CombineParams &p, void *to, bool f32, int64_t row, int n, const float (&v)[8]) {
+    const int64_t at = row * p.n + n;
+    if (p.vec) {
+        store_row(to, f32, at, v, kStoreDefault);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (n + e >= p.n) continue;
+            if (f32)
+                static_cast<float *>(to)[at + e] = v[e];
+            else
+                static_cast<_Float16 *>(to)[at + e] = (_Float16)v[e];
+        }
+    }
+}
+
+// 2^LOG threads a token, 8 columns each at a time; B rows in flight.
+template <int B>
+__global__ __launch_bounds__(kCombineThreads) void combine_kernel(const CombineParams p, int log) {
+    const int64_t token = p.first + ((int64_t)blockIdx.x << (8 - log)) + (threadIdx.x >> log);
+    if (token >= p.tokens) return;
+    const int step = 8 << log, last = *p.last;
+    for (int n = ((int)threadIdx.x & ((1 << log) - 1)) * 8; n < p.n; n += step) {
+        float y[8] = {};
+        if (p.residual) load_cols(p, p.residual, p.y_f32 != 0, token, n, y);
+        for (int f0 = 0; f0 < p.fan; f0 += B) {
+            float v[B][8], gate[B];
+            bool live[B];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                live[b] = false;
+                if (f0 + b >= p.fan) continue;
+                const int64_t r = token * p.fan + f0 + b, at = place_of(p, r);
+                live[b] = at >= 0 && at < last;
+                gate[b] = p.gates ? p.gates[r] : 1.0f;
+                if (live[b]) load_cols(p, p.rows, p.rows_f32 != 0, at, n, v[b]);
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                if (!live[b]) continue;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(gate[b], v[b][e], y[e]);
+            }
+        }
+        store_cols(p, p.y, p.y_f32 != 0, token, n, y);
+    }
+}
+
+// A wave a token: dy once, B of the token's rows at a time.
+template <int B>
+__global__ __launch_bounds__(kCombineThreads) void combine_grad_kernel(const CombineParams p, int) {
+    const int lane = threadIdx.x % kWave;
+    const int64_t token = p.first + (int64_t)blockIdx.x * (kCombineThreads / kWave) + threadIdx.x / kWave;
+    if (token >= p.tokens) return;
+    const int last = *p.last;
+    for (int f0 = 0; f0 < p.fan; f0 += B) {
+        int64_t at[B];
+        float gate[B], dot[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            at[b] = -1;
+            gate[b] = dot[b] = 0.0f;
+            if (f0 + b >= p.fan) continue;
+            const int64_t r = token * p.fan + f0 + b;
+            at[b] = place_of(p, r);
+            if (at[b] < last) gate[b] = p.gates ? p.gates[r] : 1.0f;
+        }
+        for (int n = lane * 8; n < p.n; n += kWave * 8) {
+            float dy[8], v[B][8];
+            load_cols(p, p.y, p.y_f32 != 0, token, n, dy);
+            if (p.dgates) {
+#pragma unroll
+                for (int b = 0; b < B; ++b)
+                    if (at[b] >= 0 && at[b] < last) load_cols(p, p.rows, p.rows_f32 != 0, at[b], n, v[b]);
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                if (at[b] < 0) continue;
+                const bool live = at[b] < last;
+                float d[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    d[e] = live ? gate[b] * dy[e] : 0.0f;
+                    if (p.dgates && live) dot[b] = __builtin_fmaf(dy[e], v[b][e], dot[b]);
+                }
+                if (p.drows) store_cols(p, p.drows, p.drows_f32 != 0, at[b], n, d);
+            }
+        }
+        if (!p.dgates) continue;
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+#pragma unroll
+            for (int d = 1; d < kWave; d <<= 1) dot[b] += __shfl_xor(dot[b], d);
+            if (lane == 0 && f0 + b < p.fan) p.dgates[token * p.fan + f0 + b] = dot[b];
+        }
+    }
+}
+
+// `per` tokens a workgroup; a launch holds fewer than 2^32 threads.
+static hipError_t launch(const void *kernel, CombineParams p, int per, int log, hipStream_t s) {
+    constexpr int64_t kMost = ((int64_t(1) << 32) - 1) / kCombineThreads;
+    void *args[] = {&p, &log};
+    for (int64_t at = 0, all = (p.tokens + per - 1) / per; at < all; at += kMost) {
+        p.first = at * per;
+        const hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)std::min(kMost, all - at)), dim3(kCombineThreads), args, 0, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_combine(const CombineParams &p, hipStream_t s) {
+    int log = 3;  // threads a token: its chunks of 8 columns, or a workgroup
+    while (log < 8 && (8 << log) < p.n) ++log;
+    const void *kernel = p.fan <= 2   ? reinterpret_cast<const void *>(combine_kernel<2>)
+                         : p.fan <= 4 ? reinterpret_cast<const void *>(combine_kernel<4>)
+                                      : reinterpret_cast<const void *>(combine_kernel<8>);
+    return launch(kernel, p, kCombineThreads >> log, log, s);
+}
+
+hipError_t launch_combine_grad(const CombineParams &p, hipStream_t s) {
+    const void *kernel = p.fan <= 1   ? reinterpret_cast<const void *>(combine_grad_kernel<1>)
+                         : p.fan <= 2 ? reinterpret_cast<const void *>(combine_grad_kernel<2>)
+                                      : reinterpret_cast<const void *>(combine_grad_kernel<4>);
+    return launch(kernel, p, kCombineThreads / kWave, 0, s);
+}
+
+}  // namespace gemm_f16

@@ -1,0 +1,345 @@
+// Host side of the feed-forward layer's operators: argument checks, the choice of kernel and
+// the launches (see fused.h and route.h).
+#include <algorithm>
+
+#include "checks.h"
+#include "device.h"
+#include "fused.h"
+#include "gemm_f16.h"
+#include "route.h"
+
+namespace gemm_f16 {
+
+constexpr int64_t kMaxSide = int64_t(1) << 30, kMaxDepth = int64_t(1) << 22, kMaxArea = int64_t(1) << 47;
+
+static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+static bool aligned16(const void *p) { return (uintptr_t)p % 16 == 0; }
+
+static int check_fused(int64_t m, int64_t n, int64_t k) {
+    if (m < 0 || n < 0 || k < 0 || m >= kMaxSide || n >= kMaxSide || k >= kMaxDepth) return GEMM_F16_EINVAL;
+    return below(kMaxArea, m, n) ? GEMM_F16_OK : GEMM_F16_EINVAL;
+}
+
+static bool fused_is_few(int64_t m, int64_t k) { return m <= kFusedFewRows && k >= 8; }
+
+struct TileSize {
+    int bm, bn;
+};
+
+static TileSize tile_size(int tile) {
+    switch (tile) {
+        case GEMM_F16_TILE_256x256: return {256, 256};
+        case GEMM_F16_TILE_256x128: return {256, 128};
+        case GEMM_F16_TILE_128x256: return {128, 256};
+        case GEMM_F16_TILE_128x128: return {128, 128};
+        case GEMM_F16_TILE_128x64: return {128, 64};
+        case GEMM_F16_TILE_64x128: return {64, 128};
+        default: return {64, 64};
+    }
+}
+
+static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, void *c, const gemm_f16_epilogue &e,
+                 void *workspace, int64_t workspace_bytes, hipStream_t s) {
+    int rc = check_fused(m, n, k);
+    if (rc != GEMM_F16_OK) return rc;
+    if (e.act < GEMM_F16_ACT_NONE || e.act > GEMM_F16_ACT_LAST || e.bias_f32 < 0 || e.bias_f32 > 1 || e.out_f32 < 0 ||
+        e.out_f32 > 1)
+        return GEMM_F16_EINVAL;
+    const int64_t need = gemm_f16_fused_workspace(m, n, k);
+    if (workspace_bytes < need) return GEMM_F16_EINVAL;
+    if (m == 0 || n == 0) return GEMM_F16_OK;
+    const int es = e.out_f32 ? 4 : 2, bs = e.bias_f32 ? 4 : 2;
+    // C may be the residual itself: each element is read and written by one thread
+    const bool in_place = e.residual == c;
+    const Buffer bufs[] = {{c, m * n * es, es, true},
+                           {e.pre, e.pre ? m * n * 2 : 0, 2, true},
+                           {workspace, need, 16, true},
+                           {a, m * k * 2, 2, false},
+                           {b, n * k * 2, 2, false},
+                           {e.bias, e.bias ? n * bs : 0, bs, false},
+                           {e.residual, e.residual && !in_place ? m * n * es : 0, es, false}};
+    rc = check_buffers(bufs);
+    if (rc != GEMM_F16_OK) return rc;
+    int cus;
+    rc = current_device(&cus);
+    if (rc != GEMM_F16_OK) return rc;
+
+    FusedParams p = {};
+    p.a = static_cast<const _Float16 *>(a);
+    p.b = static_cast<const _Float16 *>(b);
+    p.c = c;
+    p.m = (int32_t)m;
+    p.n = (int32_t)n;
+    p.k = (int32_t)k;
+    p.k_tiles = p.part_kt = (int32_t)cdiv(k, 64);
+    p.parts = 1;
+    p.bias = e.bias;
+    p.residual = e.residual;
+    p.pre = static_cast<_Float16 *>(e.pre);
+    p.sums = static_cast<float *>(workspace);
+    p.act = e.act;
+    p.bias_f32 = e.bias_f32;
+    p.out_f32 = e.out_f32;
+    p.vec = n % 8 == 0 && aligned16(c) && aligned16(e.bias) && aligned16(e.residual) && aligned16(e.pre);
+    // as the dense product's: device scope while everything fits in the 256 MiB Infinity
+    // Cache, past it streaming stores on rows of whole 128-byte lines
+    const int64_t each = es * (e.residual ? 2 : 1) + (e.pre ? 2 : 0);
+    p.c_store = (m + n) * k * 2 + m * n * each <= (int64_t(256) << 20)             ? kStoreDevice
+                : (n * es) % 128 == 0 && (uintptr_t)c % 128 == 0 ? kStoreStream
+                                                                                   : kStoreDefault;
+    if (k == 0) {
+        p.parts = 0;
+        return status(launch_fused_join(p, s));
+    }
+    if (fused_is_few(m, k)) return status(launch_fused_few(p, s));
+    const bool direct = k % 8 == 0 && aligned16(a) && aligned16(b);
+    int tile = gemm_f16_select_tile(m, n, k);
+    if (tile < 0) return tile;
+    if (!direct) {
+        const bool wide = tile != GEMM_F16_TILE_64x64;
+        tile = wide ? GEMM_F16_TILE_128x128 : GEMM_F16_TILE_64x64;
+    }
+    const TileSize ts = tile_size(tile);
+    p.num_m = (int32_t)cdiv(m, ts.bm);
+    p.num_n = (int32_t)cdiv(n, ts.bn);
+    if ((int64_t)p.num_m * p.num_n >= (int64_t(1) << 31)) return GEMM_F16_EINVAL;
+    p.swizzle = 4;
+    p.xcd = gemm_f16_select_xcd(p.num_m, p.num_n, p.swizzle, cus);
+    if (!direct) return status(launch_fused_staged(tile == GEMM_F16_TILE_128x128, p, s));
+    switch (tile) {
+        case GEMM_F16_TILE_256x256: return status(launch_fused_256x256(p, s));
+        case GEMM_F16_TILE_256x128: return status(launch_fused_256x128(p, s));
+        case GEMM_F16_TILE_128x256: return status(launch_fused_128x256(p, s));
+        case GEMM_F16_TILE_128x128: return status(launch_fused_128x128(p, s));
+        case GEMM_F16_TILE_128x64: return status(launch_fused_128x64(p, s));
+        case GEMM_F16_TILE_64x128: return status(launch_fused_64x128(p, s));
+        default: return status(launch_fused_64x64(p, s));
+    }
+}
+
+static int check_routing(int64_t tokens, int64_t experts, int64_t fan, int32_t logits_f32, const gemm_f16_routing *r) {
+    if (!r) return GEMM_F16_ENULL;
+    if (tokens < 0 || tokens >= kMaxSide || experts < 1 || experts > kRouteExperts || fan < 1 || fan > kRouteFan ||
+        fan > experts || logits_f32 < 0 || logits_f32 > 1)
+        return GEMM_F16_EINVAL;
+    if (r->score < GEMM_F16_SCORE_SOFTMAX || r->score > GEMM_F16_SCORE_SIGMOID || r->renormalize < 0 || r->renormalize > 1 ||
+        !(r->scale - r->scale == 0.0f))
+        return GEMM_F16_EINVAL;
+    return GEMM_F16_OK;
+}
+
+static RouteParams route_params(int64_t tokens, int64_t experts, int64_t fan, const void *logits, int32_t logits_f32,
+                                const gemm_f16_routing &r) {
+    RouteParams p = {};
+    p.logits = logits;
+    p.tokens = tokens;
+    p.experts = (int32_t)experts;
+    p.fan = (int32_t)fan;
+    p.f32 = logits_f32;
+    p.sigmoid = r.score == GEMM_F16_SCORE_SIGMOID;
+    p.renormalize = r.renormalize;
+    p.scale = r.scale;
+    p.groups = p.top_groups = p.group_top = 1;
+    p.vec = experts % 4 == 0 && aligned16(logits);
+    return p;
+}
+
+static int check_combine(int64_t tokens, int64_t fan, int64_t n) {
+    if (tokens < 0 || fan < 1 || n < 0 || tokens >= kMaxSide || fan >= kMaxSide || n >= kMaxSide) return GEMM_F16_EINVAL;
+    if (!below(kMaxSide, tokens, fan) || !below(kMaxArea, tokens * fan, n)) return GEMM_F16_EINVAL;
+    return GEMM_F16_OK;
+}
+
+}  // namespace gemm_f16
+
+using namespace gemm_f16;
+
+extern "C" {
+
+int64_t gemm_f16_fused_workspace(int64_t m, int64_t n, int64_t k) {
+    const int rc = check_fused(m, n, k);
+    return rc != GEMM_F16_OK ? rc : 0;
+}
+
+int gemm_f16_fused_nt(int64_t m, int64_t n, int64_t k, const void *a, const void *b, void *c,
+                      const gemm_f16_epilogue *epilogue, void *workspace, int64_t workspace_bytes, void *stream) {
+    static const gemm_f16_epilogue none = {};
+    return fused(m, n, k, a, b, c, epilogue ? *epilogue : none, workspace, workspace_bytes, (hipStream_t)stream);
+}
+
+int64_t gemm_f16_fused_grad_workspace(int64_t m, int64_t n) {
+    const int rc = check_fused(m, n, 0);
+    if (rc != GEMM_F16_OK) return rc;
+    const int parts = m > 0 && n > 0 ? fused_grad_parts(m, n) : 1;
+    return parts > 1 ? parts * n * 4 : 0;
+}
+
+int gemm_f16_fused_grad(int64_t m, int64_t n, const void *dy, int32_t dy_f32, const void *pre, int32_t act, void *dz,
+                        float *dbias, void *workspace, int64_t workspace_bytes, void *stream) {
+    int rc = check_fused(m, n, 0);
+    if (rc != GEMM_F16_OK) return rc;
+    if (act < GEMM_F16_ACT_NONE || act > GEMM_F16_ACT_LAST || dy_f32 < 0 || dy_f32 > 1) return GEMM_F16_EINVAL;
+    const int64_t need = dbias ? gemm_f16_fused_grad_workspace(m, n) : 0;
+    if (workspace_bytes < need) return GEMM_F16_EINVAL;
+    if (n == 0 || (!dz && !dbias) || (m == 0 && !dbias)) return GEMM_F16_OK;
+    const int ds = dy_f32 ? 4 : 2;
+    // dz may be dy itself, where both are fp16: each element is read and written by one thread
+    const bool in_place = dz == dy && !dy_f32;
+    const Buffer bufs[] = {{dz, dz ? m * n * 2 : 0, 2, true},
+                           {dbias, dbias ? n * 4 : 0, 4, true},
+                           {workspace, need, 16, true},
+                           {dy, in_place ? 0 : m * n * ds, ds, false},
+                           {pre, act != GEMM_F16_ACT_NONE ? m * n * 2 : 0, 2, false}};
+    rc = check_buffers(bufs);
+    if (rc != GEMM_F16_OK) return rc;
+    int cus;
+    rc = current_device(&cus);
+    if (rc != GEMM_F16_OK) return rc;
+    FusedGradParams p = {};
+    p.dy = dy;
+    p.pre = static_cast<const _Float16 *>(pre);
+    p.dz = static_cast<_Float16 *>(dz);
+    p.dbias = dbias;
+    p.sums = static_cast<float *>(workspace);
+    p.m = m;
+    p.n = n;
+    p.act = act;
+    p.dy_f32 = dy_f32;
+    p.vec = n % 8 == 0 && aligned16(dy) && aligned16(dz) && (act == GEMM_F16_ACT_NONE || aligned16(pre));
+    p.parts = m > 0 ? fused_grad_parts(m, n) : 1;
+    return status(launch_fused_grad(p, (hipStream_t)stream));
+}
+
+int gemm_f16_route(int64_t tokens, int64_t experts, int64_t fan, const void *logits, int32_t logits_f32, const float *bias,
+                   const gemm_f16_routing *routing, int32_t *ids, float *gates, void *stream) {
+    int rc = check_routing(tokens, experts, fan, logits_f32, routing);
+    if (rc != GEMM_F16_OK) return rc;
+    const gemm_f16_routing &r = *routing;
+    if (r.groups < 1 || r.groups > kRouteGroups || experts % r.groups != 0 || r.top_groups < 1 || r.top_groups > r.groups ||
+        r.group_top < 1 || r.group_top > 2 || fan > experts / r.groups * r.top_groups)
+        return GEMM_F16_EINVAL;
+    if (tokens == 0) return GEMM_F16_OK;
+    const int es = logits_f32 ? 4 : 2;
+    const Buffer bufs[] = {{ids, tokens * fan * 4, 4, true},
+                           {gates, tokens * fan * 4, 4, true},
+                           {logits, tokens * experts * es, es, false},
+                           {bias, bias ? experts * 4 : 0, 4, false}};
+    rc = check_buffers(bufs);
+    if (rc != GEMM_F16_OK) return rc;
+    int cus;
+    rc = current_device(&cus);
+    if (rc != GEMM_F16_OK) return rc;
+    RouteParams p = route_params(tokens, experts, fan, logits, logits_f32, r);
+    p.bias = bias;
+    p.ids = ids;
+    p.gates = gates;
+    p.groups = r.groups;
+    p.top_groups = r.top_groups;
+    p.group_top = r.group_top;
+    return status(launch_route(p, (hipStream_t)stream));
+}
+
+int gemm_f16_route_grad(int64_t tokens, int64_t experts, int64_t fan, const void *logits, int32_t logits_f32,
+                        const int32_t *ids, const float *dgates, const gemm_f16_routing *routing, void *dlogits,
+                        void *stream) {
+    int rc = check_routing(tokens, experts, fan, logits_f32, routing);
+    if (rc != GEMM_F16_OK) return rc;
+    if (tokens == 0) return GEMM_F16_OK;
+    const int es = logits_f32 ? 4 : 2;
+    const Buffer bufs[] = {{dlogits, tokens * experts * es, es, true},
+                           {logits, tokens * experts * es, es, false},
+                           {ids, tokens * fan * 4, 4, false},
+                           {dgates, tokens * fan * 4, 4, false}};
+    rc = check_buffers(bufs);
+    if (rc != GEMM_F16_OK) return rc;
+    int cus;
+    rc = current_device(&cus);
+    if (rc != GEMM_F16_OK) return rc;
+    RouteParams p = route_params(tokens, experts, fan, logits, logits_f32, *routing);
+    p.ids = const_cast<int32_t *>(ids);
+    p.dgates = dgates;
+    p.dlogits = dlogits;
+    p.vec = p.vec && aligned16(dlogits);
+    return status(launch_route_grad(p, (hipStream_t)stream));
+}
+
+int gemm_f16_combine_rows(int64_t tokens, int64_t fan, int64_t n, int64_t groups, const void *rows, int32_t rows_f32,
+                          const int32_t *inverse, const int32_t *offsets, const float *gates, const void *residual, void *y,
+                          int32_t y_f32, void *stream) {
+    int rc = check_combine(tokens, fan, n);
+    if (rc != GEMM_F16_OK) return rc;
+    if (groups < 1 || groups >= kMaxSide || rows_f32 < 0 || rows_f32 > 1 || y_f32 < 0 || y_f32 > 1) return GEMM_F16_EINVAL;
+    if (tokens == 0 || n == 0) return GEMM_F16_OK;
+    const int rs = rows_f32 ? 4 : 2, ys = y_f32 ? 4 : 2;
+    const bool in_place = residual == y;  // each element is read and written by one thread
+    const Buffer bufs[] = {{y, tokens * n * ys, ys, true},
+                           {rows, tokens * fan * n * rs, rs, false},
+                           {inverse, tokens * fan * 4, 4, false},
+                           {offsets, (groups + 1) * 4, 4, false},
+                           {gates, gates ? tokens * fan * 4 : 0, 4, false},
+                           {residual, residual && !in_place ? tokens * n * ys : 0, ys, false}};
+    rc = check_buffers(bufs);
+    if (rc != GEMM_F16_OK) return rc;
+    int cus;
+    rc = current_device(&cus);
+    if (rc != GEMM_F16_OK) return rc;
+    CombineParams p = {};
+    p.rows = rows;
+    p.inverse = inverse;
+    p.last = offsets + groups;
+    p.gates = gates;
+    p.residual = residual;
+    p.y = y;
+    p.tokens = tokens;
+    p.places = tokens * fan;
+    p.fan = (int32_t)fan;
+    p.n = (int32_t)n;
+    p.rows_f32 = rows_f32;
+    p.y_f32 = y_f32;
+    p.vec = n % 8 == 0 && aligned16(rows) && aligned16(y) && aligned16(residual);
+    return status(launch_combine(p, (hipStream_t)stream));
+}
+
+int gemm_f16_combine_rows_grad(int64_t tokens, int64_t fan, int64_t n, int64_t groups, const void *dy, int32_t dy_f32,
+                               const void *rows, int32_t rows_f32, const int32_t *inverse, const int32_t *offsets,
+                               const float *gates, void *drows, int32_t drows_f32, float *dgates, void *stream) {
+    int rc = check_combine(tokens, fan, n);
+    if (rc != GEMM_F16_OK) return rc;
+    if (groups < 1 || groups >= kMaxSide || dy_f32 < 0 || dy_f32 > 1 || rows_f32 < 0 || rows_f32 > 1 || drows_f32 < 0 ||
+        drows_f32 > 1)
+        return GEMM_F16_EINVAL;
+    if (tokens == 0 || (!drows && !dgates) || (n == 0 && !dgates)) return GEMM_F16_OK;
+    const int rs = rows_f32 ? 4 : 2, ys = dy_f32 ? 4 : 2, ds = drows_f32 ? 4 : 2;
+    const Buffer bufs[] = {{drows, drows ? tokens * fan * n * ds : 0, ds, true},
+                           {dgates, dgates ? tokens * fan * 4 : 0, 4, true},
+                           {dy, tokens * n * ys, ys, false},
+                           {rows, dgates ? tokens * fan * n * rs : 0, rs, false},
+                           {inverse, tokens * fan * 4, 4, false},
+                           {offsets, (groups + 1) * 4, 4, false},
+                           {gates, gates ? tokens * fan * 4 : 0, 4, false}};
+    rc = check_buffers(bufs);
+    if (rc != GEMM_F16_OK) return rc;
+    int cus;
+    rc = current_device(&cus);
+    if (rc != GEMM_F16_OK) return rc;
+    CombineParams p = {};
+    p.rows = rows;
+    p.inverse = inverse;
+    p.last = offsets + groups;
+    p.gates = gates;
+    p.y = const_cast<void *>(dy);
+    p.drows = drows;
+    p.dgates = dgates;
+    p.tokens = tokens;
+    p.places = tokens * fan;
+    p.fan = (int32_t)fan;
+    p.n = (int32_t)n;
+    p.rows_f32 = rows_f32;
+    p.y_f32 = dy_f32;
+    p.drows_f32 = drows_f32;
+    p.vec = n % 8 == 0 && aligned16(dy) && aligned16(drows) && (!dgates || aligned16(rows));
+    return status(launch_combine_grad(p, (hipStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,459 @@
+// C = act(A B^T + bias) + residual for gfx950: the dense product with what
+// follows it in a feed-forward layer taken into its epilogue, and the
+// elementwise part of its gradient.
+//
+// The K loops and LDS layouts are those of kernels.h; what is new is the way
+// out.  Everything behind the fp32 sum z = A B^T + bias stays in fp32 and C is
+// rounded once (nearest even); `pre` is z rounded to fp16, for the gradient.
+#pragma once
+
+#include "kernels.h"
+
+namespace gemm_f16 {
+
+// (GEMM_F16_ACT_* of gemm_f16.h)
+enum Act : int32_t { kActNone = 0, kActRelu = 1, kActGelu = 2, kActGeluTanh = 3, kActSilu = 4 };
+
+struct FusedParams : Params {
+    const void *bias;      // [n] fp16 or fp32, or null
+    const void *residual;  // [m, n] of C's type, or null; C itself, or apart from it
+    _Float16 *pre;         // [m, n] or null
+    float *sums;           // parts > 1: fp32 [parts][m, n], the parts' sums of A B^T
+    int32_t act, bias_f32, out_f32;
+    int32_t vec;           // rows in whole 16-byte chunks of 8 columns, everywhere
+    int32_t parts, part_kt;  // parts of K (1: none), of part_kt K-tiles each
+    uint32_t first;          // workgroups of this grid that earlier launches hold (launch_fused_grid)
+};
+
+// ---- activations ---------------------------------------------------------------
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ float sigmoid_f32(float x) {
+    // past the range of exp2 this is 0 or 1, as it should be
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(x * -kLog2e));
+}
+
+// gelu_tanh(z) = z / 2 (1 + tanh u) = z sigmoid(2 u), u = sqrt(2/pi) (z + 0.044715 z^3):
+// this form has no cancellation for negative z.
+constexpr float kGeluC0 = 1.5957691216057308f, kGeluC1 = 0.07135481282705285f;  // 2 sqrt(2/pi), times 0.044715
+
+// Phi(z) = erfc(-z / sqrt 2) / 2 and e = exp(-z^2 / 2).  For x = |z| the function
+// exp(x^2 / 2) Phi(-x) is smooth and falls like 1/x: a polynomial in t = 1 / (1 + 0.31 x)
+// without a constant term, fitted to it for least relative error over 0 <= x <= 15 (where
+// Phi(-x) leaves fp32), is off by 1.7e-7 of it, 4.8e-7 in fp32.  So the small values of
+// the lower tail keep their relative precision too.
+__device__ __forceinline__ float normal_cdf(float z, float &e) {
+    const float x = __builtin_fabsf(z);
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.31f, x, 1.0f));
+    e = __builtin_amdgcn_exp2f(x * x * (-0.5f * kLog2e));
+    float q = 0.035890500992536545f;
+    q = __builtin_fmaf(q, t, -0.14181861281394958f);
+    q = __builtin_fmaf(q, t, 0.15545809268951416f);
+    q = __builtin_fmaf(q, t, -0.015285272151231766f);
+    q = __builtin_fmaf(q, t, 0.11032592505216599f);
+    q = __builtin_fmaf(q, t, 0.10770097374916077f);
+    q = __builtin_fmaf(q, t, 0.12407241761684418f);
+    q = __builtin_fmaf(q, t, 0.12365606427192688f);
+    const float lower = q * t * e;
+    return z > 0.0f ? 1.0f - lower : lower;
+}
+
+// act(z), uniform over the launch.  What is not finite gives what the formula gives: -inf
+// is a NaN past relu and none (0 * inf), NaN stays NaN.
+template <int N>
+__device__ __forceinline__ void activate(int act, float (&z)[N]) {
+    switch (act) {
+        case kActRelu:
+#pragma unroll
+            for (int e = 0; e < N; ++e) z[e] = z[e] < 0.0f ? 0.0f : z[e];
+            break;
+        case kActGelu:
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                float gauss;
+                z[e] *= normal_cdf(z[e], gauss);
+            }
+            break;
+        case kActGeluTanh:
+#pragma unroll
+            for (int e = 0; e < N; ++e) z[e] *= sigmoid_f32(z[e] * __builtin_fmaf(kGeluC1, z[e] * z[e], kGeluC0));
+            break;
+        case kActSilu:
+#pragma unroll
+            for (int e = 0; e < N; ++e) z[e] *= sigmoid_f32(z[e]);
+            break;
+        default: break;
+    }
+}
+
+// ---- the way out ------------------------------------------------------------------
+
+// N (4 or 8) values of a row from element `at` on: fp16 or fp32, each chunk of them aligned.
+template <int N>
+__device__ __forceinline__ void load_row(const void *from, bool f32, int64_t at, float (&v)[N]) {
+    typedef _Float16 halfn __attribute__((ext_vector_type(N)));
+    if (f32) {
+        const floatx4 *q = reinterpret_cast<const floatx4 *>(static_cast<const float *>(from) + at);
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const floatx4 x = q[i];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[4 * i + e] = x[e];
+        }
+    } else {
+        const halfn x = *reinterpret_cast<const halfn *>(static_cast<const _Float16 *>(from) + at);
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = (float)x[e];
+    }
+}
+
+__device__ __forceinline__ float load1(const void *from, bool f32, int64_t at) {
+    return f32 ? static_cast<const float *>(from)[at] : (float)static_cast<const _Float16 *>(from)[at];
+}
+
+// 16 bytes under C's cache policy (CStore).
+__device__ __forceinline__ void store16(void *to, int4v v, int policy) {
+    if (policy == kStoreDevice)
+        store_device_scope(to, v);
+    else if (policy == kStoreStream)
+        __builtin_nontemporal_store(v, reinterpret_cast<int4v *>(to));
+    else
+        *reinterpret_cast<int4v *>(to) = v;
+}
+
+// N values rounded to fp16 (nearest even) or kept, an aligned chunk at a time.
+template <int N>
+__device__ __forceinline__ void store_row(void *to, bool f32, int64_t at, const float (&v)[N], int policy) {
+    typedef _Float16 halfn __attribute__((ext_vector_type(N)));
+    if (f32) {
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i)
+            store16(static_cast<float *>(to) + at + 4 * i,
+                    __builtin_bit_cast(int4v, floatx4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]}), policy);
+    } else {
+        halfn h;
+#pragma unroll
+        for (int e = 0; e < N; ++e) h[e] = (_Float16)v[e];
+        _Float16 *q = static_cast<_Float16 *>(to) + at;
+        if constexpr (N == 8)
+            store16(q, __builtin_bit_cast(int4v, h), policy);
+        else
+            *reinterpret_cast<halfn *>(q) = h;
+    }
+}
+
+// The bias of columns n .. n + N - 1, zeros past the last and without one.
+template <int N>
+__device__ __forceinline__ void load_bias(const FusedParams &p, int n, float (&b)[N]) {
+#pragma unroll
+    for (int e = 0; e < N; ++e) b[e] = 0.0f;
+    if (!p.bias || n >= p.n) return;
+    if (p.vec) {
+        load_row(p.bias, p.bias_f32 != 0, n, b);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (n + e < p.n) b[e] = load1(p.bias, p.bias_f32 != 0, n + e);
+    }
+}
+
+// The residual of row m, columns n .. n + N - 1 (n < p.n), where rows are in whole chunks.
+template <int N>
+__device__ __forceinline__ void load_residual(const FusedParams &p, int m, int n, float (&r)[N]) {
+    if (p.vec && p.residual) load_row(p.residual, p.out_f32 != 0, (int64_t)m * p.n + n, r);
+}
+
+// Row m, columns n .. n + N - 1 (n < p.n) of C from z, with r of load_residual (element by
+// element, the residual is read here).
+template <int N>
+__device__ __forceinline__ void finish_row(const FusedParams &p, int m, int n, float (&z)[N], const float (&r)[N]) {
+    const int64_t at = (int64_t)m * p.n + n;
+    if (p.vec) {
+        if (p.pre) store_row(p.pre, false, at, z, p.c_store);
+        activate(p.act, z);
+        if (p.residual) {
+#pragma unroll
+            for (int e = 0; e < N; ++e) z[e] += r[e];
+        }
+        store_row(p.c, p.out_f32 != 0, at, z, p.c_store);
+        return;
+    }
+    if (p.pre) {
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+            if (n + e < p.n) p.pre[at + e] = (_Float16)z[e];
+    }
+    activate(p.act, z);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        if (n + e >= p.n) continue;
+        const float v = p.residual ? z[e] + load1(p.residual, p.out_f32 != 0, at + e) : z[e];
+        if (p.out_f32)
+            static_cast<float *>(p.c)[at + e] = v;
+        else
+            static_cast<_Float16 *>(p.c)[at + e] = (_Float16)v;
+    }
+}
+
+// The workgroup's tile from its accumulators: fp32 through LDS, each wave its own piece in
+// its own share (CStaging's fp32 layout), then 8 consecutive columns a lane, so that the
+// bias is read once per wave and residual, pre and C move in whole 16-byte chunks of row
+// segments.  The loop is kept rolled: one copy of the epilogue's code, whatever the
+// activation.  Four rows' residuals are in flight at a time.
+template <class C, int kLds>
+__device__ __forceinline__ void fused_store_tile(const typename Mfma<C::MB>::Acc (&acc)[C::FN][C::FM], char *smem,
+                                                 const FusedParams &p, int m0, int n0, int wm, int wn, int wave,
+                                                 int lane) {
+    constexpr int kWaveBytes = kLds / C::kWaves;
+    using CS = CStaging<C, true, kWaveBytes>;
+    constexpr int CPL = C::TN / 8, RPI = kWave / CPL, IT = CS::SR / RPI, B = IT < 4 ? IT : 4;
+    static_assert(IT % B == 0 && IT * RPI == CS::SR, "whole batches of rows");
+    const int erow = CS::opaque_row(lane);
+    const int c8 = lane % CPL, n = n0 + wn * C::TN + 8 * c8;
+    float bias[8];
+    load_bias(p, n, bias);
+    lds_barrier();
+    char *const stg = smem + wave * (CS::SR * CS::RB);
+#pragma unroll
+    for (int pass = 0; pass < CS::kPasses; ++pass) {
+        CS::write_pass(acc, stg, pass, erow, lane);
+#pragma unroll 1
+        for (int it = 0; it < IT; it += B) {
+            float res[B][8];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int m = m0 + wm * C::TM + pass * CS::SR + (it + b) * RPI + lane / CPL;
+                if (p.parts == 1 && m < p.m && n < p.n) load_residual(p, m, n, res[b]);
+            }
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int r = (it + b) * RPI + lane / CPL, m = m0 + wm * C::TM + pass * CS::SR + r;
+                const char *row = stg + r * CS::RB;
+                const floatx4 x = *reinterpret_cast<const floatx4 *>(row + (((2 * c8) ^ (r % CS::CPR)) << 4));
+                const floatx4 y = *reinterpret_cast<const floatx4 *>(row + (((2 * c8 + 1) ^ (r % CS::CPR)) << 4));
+                if (m >= p.m || n >= p.n) continue;
+                if (p.parts > 1) {
+                    // this part's sums, each part in rows of its own
+                    float *s = p.sums + ((int64_t)blockIdx.y * p.m + m) * p.n + n;
+                    if (p.n % 4 == 0 && n + 7 < p.n) {
+                        *reinterpret_cast<floatx4 *>(s) = x;
+                        *reinterpret_cast<floatx4 *>(s + 4) = y;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (n + e < p.n) s[e] = e < 4 ? x[e & 3] : y[e & 3];
+                    }
+                    continue;
+                }
+                float z[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[e] = x[e] + bias[e], z[4 + e] = y[e] + bias[4 + e];
+                finish_row(p, m, n, z, res[b]);
+            }
+        }
+    }
+}
+
+// One block tile per workgroup, operands straight into LDS (16-byte aligned rows): the K
+// loop of gemm_f16_direct_ahead_kernel, two LDS stages, both k steps' fragments of K-tile
+// t+1 read during K-tile t, a release and an acquire barrier per K-tile.  With parts > 1
+// blockIdx.y is a part of K, whose sums leave in fp32 for fused_join_kernel.
+template <class C>
+__global__ __launch_bounds__(C::kThreads)
+__attribute__((amdgpu_waves_per_eu(C::kMinWavesPerEU, C::kMinWavesPerEU)))
+void fused_tile_kernel(const FusedParams p) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
+    constexpr int BM = C::BM, BN = C::BN;
+    constexpr int TM = C::TM, TN = C::TN, FM = C::FM, FN = C::FN;
+    static_assert(C::MB == 16 && C::KS == 2, "two 32-wide k steps per K-tile");
+    using OpA = KMajorDirect<C, BM, false>;
+    using OpB = KMajorDirect<C, BN, false>;
+    constexpr int kLdsB = OpA::kLdsBytes, kLds = OpA::kLdsBytes + OpB::kLdsBytes;
+    constexpr int LA = OpA::kLoads, L = OpA::kLoads + OpB::kLoads;
+    static_assert(kLds <= 160 * 1024 && 2 * L < 64, "LDS budget, vmcnt range");
+    __shared__ __attribute__((aligned(1024))) char smem[kLds];
+    GEMM_POISON_LDS(smem);
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    const TileCoord tc = tile_coord<uint32_t>(p.first + blockIdx.x, p.num_m, p.num_n, p.swizzle, p.xcd != 0);
+    const int m0 = (int)tc.m_block * BM, n0 = (int)tc.n_block * BN;
+    // this part's K-tiles: kt0 .. kt0 + kt_count - 1, from element k0 of every row
+    const int kt0 = (int)blockIdx.y * p.part_kt, kt_count = min(p.part_kt, p.k_tiles - kt0);
+    if (kt_count <= 0) return;  // never launched so
+
+    OpA opa;
+    OpB opb;
+    // (the descriptors end with the tile's last row: K-tiles start inside it)
+    opa.init(p.a + (int64_t)m0 * p.k, min(BM, p.m - m0), p.k, kt0 + kt_count, wave, lane, wm * TM, 0);
+    opb.init(p.b + (int64_t)n0 * p.k, min(BN, p.n - n0), p.k, kt0 + kt_count, wave, lane, wn * TN, kLdsB);
+
+    floatx4 acc[FN][FM];
+#pragma unroll
+    for (int j = 0; j < FN; ++j)
+#pragma unroll
+        for (int i = 0; i < FM; ++i) acc[j][i] = floatx4{};
+    acc_fence(acc);
+
+    half8 af[3][FM];
+    half8 bf[3][FN];
+    constexpr int NR = FM + FN;  // fragment reads per k step
+    // in the order the MFMAs consume them: B0, A0..A(FM-1), B1..
+    auto read_frag = [&](int buf, int stage, int ks, int r) {
+        if (r == 0)
+            bf[buf][0] = opb.read(smem, stage, ks, 0);
+        else if (r <= FM)
+            af[buf][r - 1] = opa.read(smem, stage, ks, r - 1);
+        else
+            bf[buf][r - FM] = opb.read(smem, stage, ks, r - FM);
+    };
+    auto load = [&](auto s_c, int t, int i) {
+        constexpr int S = decltype(s_c)::value;
+        if (i < LA)
+            opa.template load<S>(smem, t, i);
+        else
+            opb.template load<S>(smem, t, i - LA);
+    };
+    using S0 = std::integral_constant<int, 0>;
+    using S1 = std::integral_constant<int, 1>;
+    constexpr int NM = FM * FN;
+    constexpr int kRelAt = GEMM_AHEAD_REL_MFMA < NM ? GEMM_AHEAD_REL_MFMA : NM - 1;
+    constexpr int kAcqAt = GEMM_AHEAD_ACQ_MFMA < NM ? GEMM_AHEAD_ACQ_MFMA : NM - 1;
+    constexpr int L0 = L * GEMM_AHEAD_STEP0_LOADS / 16;  // loads of K-tile t+2 in step 0
+
+#pragma unroll
+    for (int i = 0; i < L; ++i) load(S0{}, kt0, i);
+#pragma unroll
+    for (int i = 0; i < L; ++i) load(S1{}, kt0 + 1, i);
+    vm_barrier<L>();
+#pragma unroll
+    for (int r = 0; r < NR; ++r) read_frag(0, 0, 0, r);
+#pragma unroll
+    for (int r = 0; r < NR; ++r) read_frag(1, 0, 1, r);
+
+    auto k_iter = [&](auto s_c, int t) {
+        constexpr int S = decltype(s_c)::value;
+        constexpr int SN = S ^ 1;
+        constexpr int B1 = S == 0 ? 1 : 2;   // this K-tile's step-1 buffer
+        constexpr int NB1 = S == 0 ? 2 : 1;  // the next K-tile's
+        static_range<0, NM>([&](auto m_c) {
+            constexpr int m = decltype(m_c)::value;
+            constexpr int j = m / FM, i = (j & 1) ? FM - 1 - m % FM : m % FM;
+            mfma16_tied(bf[0][j], af[0][i], acc[j][i]);
+            if constexpr (m == kRelAt) lgkm_barrier();
+            if constexpr (m >= kRelAt) {
+                constexpr int q = m - kRelAt, slots = NM - kRelAt;
+                static_range<q * L0 / slots, (q + 1) * L0 / slots>(
+                    [&](auto o_c) { load(s_c, t + 2, decltype(o_c)::value); });
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+#pragma unroll
+        for (int j = 0; j < FN; ++j) asm volatile("" ::"v"(bf[0][j]));
+#pragma unroll
+        for (int i = 0; i < FM; ++i) asm volatile("" ::"v"(af[0][i]));
+        static_range<0, NM>([&](auto m_c) {
+            constexpr int m = decltype(m_c)::value;
+            constexpr int j = m / FM, i = (j & 1) ? FM - 1 - m % FM : m % FM;
+            mfma16_tied(bf[B1][j], af[B1][i], acc[j][i]);
+            if constexpr (m == kAcqAt) vm_only_barrier<L0>();
+            if constexpr (m >= kAcqAt) {
+                constexpr int nl = L - L0, total = 2 * NR + nl, slots = NM - kAcqAt, q = m - kAcqAt;
+                // R R L R R L ...: the reads first while both remain
+                static_range<q * total / slots, (q + 1) * total / slots>([&](auto o_c) {
+                    constexpr int o = decltype(o_c)::value;
+                    constexpr int groups = (2 * NR) / 2 < nl ? (2 * NR) / 2 : nl;  // (R, R, L) groups
+                    constexpr bool in_groups = o < 3 * groups;
+                    constexpr bool is_read = in_groups ? (o % 3 != 2) : (2 * NR > 2 * groups);
+                    constexpr int idx = in_groups ? (is_read ? (o / 3) * 2 + (o % 3) : o / 3)
+                                                  : (is_read ? 2 * groups + (o - 3 * groups) : groups + (o - 3 * groups));
+                    if constexpr (is_read) {
+                        constexpr int ks = idx / NR, r = idx % NR;
+                        read_frag(ks == 0 ? 0 : NB1, SN, ks, r);
+                    } else {
+                        load(s_c, t + 2, L0 + idx);
+                    }
+                });
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        });
+#pragma unroll
+        for (int j = 0; j < FN; ++j) asm volatile("" ::"v"(bf[B1][j]));
+#pragma unroll
+        for (int i = 0; i < FM; ++i) asm volatile("" ::"v"(af[B1][i]));
+    };
+    // K-tiles in pairs (stage 0, stage 1); an odd count ends with one more on stage 0.
+    // Loads past the last fill stages that are never summed.
+    int kt = 0;
+    for (; kt + 1 < kt_count; kt += 2) {
+        k_iter(S0{}, kt0 + kt);
+        k_iter(S1{}, kt0 + kt + 1);
+    }
+    if (kt < kt_count) k_iter(S0{}, kt0 + kt);
+
+    vm_barrier<0>();  // no load is still writing LDS when C is staged there
+    acc_fence(acc);
+    fused_store_tile<C, kLds>(acc, smem, p, m0, n0, wm, wn, wave, lane);
+#endif
+}
+
+// ---- launches ------------------------------------------------------------------
+
+// A launch holds fewer than 2^32 threads along x, and one of more loses the rest without an
+// error: such a grid (below 2^31 workgroups) goes out in several.  parts: the grid's y.
+inline hipError_t launch_fused_grid(const void *kernel, int64_t grid, int parts, int threads, hipStream_t s,
+                                    FusedParams p) {
+    if (grid >= (int64_t(1) << 31)) return hipErrorInvalidValue;
+    const int64_t most = ((int64_t(1) << 32) - 1) / threads;
+    for (int64_t at = 0; at < grid; at += most) {
+        p.first = (uint32_t)at;
+        void *args[] = {&p};
+        const hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)(grid - at < most ? grid - at : most), (unsigned)parts),
+                                             dim3((unsigned)threads), args, 0, s);
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
+template <class C>
+hipError_t launch_fused_tile(const FusedParams &p, hipStream_t s) {
+    return launch_fused_grid(reinterpret_cast<const void *>(fused_tile_kernel<C>), (int64_t)p.num_m * p.num_n, p.parts,
+                             C::kThreads, s, p);
+}
+
+// One unit per block tile, so that they compile in parallel.
+hipError_t launch_fused_256x256(const FusedParams &p, hipStream_t s);
+hipError_t launch_fused_256x128(const FusedParams &p, hipStream_t s);
+hipError_t launch_fused_128x256(const FusedParams &p, hipStream_t s);
+hipError_t launch_fused_128x128(const FusedParams &p, hipStream_t s);
+hipError_t launch_fused_128x64(const FusedParams &p, hipStream_t s);
+hipError_t launch_fused_64x128(const FusedParams &p, hipStream_t s);
+hipError_t launch_fused_64x64(const FusedParams &p, hipStream_t s);
+
+// Rows that are not 16-byte aligned, any K >= 1 (fused_staged.hip): wide: a 128 x 128 tile,
+// else 64 x 64.
+hipError_t launch_fused_staged(bool wide, const FusedParams &p, hipStream_t s);
+
+// Few rows (fused_few.hip): K >= 8, any alignment.
+constexpr int kFusedFewRows = 64;
+hipError_t launch_fused_few(const FusedParams &p, hipStream_t s);
+
+// C from the parts' sums (parts 0: from zeros, K == 0).
+hipError_t launch_fused_join(const FusedParams &p, hipStream_t s);
+
+// dz = dy act'(pre), dbias = column sums (fused_grad.hip).
+struct FusedGradParams {
+    const void *dy;        // [m, n], fp16 or fp32
+    const _Float16 *pre;   // [m, n], null without an activation
+    _Float16 *dz;          // [m, n] or null
+    float *dbias;          // [n] or null
+    float *sums;           // dbias: [parts][n]
+    int64_t m, n;
+    int32_t act, dy_f32, vec, parts;
+};
+hipError_t launch_fused_grad(const FusedGradParams &p, hipStream_t s);
+int fused_grad_parts(int64_t m, int64_t n);
+
+}  // namespace gemm_f16

@@ -1,0 +1,153 @@
+// The elementwise part of the gradient of C = act(A B^T + bias) + residual:
+//
+//   dz = dy act'(z),   dbias[n] = sum_m dz[m][n]
+//
+// one pass over dy and z, the sums taken before dz is rounded.
+#include "fused.h"
+
+namespace gemm_f16 {
+
+// act'(z) times dy, in place.
+template <int N>
+__device__ __forceinline__ void activate_grad(int act, const float (&z)[N], float (&dy)[N]) {
+    switch (act) {
+        case kActRelu:
+#pragma unroll
+            for (int e = 0; e < N; ++e) dy[e] = z[e] > 0.0f ? dy[e] : z[e] <= 0.0f ? 0.0f : z[e];  // NaN stays
+            break;
+        case kActGelu:  // Phi(z) + z phi(z)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                float gauss;
+                const float cdf = normal_cdf(z[e], gauss);
+                dy[e] *= __builtin_fmaf(z[e] * 0.3989422804014327f, gauss, cdf);
+            }
+            break;
+        case kActGeluTanh:  // s = sigmoid(w): s + z s (1 - s) dw/dz
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float q = z[e] * z[e], s = sigmoid_f32(z[e] * __builtin_fmaf(kGeluC1, q, kGeluC0));
+                dy[e] *= __builtin_fmaf(z[e] * __builtin_fmaf(3.0f * kGeluC1, q, kGeluC0), s * (1.0f - s), s);
+            }
+            break;
+        case kActSilu:
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float s = sigmoid_f32(z[e]);
+                dy[e] *= __builtin_fmaf(z[e], s * (1.0f - s), s);
+            }
+            break;
+        default: break;
+    }
+}
+
+// A workgroup takes W chunks of 8 columns and the rows of one part, 256 / W of them at a
+// time; a thread keeps the sums of its 8 columns, which meet in LDS in a fixed order.
+// Bound by bytes.
+constexpr int kGradThreads = 256, kGradRows = 4;  // rows in flight a thread
+
+template <int W>
+__global__ __launch_bounds__(kGradThreads) void fused_grad_kernel(const FusedGradParams p) {
+    constexpr int H = kGradThreads / W;
+    __shared__ float red[H][W * 8 + 1];
+    const int c = threadIdx.x % W, h = threadIdx.x / W;
+    const int64_t n = ((int64_t)blockIdx.x * W + c) * 8;
+    const int64_t per = (p.m + p.parts - 1) / p.parts;
+    const int64_t lo = (int64_t)blockIdx.y * per, hi = lo + per < p.m ? lo + per : p.m;
+    float sum[8] = {};
+    if (n < p.n && p.vec) {
+        for (int64_t r0 = lo + h; r0 < hi; r0 += H * kGradRows) {
+            float dy[kGradRows][8], z[kGradRows][8];
+#pragma unroll
+            for (int i = 0; i < kGradRows; ++i) {
+                const int64_t r = r0 + i * H;
+                if (r >= hi) continue;
+                load_row(p.dy, p.dy_f32 != 0, r * p.n + n, dy[i]);
+                if (p.act != kActNone) load_row(p.pre, false, r * p.n + n, z[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < kGradRows; ++i) {
+                const int64_t r = r0 + i * H;
+                if (r >= hi) continue;
+                activate_grad(p.act, z[i], dy[i]);
+                if (p.dz) store_row(p.dz, false, r * p.n + n, dy[i], kStoreDefault);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += dy[i][e];
+            }
+        }
+    } else if (n < p.n) {
+        for (int64_t r = lo + h; r < hi; r += H) {
+            const int64_t at = r * p.n + n;
+            float dy[8], z[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const bool in = n + e < p.n;
+                dy[e] = in ? load1(p.dy, p.dy_f32 != 0, at + e) : 0.0f;
+                z[e] = in && p.act != kActNone ? (float)p.pre[at + e] : 0.0f;
+            }
+            activate_grad(p.act, z, dy);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (n + e >= p.n) continue;
+                if (p.dz) p.dz[at + e] = (_Float16)dy[e];
+                sum[e] += dy[e];
+            }
+        }
+    }
+    if (!p.dbias) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) red[h][8 * c + e] = sum[e];
+    __syncthreads();
+    for (int x = threadIdx.x; x < W * 8; x += kGradThreads) {
+        const int64_t col = (int64_t)blockIdx.x * W * 8 + x;
+        if (col >= p.n) continue;
+        float v = 0.0f;
+        for (int i = 0; i < H; ++i) v += red[i][x];
+        (p.parts > 1 ? p.sums + (int64_t)blockIdx.y * p.n : p.dbias)[col] = v;
+    }
+}
+
+// dbias from the parts' sums: 32 columns a workgroup, eight threads a column.
+__global__ __launch_bounds__(256) void fused_grad_join_kernel(const FusedGradParams p) {
+    __shared__ float red[8][32];
+    const int x = threadIdx.x % 32, h = threadIdx.x / 32;
+    const int64_t col = (int64_t)blockIdx.x * 32 + x;
+    float v = 0.0f;
+    if (col < p.n) {
+#pragma unroll 16
+        for (int q = h; q < p.parts; q += 8) v += p.sums[(int64_t)q * p.n + col];
+    }
+    red[h][x] = v;
+    __syncthreads();
+    if (h != 0 || col >= p.n) return;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v += red[i][x];
+    p.dbias[col] = v;
+}
+
+// Chunks of 8 columns that a workgroup takes: rows' segments of up to 512 bytes.
+static int grad_width(int64_t n) { return n > 128 ? 32 : n > 32 ? 16 : 4; }
+
+// Parts of the rows: workgroups for every CU several times over, of 4 steps at least.
+int fused_grad_parts(int64_t m, int64_t n) {
+    const int w = grad_width(n);
+    const int64_t cols = (n + 8 * w - 1) / (8 * w), step = kGradThreads / w * kGradRows;
+    int64_t parts = (2048 + cols - 1) / (cols > 0 ? cols : 1);
+    if (parts > (m + step - 1) / step) parts = (m + step - 1) / step;
+    return (int)(parts < 1 ? 1 : parts);
+}
+
+hipError_t launch_fused_grad(const FusedGradParams &p, hipStream_t s) {
+    const int w = grad_width(p.n);
+    const void *kernel = w == 32   ? reinterpret_cast<const void *>(fused_grad_kernel<32>)
+                         : w == 16 ? reinterpret_cast<const void *>(fused_grad_kernel<16>)
+                                   : reinterpret_cast<const void *>(fused_grad_kernel<4>);
+    void *args[] = {const_cast<FusedGradParams *>(&p)};
+    const int64_t cols = (p.n + 8 * w - 1) / (8 * w);
+    hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)cols, (unsigned)p.parts), dim3(kGradThreads), args, 0, s);
+    if (e != hipSuccess || !p.dbias || p.parts == 1) return e;
+    return hipLaunchKernel(reinterpret_cast<const void *>(fused_grad_join_kernel), dim3((unsigned)((p.n + 31) / 32)), dim3(256),
+                           args, 0, s);
+}
+
+}  // namespace gemm_f16

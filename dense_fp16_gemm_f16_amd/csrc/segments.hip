@@ -6,6 +6,7 @@
 #include <cmath>
 #include <iterator>
 
+#include "checks.h"
 #include "device.h"
 #include "gemm_f16.h"
 
@@ -16,38 +17,6 @@ constexpr int64_t kMaxRows = int64_t(1) << 30, kMaxK = int64_t(1) << 22, kMaxNMa
 constexpr int kTnCus = 256, kTnSplits = 64;
 constexpr int64_t kMaxElems = int64_t(1) << 47, kMaxGroups = int64_t(1) << 20;
 
-// One buffer of a call, for the checks on pointers.
-struct Buffer {
-    const void *p;
-    int64_t bytes;
-    int align;
-    bool out;
-};
-
-// Null, alignment and overlap: outputs (and the workspace) against every
-// other buffer.
-template <int N>
-static int check_buffers(const Buffer (&bufs)[N]) {
-    for (const Buffer &b : bufs)
-        if (b.bytes > 0 && !b.p) return GEMM_F16_ENULL;
-    for (const Buffer &b : bufs)
-        if (b.bytes > 0 && ((uintptr_t)b.p % (uintptr_t)b.align) != 0) return GEMM_F16_EALIGN;
-    for (int i = 0; i < N; ++i)
-        for (int j = 0; j < N; ++j) {
-            if (i == j || !bufs[i].out || bufs[i].bytes <= 0 || bufs[j].bytes <= 0) continue;
-            const uintptr_t a0 = (uintptr_t)bufs[i].p, a1 = a0 + (uintptr_t)bufs[i].bytes;
-            const uintptr_t b0 = (uintptr_t)bufs[j].p, b1 = b0 + (uintptr_t)bufs[j].bytes;
-            if (a0 < b1 && b0 < a1) return GEMM_F16_EOVERLAP;
-        }
-    return GEMM_F16_OK;
-}
-
-static bool below(int64_t limit, int64_t a, int64_t b, int64_t c = 1) {
-    // a, b, c >= 0 and below 2^31: a * b cannot wrap
-    if (a == 0 || b == 0 || c == 0) return true;
-    return a * b < limit && a * b <= (limit - 1) / c;
-}
-
 static int check_grouped(int kind, int64_t rows, int64_t groups, int64_t n, int64_t k) {
     if (kind < kSegNT || kind > kSegTN) return GEMM_F16_EINVAL;
     if (rows < 0 || n < 0 || k < 0 || rows >= kMaxRows || n >= kMaxRows || k >= kMaxK) return GEMM_F16_EINVAL;
@@ -56,8 +25,6 @@ static int check_grouped(int kind, int64_t rows, int64_t groups, int64_t n, int6
     if (!below(kMaxElems, rows, n) || !below(kMaxElems, n, k, groups)) return GEMM_F16_EINVAL;
     return GEMM_F16_OK;
 }
-
-static int status(hipError_t e) { return e == hipSuccess ? GEMM_F16_OK : e == hipErrorInvalidValue ? GEMM_F16_EINVAL : GEMM_F16_EHIP; }
 
 // Whether the operands' rows can go straight into LDS: 16-byte chunks, and
 // a gathered A below 2 GiB (one descriptor spans it).

@@ -298,6 +298,155 @@ int gemm_f16_lora_nt(int64_t rows, int64_t n, int64_t k, int64_t adapters, int64
 int64_t gemm_f16_lora_workspace(int64_t rows, int64_t n, int64_t k, int64_t adapters,
                                 int64_t rank);
 
+/* ---- the feed-forward layer around the products --------------------------------
+ *
+ * What a transformer's feed-forward layer, dense or routed, needs between its
+ * products: a product with bias, activation and residual in its epilogue, the
+ * routing of tokens to experts and the way back from them, each with its
+ * gradient.  The common rules of the segmented products above hold here too.
+ */
+
+enum {
+    GEMM_F16_ACT_NONE = 0,
+    GEMM_F16_ACT_RELU = 1,       /* max(z, 0) */
+    GEMM_F16_ACT_GELU = 2,       /* z Phi(z), Phi the normal distribution (erf) */
+    GEMM_F16_ACT_GELU_TANH = 3,  /* z / 2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) */
+    GEMM_F16_ACT_SILU = 4,       /* z / (1 + exp(-z)) */
+    GEMM_F16_ACT_LAST = 4
+};
+
+/*
+ * The epilogue of gemm_f16_fused_nt.  Null pointers leave their part out; all
+ * zeros is the plain product.
+ */
+typedef struct {
+    int32_t act;          /* GEMM_F16_ACT_* */
+    int32_t bias_f32;     /* type of bias: fp16 (0) or fp32 (1) */
+    int32_t out_f32;      /* type of c and residual: fp16 (0) or fp32 (1) */
+    const void *bias;     /* [n] */
+    const void *residual; /* [m,n]; may be c itself, else must not overlap it */
+    void *pre;            /* fp16 [m,n]: z, for the gradient */
+} gemm_f16_epilogue;
+
+/*
+ *   z = A B^T + bias,   c = act(z) + residual,   pre = fp16(z)
+ *
+ *   a  fp16 [m,k]    b  fp16 [n,k]    c  fp16 or fp32 [m,n]
+ *
+ * Everything is summed in fp32 and c rounded once; act takes the unrounded z.
+ * m, n < 2^30; m*n < 2^47; k < 2^22; any size and alignment; k == 0: z is the
+ * bias.  epilogue == NULL: the plain product.  Where z is -inf, the
+ * activations but relu give what their formulas give, a NaN.
+ */
+int gemm_f16_fused_nt(int64_t m, int64_t n, int64_t k, const void *a, const void *b, void *c,
+                      const gemm_f16_epilogue *epilogue, void *workspace, int64_t workspace_bytes,
+                      void *stream);
+int64_t gemm_f16_fused_workspace(int64_t m, int64_t n, int64_t k);
+
+/*
+ * The elementwise part of its gradient:
+ *
+ *   dz[m][n] = dy[m][n] act'(pre[m][n])        dbias[n] = sum_m dz[m][n]
+ *
+ *   dy   fp16 or fp32 [m,n]: the gradient of c
+ *   pre  fp16 [m,n]: of the forward call; not read without an activation
+ *   dz   fp16 [m,n] or NULL; may be dy itself where that is fp16
+ *   dbias  fp32 [n] or NULL: sums in fp32 of dz before it is rounded
+ *
+ * The residual's gradient is dy; A's is dz B and B's dz^T A (gemm_f16_nn_f32
+ * or gemm_f16_grouped_nn, and gemm_f16_grouped_tn, with one segment).  The
+ * workspace is needed with dbias only.
+ */
+int gemm_f16_fused_grad(int64_t m, int64_t n, const void *dy, int32_t dy_f32, const void *pre,
+                        int32_t act, void *dz, float *dbias, void *workspace,
+                        int64_t workspace_bytes, void *stream);
+int64_t gemm_f16_fused_grad_workspace(int64_t m, int64_t n);
+
+enum { GEMM_F16_SCORE_SOFTMAX = 0, GEMM_F16_SCORE_SIGMOID = 1 };
+
+/* How tokens are routed (see gemm_f16_route). */
+typedef struct {
+    int32_t score;        /* GEMM_F16_SCORE_* */
+    int32_t groups;       /* groups of experts / groups neighbours each; 1: none */
+    int32_t top_groups;   /* groups that a token may use */
+    int32_t group_top;    /* a group's value: its largest key (1), or the sum of its two largest (2) */
+    int32_t renormalize;  /* 1: a token's gates sum to scale */
+    float scale;          /* finite */
+} gemm_f16_routing;
+
+/*
+ * The experts of each token and their gates.
+ *
+ *   s = softmax(logits) over a token's experts, or sigmoid(logits)
+ *   key = s + bias; without a bias, the logit (whose order is that of s)
+ *   ids = the `fan` largest keys among the top_groups groups of largest value,
+ *         in falling order, ties to the lowest index (of groups, too); a
+ *         group's sum is that of keys, without a bias of scores
+ *   gates = scale * s[ids], renormalised: scale * s[ids] / sum(s[ids])
+ *
+ *   logits  fp16 or fp32 [tokens,experts]     bias  fp32 [experts] or NULL
+ *   ids     int32 [tokens,fan]                gates fp32 [tokens,fan]
+ *
+ * The choice is that of the formula in 64 bits (keys that differ by less than
+ * their rounding in fp32 are told apart in 64).  An expert whose logit or key
+ * is -inf or NaN is never chosen, and counts as 0 in the softmax; where too
+ * few are left, the remaining ids are -1, which gemm_f16_group_rows sorts
+ * behind all experts, with gates of 0.
+ * 0 <= tokens < 2^30; 1 <= experts <= 2048; 1 <= fan <= 32; fan <= experts /
+ * groups * top_groups; 1 <= groups <= 64, a divisor of experts.
+ */
+int gemm_f16_route(int64_t tokens, int64_t experts, int64_t fan, const void *logits,
+                   int32_t logits_f32, const float *bias, const gemm_f16_routing *routing,
+                   int32_t *ids, float *gates, void *stream);
+
+/*
+ * dlogits [tokens,experts], of the logits' type, from dgates fp32 [tokens,fan]:
+ * the gates' gradient with the choice held fixed.  Zeros for what has no part
+ * in the gates; ids outside [0, experts) have none.  Of `routing`, score,
+ * renormalize and scale are used.
+ */
+int gemm_f16_route_grad(int64_t tokens, int64_t experts, int64_t fan, const void *logits,
+                        int32_t logits_f32, const int32_t *ids, const float *dgates,
+                        const gemm_f16_routing *routing, void *dlogits, void *stream);
+
+/*
+ * Rows that were routed by gemm_f16_group_rows(tokens * fan, groups, ids)
+ * back to their tokens:
+ *
+ *   y[t][n] = residual[t][n] + sum_f gates[t][f] * rows[inverse[t*fan + f]][n]
+ *
+ *   rows      fp16 or fp32 [tokens*fan, n], in the plan's order
+ *   inverse, offsets   of the plan; places from offsets[groups] on belong to
+ *             no group and add nothing, whatever they hold
+ *   gates     fp32 [tokens,fan], or NULL for ones: the gradient of
+ *             gemm_f16_grouped_nt's gathered tokens from that of its rows
+ *   residual  [tokens,n] of y's type, or NULL; may be y itself, else must not overlap it
+ *   y         fp16 or fp32 [tokens,n]: summed in fp32, rounded once
+ *
+ * tokens*fan, n < 2^30; fan >= 1; tokens*fan*n < 2^47.
+ */
+int gemm_f16_combine_rows(int64_t tokens, int64_t fan, int64_t n, int64_t groups, const void *rows,
+                          int32_t rows_f32, const int32_t *inverse, const int32_t *offsets,
+                          const float *gates, const void *residual, void *y, int32_t y_f32,
+                          void *stream);
+
+/*
+ * Its gradient:
+ *
+ *   drows[inverse[t*fan + f]][n] = gates[t][f] * dy[t][n]
+ *   dgates[t][f] = sum_n dy[t][n] * rows[inverse[t*fan + f]][n]
+ *
+ *   dy fp16 or fp32 [tokens,n]; drows fp16 or fp32 [tokens*fan, n] or NULL;
+ *   dgates fp32 [tokens,fan] or NULL (then rows is not read)
+ *
+ * Rows behind offsets[groups] get zeros, and so do their gates.  The
+ * residual's gradient is dy.
+ */
+int gemm_f16_combine_rows_grad(int64_t tokens, int64_t fan, int64_t n, int64_t groups,
+                               const void *dy, int32_t dy_f32, const void *rows, int32_t rows_f32,
+                               const int32_t *inverse, const int32_t *offsets, const float *gates,
+                               void *drows, int32_t drows_f32, float *dgates, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
