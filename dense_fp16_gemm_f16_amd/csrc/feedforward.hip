@@ -232,6 +232,7 @@ int gemm_f16_route(int64_t tokens, int64_t experts, int64_t fan, const void *log
     if (rc != GEMM_F16_OK) return rc;
     RouteParams p = route_params(tokens, experts, fan, logits, logits_f32, r);
     p.bias = bias;
+    p.bias_vec = experts % 4 == 0 && aligned16(bias);
     p.ids = ids;
     p.gates = gates;
     p.groups = r.groups;

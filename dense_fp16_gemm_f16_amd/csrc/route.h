@@ -19,7 +19,7 @@ struct RouteParams {
     void *dlogits;         // gradient: [tokens, experts], of the logits' type
     int64_t tokens, first;  // first: tokens that earlier launches hold
     int32_t experts, fan, f32, sigmoid, groups, top_groups, group_top, renormalize;
-    int32_t vec;           // rows in whole aligned chunks of 4
+    int32_t vec, bias_vec; // rows, the bias in whole aligned chunks of 4
     float scale;
 };
 hipError_t launch_route(const RouteParams &p, hipStream_t s);

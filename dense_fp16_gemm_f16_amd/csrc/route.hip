@@ -10,16 +10,16 @@
 // a reduction over a row is four rotations within it.  Each pick is one such reduction for
 // the largest key and one for its lowest index.
 //
-// The selection is that of the formula in 64 bits.  Keys are computed in fp32 and the picks
-// made with them; where two keys that decide (neighbours in the order, or the last one in and
-// the first one out) are closer than their rounding errors, the wave makes its picks again
-// from keys in 64 bits, some ten times slower and rare: so which experts a token gets does
-// not hang on the order of a sum.  Without a bias the order is that of the logits and exact.
+// The choice is that of the formula in 64 bits, so which experts a token gets does not hang on
+// the order of a sum.  Keys are computed in fp32 and the picks made with them; where keys that
+// decide (neighbours in the order, or the last one in and the first one out) are closer than
+// their rounding errors, the picks in question get their keys in 64 bits and are put in order.
+// Without a bias the order is that of the logits and exact.
 #include "route.h"
 
 #include <algorithm>
 
-#include "kernels.h"
+#include "fused.h"
 
 namespace gemm_f16 {
 
@@ -28,6 +28,8 @@ namespace gemm_f16 {
 template <int L>
 constexpr int kRouteWaves = L == 16 ? 4 : 2;
 
+// A move within rows of 16 lanes.  Every lane of the wave has to take part: what an inactive
+// lane holds comes out as 0.
 template <int CTRL>
 __device__ __forceinline__ int rot(int x) {
     return __builtin_amdgcn_update_dpp(0, x, CTRL, 0xf, 0xf, true);
@@ -57,9 +59,28 @@ __device__ __forceinline__ T lanes_reduce(T x, Op op) {
     }
     return x;
 }
+// (none of them is a NaN)
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_fmaxf(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return __builtin_fminf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return a > b ? a : b; }
+__device__ __forceinline__ double smaller(double a, double b) { return a < b ? a : b; }
+
 template <int L, class T>
 __device__ __forceinline__ T lanes_max(T x) {
-    return lanes_reduce<L>(x, [](T a, T b) { return a > b ? a : b; });
+    return lanes_reduce<L>(x, [](T a, T b) { return larger(a, b); });
+}
+
+// The largest of a lane's values, as a tree.
+template <int V, class T>
+__device__ __forceinline__ T largest_of(const T (&x)[V]) {
+    T y[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) y[v] = x[v];
+#pragma unroll
+    for (int d = 1; d < V; d *= 2)
+#pragma unroll
+        for (int v = 0; v + d < V; v += 2 * d) y[v] = larger(y[v], y[v + d]);
+    return y[0];
 }
 template <int L>
 __device__ __forceinline__ int lanes_min(int x) {
@@ -147,141 +168,377 @@ __device__ __forceinline__ void wave_lds_fence() {
     __builtin_amdgcn_wave_barrier();
 }
 
-// The experts of the wave's tokens: lane f % L of a token gets the f-th's id (-1: none left)
-// in slot f / L.  lds: the wave's part, for the groups.  Returns whether the token's picks
-// hang on differences below the keys' rounding errors (never for T = double).
+// exp for keys: in fp32 the hardware's exp2 of a rounded product, relatively off by |x| 2^-24 +
+// 2^-23.  A key needs it against 1, where x exp(x) <= 0.37 and x s (1 - s) <= 0.23 make that
+// less than 2^-23.
+__device__ __forceinline__ float key_exp(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
+__device__ __forceinline__ double key_exp(double x) { return exp(x); }
+__device__ __forceinline__ float inverse_of(float x) { return __builtin_amdgcn_rcpf(x); }
+__device__ __forceinline__ double inverse_of(double x) { return 1.0 / x; }
+
+// What a choice goes by, in T: among the experts, or (`sums`) for groups valued by a sum.
 template <class T, int L, int V>
-__device__ __forceinline__ bool pick_experts(const RouteParams &p, const float (&l)[V], int sub, int row, char *lds,
-                                             int (&id)[kRouteFan / 16]) {
-    using E = Experts<L, V>;
-    constexpr bool kExact = sizeof(T) == 8;
-    T key[V], score[V];
-    const bool by_score = p.bias != nullptr, need = by_score || (p.groups > 1 && p.group_top == 2);
-    T largest = T(0);  // score, for the rounding errors
-    if (need) {
+struct Keys {
+    T key[V];  // -inf: never chosen
+    T share;   // softmax: the largest score, 1 / sum of exp(l - m)
+
+    __device__ __forceinline__ void init(const RouteParams &p, const float (&l)[V], int sub, bool sums) {
+        using E = Experts<L, V>;
+        share = T(1);
+        const bool by_score = p.bias != nullptr;
+        if (!by_score && !sums) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) key[v] = T(l[v]);
+            return;
+        }
         if (p.sigmoid) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) score[v] = sigmoid_of<T>(l[v]);
-            largest = T(1);
+            for (int v = 0; v < V; ++v) key[v] = inverse_of(T(1) + key_exp(-T(l[v])));
         } else {
-            float m = l[0];
-#pragma unroll
-            for (int v = 1; v < V; ++v) m = l[v] > m ? l[v] : m;
-            m = lanes_max<L>(m);
+            const float m = lanes_max<L>(largest_of<V>(l));
             T sum = T(0);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                score[v] = l[v] == kNone ? T(0) : exp_below<T>(l[v], m);
-                sum += score[v];
+                key[v] = l[v] == kNone ? T(0) : l[v] == m ? T(1) : key_exp(T(l[v]) - T(m));
+                sum += key[v];
             }
-            sum = lanes_sum<L>(sum);
+            share = inverse_of(lanes_sum<L>(sum));
 #pragma unroll
-            for (int v = 0; v < V; ++v) score[v] /= sum;
-            largest = T(1) / sum;
+            for (int v = 0; v < V; ++v) key[v] *= share;
+        }
+#pragma unroll
+        for (int v = 0; v < V; v += E::B) {
+            float bias[E::B];
+            const int e = E::at(v, sub);
+#pragma unroll
+            for (int i = 0; i < E::B; ++i) bias[i] = 0.0f;
+            if (by_score) {
+                if (E::B == 4 && p.bias_vec) {
+                    const floatx4 x = e < p.experts ? *reinterpret_cast<const floatx4 *>(p.bias + e) : floatx4{};
+#pragma unroll
+                    for (int i = 0; i < E::B; ++i) bias[i] = x[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < E::B; ++i)
+                        if (e + i < p.experts) bias[i] = p.bias[e + i];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < E::B; ++i) {
+                const T k = key[v + i] + T(bias[i]);
+                key[v + i] = l[v + i] == kNone || !(k == k) ? T(kNone) : k;
+            }
         }
     }
+
+    // What two fp32 scores can be off by against each other.  A sigmoid: 2^-24.9 by its exp (see
+    // key_exp), 2^-24 by its sum and 2^-23 by its reciprocal, less than 2^-22 for each of the
+    // two.  A softmax's shares as much relative to the largest, and its sum, which all scores
+    // share, is off by less than 2^-18 of itself.  Keys' own roundings come on top (kKeyError).
+    __device__ __forceinline__ float error(const RouteParams &p) const { return p.sigmoid ? 0x1p-21f : 0x1p-17f * (float)share; }
+};
+
+constexpr float kKeyError = 0x1.1p-23f;  // of a key: both roundings of a comparison, 2^-24 each
+
+// The open groups of the wave's tokens, a bit each, the same in all lanes of a token.  A
+// group's value is its largest key, or the sum of its two largest; lane g of a token takes
+// group g, from the keys in LDS (a pad per group keeps the lanes on different banks).  close:
+// the last group in and some other one are within `error` and their keys' roundings (negative:
+// exact).
+template <class T, int L, int V>
+__device__ __forceinline__ uint64_t open_groups(const RouteParams &p, const Keys<T, L, V> &k, int sub, int row, char *lds, T error,
+                                                bool &close) {
+    using E = Experts<L, V>;
+    const int per = p.experts / p.groups;
+    const float inv_per = 1.0f / (float)per;
+    T *const keys = reinterpret_cast<T *>(lds) + (int64_t)row * (p.experts + 2 * p.groups);
+    T *const value = keys + p.experts + p.groups;
+    wave_lds_fence();
+    T size = T(1);
+    // a group's value from its two largest (one with one expert left counts that one alone)
+    auto worth = [&](T first, T second) {
+        if (second != T(kNone))
+            size = larger(size, larger(larger(first, -first), larger(second, -second)));
+        else if (first != T(kNone))
+            size = larger(size, larger(first, -first));
+        return p.group_top == 2 && second != T(kNone) ? first + second : first;
+    };
+    if (L == 16 && V >= 4 && per >= 4 && per <= 64 && (per & (per - 1)) == 0) {
+        // groups of 1, 2, 4, 8 or 16 lanes' neighbours: in registers, each lane of a group
+        // meeting the others (256 experts in 8 groups: 2 us less than from LDS)
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const int e = E::at(v, sub);
-        if (by_score) {
-            const T k = score[v] + (e < p.experts ? T(p.bias[e]) : T(0));
-            key[v] = l[v] == kNone || !(k == k) ? T(kNone) : k;
-        } else {
-            key[v] = T(l[v]);
-        }
-    }
-    // What two keys can be off by against each other: a score by 2^-22 of itself (exp, a sum,
-    // a quotient), a softmax's sum, which all scores share, by 2^-18 of itself, a key's last
-    // rounding by 2^-24 of the key.  Twice that for sums of two.
-    T error = T(0);
-    if (!kExact && need) {
-        T size = T(1);
+        for (int v = 0; v + 3 < V; v += 4) {
+            T first = T(kNone), second = T(kNone);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const T k = key[v] < T(0) ? -key[v] : key[v];
-            size = by_score && k > size && k < T(__builtin_inff()) ? k : size;
+            for (int i = 0; i < 4; ++i) {
+                const T x = k.key[v + i];
+                second = larger(second, smaller(first, x));
+                first = larger(first, x);
+            }
+            auto meet = [&](T f, T s) {
+                second = larger(smaller(first, f), larger(second, s));
+                first = larger(first, f);
+            };
+            if (per >= 8) meet(rot<0xb1>(first), rot<0xb1>(second));     // the lane next to this one
+            if (per >= 16) meet(rot<0x4e>(first), rot<0x4e>(second));    // the other pair of four
+            if (per >= 32) meet(rot<0x141>(first), rot<0x141>(second));  // the other four of eight
+            if (per >= 64) meet(rot<0x140>(first), rot<0x140>(second));  // the other half of the row
+            const int e = E::at(v, sub);
+            if (e < p.experts && (e & (per - 1)) == 0) value[group_of(e, inv_per)] = worth(first, second);
         }
-        error = lanes_max<L>(size) * T(0x1p-22) + (p.sigmoid ? T(0x1p-20) : largest * T(0x1p-17));
-    }
-    bool close = false;
-    if (p.groups > 1) {
-        // the group's largest key, or the sum of its two largest: lane g of a token takes
-        // group g; a pad per group keeps the lanes on different banks
-        const int per = p.experts / p.groups;
-        const float inv_per = 1.0f / (float)per;
-        T *const keys = reinterpret_cast<T *>(lds) + (int64_t)row * (p.experts + 2 * p.groups);
-        T *const value = keys + p.experts + p.groups;
-        wave_lds_fence();
+    } else {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             const int e = E::at(v, sub);
-            if (e < p.experts) keys[e + group_of(e, inv_per)] = p.group_top == 2 && !by_score ? (l[v] == kNone ? T(kNone) : score[v]) : key[v];
+            if (e < p.experts) keys[e + group_of(e, inv_per)] = k.key[v];
         }
         wave_lds_fence();
         for (int g = sub; g < p.groups; g += L) {
             T first = T(kNone), second = T(kNone);
-            const T *k = keys + g * (per + 1);
-#pragma unroll 4
+            const T *q = keys + g * (per + 1);
+#pragma unroll 8
             for (int i = 0; i < per; ++i) {
-                const T x = k[i], low = x < first ? x : first;
-                first = x > first ? x : first;
-                second = low > second ? low : second;
+                const T x = q[i];
+                second = larger(second, smaller(first, x));
+                first = larger(first, x);
             }
-            // (a group with one expert left counts that one alone)
-            value[g] = p.group_top == 2 && second != T(kNone) ? first + second : first;
-        }
-        wave_lds_fence();
-        uint64_t mine = 0;  // open groups, the bits of this lane's
-        for (int g = sub; g < p.groups; g += L) {
-            const T x = value[g];
-            int rank = 0;
-            for (int o = 0; o < p.groups; ++o) rank += value[o] > x || (value[o] == x && o < g);
-            const bool open = rank < p.top_groups && x != T(kNone);
-            mine |= (uint64_t)open << g;
-            // the last one in, and another group within their errors
-            if (!kExact && need && open && rank == p.top_groups - 1) {
-                for (int o = 0; o < p.groups; ++o) {
-                    const T y = value[o], d = x > y ? x - y : y - x;
-                    if (o != g && d <= T(2) * error) close = true;
-                }
-            }
-        }
-        const uint32_t lo = (uint32_t)lanes_reduce<L>((int)(uint32_t)mine, [](int a, int b) { return a | b; });
-        const uint32_t hi = (uint32_t)lanes_reduce<L>((int)(uint32_t)(mine >> 32), [](int a, int b) { return a | b; });
-        const uint64_t open = (uint64_t)hi << 32 | lo;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int e = E::at(v, sub);
-            if (e < p.experts && !((open >> group_of(e, inv_per)) & 1)) key[v] = T(kNone);
+            value[g] = worth(first, second);
         }
     }
+    wave_lds_fence();
+    // (two keys' roundings on each side, and the sums', of up to twice their size)
+    if (error >= T(0)) error += T(4) * T(kKeyError) * lanes_max<L>(size);
+    uint64_t mine = 0;  // of this lane's groups
+    for (int g = sub; g < p.groups; g += L) {
+        const T x = value[g];
+        int rank = 0;
+        bool near = false;
+#pragma unroll 8
+        for (int o = 0; o < p.groups; ++o) {
+            const T y = value[o], d = x > y ? x - y : y - x;
+            rank += y > x || (y == x && o < g);
+            near = near || (o != g && d <= error);
+        }
+        const bool open = rank < p.top_groups && x != T(kNone);
+        mine |= (uint64_t)open << g;
+        close = close || (open && rank == p.top_groups - 1 && near);
+    }
+    const auto any = [](int a, int b) { return a | b; };
+    const uint32_t lo = (uint32_t)lanes_reduce<L>((int)(uint32_t)mine, any);
+    const uint32_t hi = p.groups > 32 ? (uint32_t)lanes_reduce<L>((int)(uint32_t)(mine >> 32), any) : 0;
+    return (uint64_t)hi << 32 | lo;
+}
+
+template <class T, int L, int V>
+__device__ __forceinline__ void close_groups(const RouteParams &p, Keys<T, L, V> &k, uint64_t open, int sub) {
+    using E = Experts<L, V>;
+    const float inv_per = 1.0f / (float)(p.experts / p.groups);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        if (!((open >> (group_of(E::at(v, sub), inv_per) & 63)) & 1)) k.key[v] = T(kNone);
+}
+
+// A bound from below of the fan-th largest key of a token of 16 lanes: the fan-th largest among
+// the largest keys of 32 disjoint sets, two of a lane: its even and odd values, or (HALVES) its
+// first and second half.
+template <bool HALVES, int V>
+__device__ __forceinline__ float lower_bound(const float (&key)[V], int fan) {
+    float part[2][V / 2];
+#pragma unroll
+    for (int v = 0; v < V; ++v) part[HALVES ? v / (V / 2) : v % 2][HALVES ? v % (V / 2) : v / 2] = key[v];
+    const float x = largest_of<V / 2>(part[0]), y = largest_of<V / 2>(part[1]);
+    int over_x = y > x, over_y = x > y;  // sets with a larger one
+    static_range<1, 16>([&](auto r_c) {
+        const float a = rot<0x120 + decltype(r_c)::value>(x), b = rot<0x120 + decltype(r_c)::value>(y);
+        over_x += (a > x) + (b > x);
+        over_y += (a > y) + (b > y);
+    });
+    const float least = smaller(over_x < fan ? x : __builtin_inff(), over_y < fan ? y : __builtin_inff());
+    return lanes_reduce<16>(least, [](float a, float b) { return smaller(a, b); });
+}
+
+// The candidates of tokens of 16 lanes that want up to 16 experts, in falling order of their
+// keys: the f-th in lane f of a token (-1: none left).  Few keys reach lower_bound (less
+// `error` and the keys' roundings): of 256 normally distributed ones, for 8 experts, 9, and
+// more than 16 for one token in 10^4, in whose wave a second bound is tried.  They go to LDS,
+// one to a lane, and each counts those before it.  Unlike picks one after the other this does
+// not wait for itself.
+// false, and no result: some token has more candidates than lanes.  close: neighbours among a
+// token's first fan + 1 are within the error (negative: exact).
+template <int V>
+__device__ __forceinline__ bool sort_candidates(const RouteParams &p, const Keys<float, 16, V> &k, int sub, int row, bool live,
+                                                float error, float2 *slots, bool &close, int &id) {
+    using E = Experts<16, V>;
+    float key;
+    int who;
+    if constexpr (V == 1) {
+        key = k.key[0];
+        who = key > kNone ? sub : (1 << 30) + sub;
+    } else {
+        int count, all;
+        float limit;
+        auto within = [&](float bound) {
+            limit = error >= 0.0f ? bound - (error + kKeyError * __builtin_fabsf(bound)) : bound;
+            count = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) count += k.key[v] > kNone && !(k.key[v] < limit);
+            all = lanes_sum<16>(count);
+        };
+        const float bound = lower_bound<false, V>(k.key, p.fan);
+        within(bound);
+        if constexpr (V >= 4) {
+            if (__ballot(live && all > 16)) within(larger(bound, lower_bound<true, V>(k.key, p.fan)));
+        }
+        if (__ballot(live && all > 16)) return false;
+        // places: the candidates of the lanes before, then this lane's own
+        // (shifts right within a row, which bring 0 to its first lanes)
+        int at = count;
+        at += rot<0x111>(at);
+        at += rot<0x112>(at);
+        at += rot<0x114>(at);
+        at += rot<0x118>(at);
+        at -= count;
+        float2 *const mine = slots + row * 16;
+        wave_lds_fence();
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (k.key[v] > kNone && !(k.key[v] < limit) && at < 16)
+                mine[at++] = make_float2(k.key[v], __builtin_bit_cast(float, E::at(v, sub)));
+        wave_lds_fence();
+        const float2 slot = mine[sub];
+        key = sub < all ? slot.x : kNone;
+        who = sub < all ? __builtin_bit_cast(int, slot.y) : (1 << 30) + sub;
+    }
+    int place = 0;
+    static_range<1, 16>([&](auto r_c) {
+        const float other = rot<0x120 + decltype(r_c)::value>(key);
+        const int o = rot<0x120 + decltype(r_c)::value>(who);
+        place += other > key || (other == key && o < who);
+    });
+    const int to = (row * 16 + place) * 4;
+    const float sorted = __builtin_bit_cast(float, __builtin_amdgcn_ds_permute(to, __builtin_bit_cast(int, key)));
+    const int expert = __builtin_amdgcn_ds_permute(to, who);
+    id = expert < p.experts ? expert : -1;
+    if (error >= 0.0f) {
+        const float next = __shfl(sorted, row * 16 + ((sub + 1) & 15));
+        close = sub < p.fan && sub < 15 && next > kNone && sorted - next <= error + kKeyError * __builtin_fabsf(next);
+    }
+    return true;
+}
+
+// Picks in falling order of the keys: the f-th in lane f % L of a token, slot f / L (-1: none
+// left), of p.fan of them.  `bounded`: the picks go on while some token's last one in and
+// first one out are within `error` and their roundings (L at most), and `close` says that
+// neighbours among a token's first p.fan + 1 are.  Returns the picks made.
+template <class T, int L, int V>
+__device__ __forceinline__ int pick_experts(const RouteParams &p, Keys<T, L, V> &k, int sub, bool live, bool bounded, float error,
+                                            bool &close, int (&id)[kRouteFan / 16]) {
+    using E = Experts<L, V>;
 #pragma unroll
     for (int i = 0; i < kRouteFan / 16; ++i) id[i] = -1;
     T before = T(0);
-    // (one more than the picks: the first one out)
-    const int turns = !kExact && by_score ? p.fan + 1 : p.fan;
-    for (int f = 0; f < turns; ++f) {
-        T m = key[0];
-#pragma unroll
-        for (int v = 1; v < V; ++v) m = key[v] > m ? key[v] : m;
-        m = lanes_max<L>(m);
-        if (!kExact && by_score && f > 0 && m != T(kNone) && before - m <= error) close = true;
-        before = m;
-        if (f == p.fan) break;
+    int f = 0;
+    for (;; ++f) {
+        if (f >= p.fan && !bounded) break;
+        const T m = lanes_max<L>(largest_of<V>(k.key));
+        if (bounded) {
+            const bool near = f > 0 && m != T(kNone) && before - m <= T(error) + T(kKeyError) * larger(m, -m);
+            if (f <= p.fan) close = close || near;
+            if (f >= p.fan && (f >= L || !__ballot(live && near))) break;
+            before = m;
+        }
         int at = V;
 #pragma unroll
-        for (int v = V - 1; v >= 0; --v) at = key[v] == m ? v : at;
+        for (int v = V - 1; v >= 0; --v) at = k.key[v] == m ? v : at;
         const int e = at < V && m != T(kNone) ? sub * E::B + at / E::B * (E::B * L) + at % E::B : 1 << 30;
         const int winner = lanes_min<L>(e);
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (e == winner && v == at) key[v] = T(kNone);
+            if (e == winner && v == at) k.key[v] = T(kNone);
         const int found = winner < (1 << 30) ? winner : -1;
 #pragma unroll
         for (int i = 0; i < kRouteFan / 16; ++i)
-            if (i < (p.fan + L - 1) / L && f == i * L + sub) id[i] = found;
+            if (f == i * L + sub) id[i] = found;
     }
-    return close;
+    return f;
+}
+
+// The experts of the wave's tokens, as the formula in 64 bits chooses them.
+template <int L, int V>
+__device__ __forceinline__ void choose(const RouteParams &p, const float (&l)[V], int sub, int row, bool live, int64_t token, char *lds,
+                                       int (&id)[kRouteFan / 16]) {
+    // (the rare ways read the logits again: held through the common one they cost registers)
+    const bool by_score = p.bias != nullptr, sums = p.groups > 1 && p.group_top == 2;
+    Keys<float, L, V> k;
+    k.init(p, l, sub, sums);
+    const float error = by_score || sums ? k.error(p) : -1.0f;
+    uint64_t open = ~uint64_t(0);
+    if (p.groups > 1) {
+        bool close = false;
+        open = open_groups(p, k, sub, row, lds, by_score || sums ? 2.0f * error : -1.0f, close);
+        if (__ballot(close && live)) {
+            float again[V];
+            load_logits<L, V>(p, token, sub, again);
+            Keys<double, L, V> exact;
+            exact.init(p, again, sub, sums);
+            open = open_groups(p, exact, sub, row, lds, -1.0, close);
+        }
+        if (sums && !by_score) k.init(p, l, sub, false);
+        close_groups(p, k, open, sub);
+    }
+    bool close = false, sorted = false;
+    if constexpr (L == 16) {
+        __shared__ float2 slots[kRouteWaves<16> * kWave];
+        if (p.fan <= 16) {
+            sorted = sort_candidates<V>(p, k, sub, row, live, by_score ? error : -1.0f, slots + threadIdx.x / kWave * kWave, close,
+                                        id[0]);
+            id[1] = -1;
+        }
+    }
+    int made = 16;
+    if (!sorted) made = pick_experts(p, k, sub, live, by_score, error, close, id);
+    if (!__ballot(close && live)) {
+        if (sorted && sub >= p.fan) id[0] = -1;
+        return;
+    }
+    if (sorted || made < L) {
+        // The picks made are all that can be in, in an order that may be off: each lane's
+        // pick gets its key in 64 bits, and its place among them.
+        double m = 0.0, sum = 1.0;
+        if (!p.sigmoid) {
+            float again[V];
+            load_logits<L, V>(p, token, sub, again);
+            const float top = lanes_max<L>(largest_of<V>(again));
+            sum = 0.0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) sum += again[v] == kNone ? 0.0 : exp_below<double>(again[v], top);
+            sum = lanes_sum<L>(sum);
+            m = top;
+        }
+        const int mine = sub < made ? id[0] : -1;
+        double key = (double)kNone;
+        if (mine >= 0) {
+            const float x = load_logit(p, token, mine);
+            key = (p.sigmoid ? sigmoid_of<double>(x) : exp_below<double>(x, (float)m) / sum) + (double)p.bias[mine];
+        }
+        int place = 0;
+        for (int f = 0; f < made; ++f) {
+            const double other = __shfl(key, row * L + f);
+            const int who = __shfl(mine, row * L + f);
+            place += who >= 0 && (other > key || (other == key && who < mine));
+        }
+        // (lanes without a pick, and picks of none, keep to the end)
+        if (mine < 0) place = sub;
+        const int moved = __builtin_amdgcn_ds_permute((row * L + place) * 4, mine);
+        id[0] = sub < p.fan ? moved : -1;
+        return;
+    }
+    float again[V];
+    load_logits<L, V>(p, token, sub, again);
+    Keys<double, L, V> exact;
+    exact.init(p, again, sub, false);
+    if (p.groups > 1) close_groups(p, exact, open, sub);
+    pick_experts(p, exact, sub, live, false, 0.0f, close, id);
 }
 
 // Renormalised gates: the largest pick (sigmoids: below 0, or 0), the scores' common factor.
@@ -303,7 +560,7 @@ __device__ __forceinline__ float pick_score(const RouteParams &p, float l, float
 }
 
 template <int L, int V>
-__global__ __launch_bounds__(kRouteWaves<L> *kWave) void route_kernel(const RouteParams p) {
+__global__ __launch_bounds__(kRouteWaves<L> *kWave) __attribute__((amdgpu_waves_per_eu(L == 16 || V <= 8 ? 4 : V <= 16 ? 3 : 1))) void route_kernel(const RouteParams p) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     constexpr int R = kWave / L;  // tokens of a wave
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, sub = lane % L, row = lane / L;
@@ -313,31 +570,26 @@ __global__ __launch_bounds__(kRouteWaves<L> *kWave) void route_kernel(const Rout
     float l[V];
     load_logits<L, V>(p, from, sub, l);
     char *const mine = lds + (int64_t)wave * R * (p.experts + 2 * p.groups) * 8;
-    int id[kRouteFan / 16];
-    const bool close = pick_experts<float, L, V>(p, l, sub, row, mine, id);
-    if (__ballot(close && live)) pick_experts<double, L, V>(p, l, sub, row, mine, id);
-
-    // the scores of the picks, each in its lane
-    const int slots = (p.fan + L - 1) / L;
-    float s[kRouteFan / 16];
     float m = kNone, sum = 1.0f;  // what the picks' scores are relative to, and divided by
-    float pick[kRouteFan / 16];
-#pragma unroll
-    for (int i = 0; i < kRouteFan / 16; ++i) {
-        pick[i] = kNone;
-        if (i < slots && id[i] >= 0) pick[i] = load_logit(p, from, id[i]);
-    }
-    if (p.renormalize) {
-        m = largest_pick<L>(p, pick);
-    } else if (!p.sigmoid) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) m = l[v] > m ? l[v] : m;
-        m = lanes_max<L>(m);
+    if (!p.renormalize && !p.sigmoid) {
+        m = lanes_max<L>(largest_of<V>(l));
         sum = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v) sum += l[v] == kNone ? 0.0f : exp_below<float>(l[v], m);
         sum = lanes_sum<L>(sum);
     }
+    int id[kRouteFan / 16];
+    choose<L, V>(p, l, sub, row, live, from, mine, id);
+
+    // the scores of the picks, each in its lane
+    const int slots = (p.fan + L - 1) / L;
+    float s[kRouteFan / 16], pick[kRouteFan / 16];
+#pragma unroll
+    for (int i = 0; i < kRouteFan / 16; ++i) {
+        pick[i] = kNone;
+        if (i < slots && id[i] >= 0) pick[i] = load_logit(p, from, id[i]);
+    }
+    if (p.renormalize) m = largest_pick<L>(p, pick);
 #pragma unroll
     for (int i = 0; i < kRouteFan / 16; ++i) s[i] = pick_score(p, pick[i], m);
     if (p.renormalize) {
@@ -373,9 +625,7 @@ __global__ __launch_bounds__(kRouteWaves<L> *kWave) void route_grad_kernel(const
     float m = kNone, total = 0.0f;
     if (dense) {
         load_logits<L, V>(p, from, sub, l);
-#pragma unroll
-        for (int v = 0; v < V; ++v) m = l[v] > m ? l[v] : m;
-        m = lanes_max<L>(m);
+        m = lanes_max<L>(largest_of<V>(l));
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             l[v] = l[v] == kNone ? 0.0f : exp_below<float>(l[v], m);
