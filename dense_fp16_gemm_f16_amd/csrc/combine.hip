@@ -23,13 +23,20 @@ __device__ __forceinline__ int64_t place_of(const CombineParams &p, int64_t r) {
 }
 
 // 8 columns of a row (n < p.n), those past the last 0.
-__device__ __forceinline__ void load_cols(const CombineParams &p, const void *from, bool f32, int64_t row, int n, float (&v)[8]) {
+template <bool F32>
+__device__ __forceinline__ void load_cols(const CombineParams &p, const void *from, int64_t row, int n, Chunk8<F32> &v) {
     const int64_t at = row * p.n + n;
     if (p.vec) {
-        load_row(from, f32, at, v);
+        v.load(from, at);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = n + e < p.n ? load1(from, f32, at + e) : 0.0f;
+        for (int e = 0; e < 8; ++e) {
+            const float x = n + e < p.n ? load1(from, F32, at + e) : 0.0f;
+            if constexpr (F32)
+                v.v[e / 4][e % 4] = x;
+            else
+                v.v[0][e] = (_Float16)x;
+        }
     }
 }
 
@@ -49,17 +56,23 @@ __device__ __forceinline__ void store_cols(const CombineParams &p, void *to, boo
     }
 }
 
-// 2^LOG threads a token, 8 columns each at a time; B rows in flight.
-template <int B>
+// 2^log threads a token, 8 columns each at a time; B rows in flight.  ROWS, Y: fp32 rows, y.
+template <int B, bool ROWS, bool Y>
 __global__ __launch_bounds__(kCombineThreads) void combine_kernel(const CombineParams p, int log) {
     const int64_t token = p.first + ((int64_t)blockIdx.x << (8 - log)) + (threadIdx.x >> log);
     if (token >= p.tokens) return;
     const int step = 8 << log, last = *p.last;
     for (int n = ((int)threadIdx.x & ((1 << log) - 1)) * 8; n < p.n; n += step) {
         float y[8] = {};
-        if (p.residual) load_cols(p, p.residual, p.y_f32 != 0, token, n, y);
+        if (p.residual) {
+            Chunk8<Y> r;
+            load_cols(p, p.residual, token, n, r);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = r[e];
+        }
         for (int f0 = 0; f0 < p.fan; f0 += B) {
-            float v[B][8], gate[B];
+            Chunk8<ROWS> v[B];
+            float gate[B];
             bool live[B];
 #pragma unroll
             for (int b = 0; b < B; ++b) {
@@ -68,7 +81,7 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(const CombineP
                 const int64_t r = token * p.fan + f0 + b, at = place_of(p, r);
                 live[b] = at >= 0 && at < last;
                 gate[b] = p.gates ? p.gates[r] : 1.0f;
-                if (live[b]) load_cols(p, p.rows, p.rows_f32 != 0, at, n, v[b]);
+                if (live[b]) load_cols(p, p.rows, at, n, v[b]);
             }
 #pragma unroll
             for (int b = 0; b < B; ++b) {
@@ -77,12 +90,12 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(const CombineP
                 for (int e = 0; e < 8; ++e) y[e] = __builtin_fmaf(gate[b], v[b][e], y[e]);
             }
         }
-        store_cols(p, p.y, p.y_f32 != 0, token, n, y);
+        store_cols(p, p.y, Y, token, n, y);
     }
 }
 
-// A wave a token: dy once, B of the token's rows at a time.
-template <int B>
+// A wave a token: dy once, B of the token's rows at a time, two chunks of columns in flight.
+template <int B, bool ROWS, bool Y>
 __global__ __launch_bounds__(kCombineThreads) void combine_grad_kernel(const CombineParams p, int) {
     const int lane = threadIdx.x % kWave;
     const int64_t token = p.first + (int64_t)blockIdx.x * (kCombineThreads / kWave) + threadIdx.x / kWave;
@@ -90,33 +103,37 @@ __global__ __launch_bounds__(kCombineThreads) void combine_grad_kernel(const Com
     const int last = *p.last;
     for (int f0 = 0; f0 < p.fan; f0 += B) {
         int64_t at[B];
+        bool live[B];
         float gate[B], dot[B];
 #pragma unroll
         for (int b = 0; b < B; ++b) {
             at[b] = -1;
             gate[b] = dot[b] = 0.0f;
-            if (f0 + b >= p.fan) continue;
-            const int64_t r = token * p.fan + f0 + b;
-            at[b] = place_of(p, r);
-            if (at[b] < last) gate[b] = p.gates ? p.gates[r] : 1.0f;
+            if (f0 + b < p.fan) {
+                const int64_t r = token * p.fan + f0 + b;
+                at[b] = place_of(p, r);
+                if (at[b] < last) gate[b] = p.gates ? p.gates[r] : 1.0f;
+            }
+            live[b] = at[b] >= 0 && at[b] < last;
         }
+#pragma unroll 2
         for (int n = lane * 8; n < p.n; n += kWave * 8) {
-            float dy[8], v[B][8];
-            load_cols(p, p.y, p.y_f32 != 0, token, n, dy);
+            Chunk8<Y> dy;
+            Chunk8<ROWS> v[B];
+            load_cols(p, p.y, token, n, dy);
             if (p.dgates) {
 #pragma unroll
-                for (int b = 0; b < B; ++b)
-                    if (at[b] >= 0 && at[b] < last) load_cols(p, p.rows, p.rows_f32 != 0, at[b], n, v[b]);
+                for (int b = 0; b < B; ++b)  // (a row out of play is the first one: not used)
+                    load_cols(p, p.rows, live[b] ? at[b] : 0, n, v[b]);
             }
 #pragma unroll
             for (int b = 0; b < B; ++b) {
                 if (at[b] < 0) continue;
-                const bool live = at[b] < last;
                 float d[8];
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    d[e] = live ? gate[b] * dy[e] : 0.0f;
-                    if (p.dgates && live) dot[b] = __builtin_fmaf(dy[e], v[b][e], dot[b]);
+                    d[e] = live[b] ? gate[b] * dy[e] : 0.0f;
+                    if (p.dgates) dot[b] = live[b] ? __builtin_fmaf(dy[e], v[b][e], dot[b]) : dot[b];
                 }
                 if (p.drows) store_cols(p, p.drows, p.drows_f32 != 0, at[b], n, d);
             }
@@ -143,20 +160,30 @@ static hipError_t launch(const void *kernel, CombineParams p, int per, int log, 
     return hipSuccess;
 }
 
+template <bool ROWS, bool Y>
+static const void *kernel_of(bool grad, int64_t fan) {
+    if (grad)
+        return fan <= 1   ? reinterpret_cast<const void *>(combine_grad_kernel<1, ROWS, Y>)
+               : fan <= 2 ? reinterpret_cast<const void *>(combine_grad_kernel<2, ROWS, Y>)
+                          : reinterpret_cast<const void *>(combine_grad_kernel<4, ROWS, Y>);
+    return fan <= 2   ? reinterpret_cast<const void *>(combine_kernel<2, ROWS, Y>)
+           : fan <= 4 ? reinterpret_cast<const void *>(combine_kernel<4, ROWS, Y>)
+                      : reinterpret_cast<const void *>(combine_kernel<8, ROWS, Y>);
+}
+
+static const void *kernel_of(bool grad, const CombineParams &p) {
+    if (p.rows_f32) return p.y_f32 ? kernel_of<true, true>(grad, p.fan) : kernel_of<true, false>(grad, p.fan);
+    return p.y_f32 ? kernel_of<false, true>(grad, p.fan) : kernel_of<false, false>(grad, p.fan);
+}
+
 hipError_t launch_combine(const CombineParams &p, hipStream_t s) {
     int log = 3;  // threads a token: its chunks of 8 columns, or a workgroup
     while (log < 8 && (8 << log) < p.n) ++log;
-    const void *kernel = p.fan <= 2   ? reinterpret_cast<const void *>(combine_kernel<2>)
-                         : p.fan <= 4 ? reinterpret_cast<const void *>(combine_kernel<4>)
-                                      : reinterpret_cast<const void *>(combine_kernel<8>);
-    return launch(kernel, p, kCombineThreads >> log, log, s);
+    return launch(kernel_of(false, p), p, kCombineThreads >> log, log, s);
 }
 
 hipError_t launch_combine_grad(const CombineParams &p, hipStream_t s) {
-    const void *kernel = p.fan <= 1   ? reinterpret_cast<const void *>(combine_grad_kernel<1>)
-                         : p.fan <= 2 ? reinterpret_cast<const void *>(combine_grad_kernel<2>)
-                                      : reinterpret_cast<const void *>(combine_grad_kernel<4>);
-    return launch(kernel, p, kCombineThreads / kWave, 0, s);
+    return launch(kernel_of(true, p), p, kCombineThreads / kWave, 0, s);
 }
 
 }  // namespace gemm_f16

@@ -112,6 +112,29 @@ __device__ __forceinline__ float load1(const void *from, bool f32, int64_t at) {
     return f32 ? static_cast<const float *>(from)[at] : (float)static_cast<const _Float16 *>(from)[at];
 }
 
+// 8 columns of a row as they come, converted where they are used: in half the registers of 8
+// floats.
+template <bool F32>
+struct Chunk8 {
+    std::conditional_t<F32, floatx4, half8> v[F32 ? 2 : 1];
+
+    __device__ __forceinline__ void load(const void *from, int64_t at) {
+        if constexpr (F32) {
+            const floatx4 *q = reinterpret_cast<const floatx4 *>(static_cast<const float *>(from) + at);
+            v[0] = q[0];
+            v[1] = q[1];
+        } else {
+            v[0] = *reinterpret_cast<const half8 *>(static_cast<const _Float16 *>(from) + at);
+        }
+    }
+    __device__ __forceinline__ float operator[](int e) const {
+        if constexpr (F32)
+            return v[e / 4][e % 4];
+        else
+            return (float)v[0][e];
+    }
+};
+
 // 16 bytes under C's cache policy (CStore).
 __device__ __forceinline__ void store16(void *to, int4v v, int policy) {
     if (policy == kStoreDevice)

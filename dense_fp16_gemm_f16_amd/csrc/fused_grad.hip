@@ -8,45 +8,33 @@
 namespace gemm_f16 {
 
 // act'(z) times dy, in place.
-template <int N>
-__device__ __forceinline__ void activate_grad(int act, const float (&z)[N], float (&dy)[N]) {
-    switch (act) {
-        case kActRelu:
+template <int ACT, int N>
+__device__ __forceinline__ void activate_grad(const float (&z)[N], float (&dy)[N]) {
 #pragma unroll
-            for (int e = 0; e < N; ++e) dy[e] = z[e] > 0.0f ? dy[e] : z[e] <= 0.0f ? 0.0f : z[e];  // NaN stays
-            break;
-        case kActGelu:  // Phi(z) + z phi(z)
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                float gauss;
-                const float cdf = normal_cdf(z[e], gauss);
-                dy[e] *= __builtin_fmaf(z[e] * 0.3989422804014327f, gauss, cdf);
-            }
-            break;
-        case kActGeluTanh:  // s = sigmoid(w): s + z s (1 - s) dw/dz
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float q = z[e] * z[e], s = sigmoid_f32(z[e] * __builtin_fmaf(kGeluC1, q, kGeluC0));
-                dy[e] *= __builtin_fmaf(z[e] * __builtin_fmaf(3.0f * kGeluC1, q, kGeluC0), s * (1.0f - s), s);
-            }
-            break;
-        case kActSilu:
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float s = sigmoid_f32(z[e]);
-                dy[e] *= __builtin_fmaf(z[e], s * (1.0f - s), s);
-            }
-            break;
-        default: break;
+    for (int e = 0; e < N; ++e) {
+        if constexpr (ACT == kActRelu) {
+            dy[e] = z[e] > 0.0f ? dy[e] : z[e] <= 0.0f ? 0.0f : z[e];  // NaN stays
+        } else if constexpr (ACT == kActGelu) {  // Phi(z) + z phi(z)
+            float gauss;
+            const float cdf = normal_cdf(z[e], gauss);
+            dy[e] *= __builtin_fmaf(z[e] * 0.3989422804014327f, gauss, cdf);
+        } else if constexpr (ACT == kActGeluTanh) {  // s = sigmoid(w): s + z s (1 - s) dw/dz
+            const float q = z[e] * z[e], s = sigmoid_f32(z[e] * __builtin_fmaf(kGeluC1, q, kGeluC0));
+            dy[e] *= __builtin_fmaf(z[e] * __builtin_fmaf(3.0f * kGeluC1, q, kGeluC0), s * (1.0f - s), s);
+        } else if constexpr (ACT == kActSilu) {
+            const float s = sigmoid_f32(z[e]);
+            dy[e] *= __builtin_fmaf(z[e], s * (1.0f - s), s);
+        }
     }
 }
 
 // A workgroup takes W chunks of 8 columns and the rows of one part, 256 / W of them at a
 // time; a thread keeps the sums of its 8 columns, which meet in LDS in a fixed order.
-// Bound by bytes.
-constexpr int kGradThreads = 256, kGradRows = 4;  // rows in flight a thread
+// Bound by bytes: FIGURES.  Four rows of dy and z are in flight a thread, as they come (as
+// floats they took twice the registers, and half the waves were left: 146 us).
+constexpr int kGradThreads = 256, kGradRows = 4;
 
-template <int W>
+template <int W, bool F32, int ACT>
 __global__ __launch_bounds__(kGradThreads) void fused_grad_kernel(const FusedGradParams p) {
     constexpr int H = kGradThreads / W;
     __shared__ float red[H][W * 8 + 1];
@@ -57,22 +45,28 @@ __global__ __launch_bounds__(kGradThreads) void fused_grad_kernel(const FusedGra
     float sum[8] = {};
     if (n < p.n && p.vec) {
         for (int64_t r0 = lo + h; r0 < hi; r0 += H * kGradRows) {
-            float dy[kGradRows][8], z[kGradRows][8];
+            Chunk8<F32> raw[kGradRows];
+            half8 pre[kGradRows];
 #pragma unroll
             for (int i = 0; i < kGradRows; ++i) {
-                const int64_t r = r0 + i * H;
-                if (r >= hi) continue;
-                load_row(p.dy, p.dy_f32 != 0, r * p.n + n, dy[i]);
-                if (p.act != kActNone) load_row(p.pre, false, r * p.n + n, z[i]);
+                const int64_t r = r0 + i * H < hi ? r0 + i * H : r0;  // (the first again: not used)
+                raw[i].load(p.dy, r * p.n + n);
+                if constexpr (ACT != kActNone) pre[i] = *reinterpret_cast<const half8 *>(p.pre + r * p.n + n);
             }
 #pragma unroll
             for (int i = 0; i < kGradRows; ++i) {
                 const int64_t r = r0 + i * H;
                 if (r >= hi) continue;
-                activate_grad(p.act, z[i], dy[i]);
-                if (p.dz) store_row(p.dz, false, r * p.n + n, dy[i], kStoreDefault);
+                float dy[8], z[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum[e] += dy[i][e];
+                for (int e = 0; e < 8; ++e) {
+                    dy[e] = raw[i][e];
+                    z[e] = ACT != kActNone ? (float)pre[i][e] : 0.0f;
+                }
+                activate_grad<ACT>(z, dy);
+                if (p.dz) store_row(p.dz, false, r * p.n + n, dy, kStoreDefault);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum[e] += dy[e];
             }
         }
     } else if (n < p.n) {
@@ -82,10 +76,10 @@ __global__ __launch_bounds__(kGradThreads) void fused_grad_kernel(const FusedGra
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const bool in = n + e < p.n;
-                dy[e] = in ? load1(p.dy, p.dy_f32 != 0, at + e) : 0.0f;
-                z[e] = in && p.act != kActNone ? (float)p.pre[at + e] : 0.0f;
+                dy[e] = in ? load1(p.dy, F32, at + e) : 0.0f;
+                z[e] = in && ACT != kActNone ? (float)p.pre[at + e] : 0.0f;
             }
-            activate_grad(p.act, z, dy);
+            activate_grad<ACT>(z, dy);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 if (n + e >= p.n) continue;
@@ -137,11 +131,25 @@ int fused_grad_parts(int64_t m, int64_t n) {
     return (int)(parts < 1 ? 1 : parts);
 }
 
+template <int W, bool F32>
+static const void *grad_kernel(int act) {
+    switch (act) {
+        case kActRelu: return reinterpret_cast<const void *>(fused_grad_kernel<W, F32, kActRelu>);
+        case kActGelu: return reinterpret_cast<const void *>(fused_grad_kernel<W, F32, kActGelu>);
+        case kActGeluTanh: return reinterpret_cast<const void *>(fused_grad_kernel<W, F32, kActGeluTanh>);
+        case kActSilu: return reinterpret_cast<const void *>(fused_grad_kernel<W, F32, kActSilu>);
+        default: return reinterpret_cast<const void *>(fused_grad_kernel<W, F32, kActNone>);
+    }
+}
+
+template <int W>
+static const void *grad_kernel(const FusedGradParams &p) {
+    return p.dy_f32 ? grad_kernel<W, true>(p.act) : grad_kernel<W, false>(p.act);
+}
+
 hipError_t launch_fused_grad(const FusedGradParams &p, hipStream_t s) {
     const int w = grad_width(p.n);
-    const void *kernel = w == 32   ? reinterpret_cast<const void *>(fused_grad_kernel<32>)
-                         : w == 16 ? reinterpret_cast<const void *>(fused_grad_kernel<16>)
-                                   : reinterpret_cast<const void *>(fused_grad_kernel<4>);
+    const void *kernel = w == 32 ? grad_kernel<32>(p) : w == 16 ? grad_kernel<16>(p) : grad_kernel<4>(p);
     void *args[] = {const_cast<FusedGradParams *>(&p)};
     const int64_t cols = (p.n + 8 * w - 1) / (8 * w);
     hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)cols, (unsigned)p.parts), dim3(kGradThreads), args, 0, s);
