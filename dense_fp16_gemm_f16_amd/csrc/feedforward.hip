@@ -39,6 +39,16 @@ static TileSize tile_size(int tile) {
     }
 }
 
+// Whether the product can walk its tiles: more of them than CUs, fp16 results in whole 16-byte
+// chunks, and what the kernels of fused_walk.h take.
+static bool walk_takes(int tile, const TileSize &ts, int cus, const FusedParams &p) {
+    if ((int64_t)p.num_m * p.num_n <= cus || !p.vec || p.out_f32 || (p.residual && p.act != kActNone) ||
+        (int64_t)ts.bm * p.n * 2 >= (int64_t(1) << 31))
+        return false;
+    if (tile == GEMM_F16_TILE_256x256) return p.k % 128 == 0 && p.k >= 256;
+    return (tile == GEMM_F16_TILE_256x128 || tile == GEMM_F16_TILE_128x256) && p.k_tiles >= 3;
+}
+
 static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, void *c, const gemm_f16_epilogue &e,
                  void *workspace, int64_t workspace_bytes, hipStream_t s) {
     int rc = check_fused(m, n, k);
@@ -107,6 +117,14 @@ static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, 
     p.swizzle = 4;
     p.xcd = gemm_f16_select_xcd(p.num_m, p.num_n, p.swizzle, cus);
     if (!direct) return status(launch_fused_staged(tile == GEMM_F16_TILE_128x128, p, s));
+    if (walk_takes(tile, ts, cus, p)) {
+        const bool dev = p.c_store == kStoreDevice;
+        switch (tile) {
+            case GEMM_F16_TILE_256x256: return status(launch_fused_walk_256x256(dev, p, cus, s));
+            case GEMM_F16_TILE_256x128: return status(launch_fused_walk_256x128(dev, p, cus, s));
+            default: return status(launch_fused_walk_128x256(dev, p, cus, s));
+        }
+    }
     switch (tile) {
         case GEMM_F16_TILE_256x256: return status(launch_fused_256x256(p, s));
         case GEMM_F16_TILE_256x128: return status(launch_fused_256x128(p, s));

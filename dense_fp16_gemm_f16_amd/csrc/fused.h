@@ -278,42 +278,15 @@ __device__ __forceinline__ void fused_store_tile(const typename Mfma<C::MB>::Acc
     }
 }
 
-// One block tile per workgroup, operands straight into LDS (16-byte aligned rows): the K
-// loop of gemm_f16_direct_ahead_kernel, two LDS stages, both k steps' fragments of K-tile
-// t+1 read during K-tile t, a release and an acquire barrier per K-tile.  With parts > 1
-// blockIdx.y is a part of K, whose sums leave in fp32 for fused_join_kernel.
-template <class C>
-__global__ __launch_bounds__(C::kThreads)
-__attribute__((amdgpu_waves_per_eu(C::kMinWavesPerEU, C::kMinWavesPerEU)))
-void fused_tile_kernel(const FusedParams p) {
-#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
-    constexpr int BM = C::BM, BN = C::BN;
-    constexpr int TM = C::TM, TN = C::TN, FM = C::FM, FN = C::FN;
-    static_assert(C::MB == 16 && C::KS == 2, "two 32-wide k steps per K-tile");
-    using OpA = KMajorDirect<C, BM, false>;
-    using OpB = KMajorDirect<C, BN, false>;
-    constexpr int kLdsB = OpA::kLdsBytes, kLds = OpA::kLdsBytes + OpB::kLdsBytes;
+// The K loop of gemm_f16_direct_ahead_kernel over K-tiles kt0 .. kt0 + kt_count - 1: two LDS
+// stages, both k steps' fragments of K-tile t+1 read during K-tile t, a release and an acquire
+// barrier per K-tile.
+template <class C, class OpA, class OpB>
+__device__ __forceinline__ void fused_k_loop(const OpA &opa, const OpB &opb, floatx4 (&acc)[C::FN][C::FM], char *smem, int kt0,
+                                             int kt_count) {
+    constexpr int FM = C::FM, FN = C::FN;
     constexpr int LA = OpA::kLoads, L = OpA::kLoads + OpB::kLoads;
-    static_assert(kLds <= 160 * 1024 && 2 * L < 64, "LDS budget, vmcnt range");
-    __shared__ __attribute__((aligned(1024))) char smem[kLds];
-    GEMM_POISON_LDS(smem);
-
-    const int tid = threadIdx.x, lane = tid & (kWave - 1);
-    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-    const int wm = wave / C::WN, wn = wave % C::WN;
-    const TileCoord tc = tile_coord<uint32_t>(p.first + blockIdx.x, p.num_m, p.num_n, p.swizzle, p.xcd != 0);
-    const int m0 = (int)tc.m_block * BM, n0 = (int)tc.n_block * BN;
-    // this part's K-tiles: kt0 .. kt0 + kt_count - 1, from element k0 of every row
-    const int kt0 = (int)blockIdx.y * p.part_kt, kt_count = min(p.part_kt, p.k_tiles - kt0);
-    if (kt_count <= 0) return;  // never launched so
-
-    OpA opa;
-    OpB opb;
-    // (the descriptors end with the tile's last row: K-tiles start inside it)
-    opa.init(p.a + (int64_t)m0 * p.k, min(BM, p.m - m0), p.k, kt0 + kt_count, wave, lane, wm * TM, 0);
-    opb.init(p.b + (int64_t)n0 * p.k, min(BN, p.n - n0), p.k, kt0 + kt_count, wave, lane, wn * TN, kLdsB);
-
-    floatx4 acc[FN][FM];
+    static_assert(2 * L < 64, "vmcnt range");
 #pragma unroll
     for (int j = 0; j < FN; ++j)
 #pragma unroll
@@ -414,11 +387,121 @@ void fused_tile_kernel(const FusedParams p) {
         k_iter(S0{}, kt0 + kt);
         k_iter(S1{}, kt0 + kt + 1);
     }
-    if (kt < kt_count) k_iter(S0{}, kt0 + kt);
-
-    vm_barrier<0>();  // no load is still writing LDS when C is staged there
+    // The accumulators may move where the two ways on meet, and the compiler knows of no MFMA
+    // still writing them: each way waits for its own.
     acc_fence(acc);
+    if (kt < kt_count) {
+        k_iter(S0{}, kt0 + kt);
+        acc_fence(acc);
+    }
+    vm_barrier<0>();  // no load is still writing LDS
+}
+
+// One block tile per workgroup, operands straight into LDS (16-byte aligned rows).  With parts
+// > 1 blockIdx.y is a part of K, whose sums leave in fp32 for fused_join_kernel.
+template <class C>
+__global__ __launch_bounds__(C::kThreads)
+__attribute__((amdgpu_waves_per_eu(C::kMinWavesPerEU, C::kMinWavesPerEU)))
+void fused_tile_kernel(const FusedParams p) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
+    constexpr int BM = C::BM, BN = C::BN;
+    static_assert(C::MB == 16 && C::KS == 2, "two 32-wide k steps per K-tile");
+    using OpA = KMajorDirect<C, BM, false>;
+    using OpB = KMajorDirect<C, BN, false>;
+    constexpr int kLdsB = OpA::kLdsBytes, kLds = OpA::kLdsBytes + OpB::kLdsBytes;
+    static_assert(kLds <= 160 * 1024, "LDS budget");
+    __shared__ __attribute__((aligned(1024))) char smem[kLds];
+    GEMM_POISON_LDS(smem);
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    const TileCoord tc = tile_coord<uint32_t>(p.first + blockIdx.x, p.num_m, p.num_n, p.swizzle, p.xcd != 0);
+    const int m0 = (int)tc.m_block * BM, n0 = (int)tc.n_block * BN;
+    const int kt0 = (int)blockIdx.y * p.part_kt, kt_count = min(p.part_kt, p.k_tiles - kt0);  // this part's K-tiles
+    if (kt_count <= 0) return;  // never launched so
+
+    OpA opa;
+    OpB opb;
+    opa.init(p.a + (int64_t)m0 * p.k, min(BM, p.m - m0), p.k, kt0 + kt_count, wave, lane, wm * C::TM, 0);
+    opb.init(p.b + (int64_t)n0 * p.k, min(BN, p.n - n0), p.k, kt0 + kt_count, wave, lane, wn * C::TN, kLdsB);
+    floatx4 acc[C::FN][C::FM];
+    fused_k_loop<C>(opa, opb, acc, smem, kt0, kt_count);
     fused_store_tile<C, kLds>(acc, smem, p, m0, n0, wm, wn, wave, lane);
+#endif
+}
+
+// The same for fp16 results in whole 16-byte chunks, which leave straight from the accumulators:
+// B's fragment rows are interleaved (KMajorDirect PERM), so a lane's blocks (2q, i) and (2q + 1,
+// i) hold 8 neighbouring columns of row 16 i + l % 16.  With the K loop over, its fragments'
+// registers hold the residual of kAhead such units in flight.
+// ACT and RES are template arguments: the units are unrolled, and a copy for each activation
+// would not fit the instruction cache.
+template <class C, int ACT, bool RES>
+__global__ __launch_bounds__(C::kThreads)
+__attribute__((amdgpu_waves_per_eu(C::kMinWavesPerEU, C::kMinWavesPerEU)))
+void fused_direct_kernel(const FusedParams p) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
+    constexpr int BM = C::BM, BN = C::BN, FM = C::FM, FN = C::FN;
+    static_assert(C::MB == 16 && C::KS == 2 && FN % 2 == 0, "two 32-wide k steps per K-tile, blocks in pairs");
+    using OpA = KMajorDirect<C, BM, false>;
+    using OpB = KMajorDirect<C, BN, false, true>;
+    constexpr int kLdsB = OpA::kLdsBytes, kLds = OpA::kLdsBytes + OpB::kLdsBytes;
+    static_assert(kLds <= 160 * 1024, "LDS budget");
+    __shared__ __attribute__((aligned(1024))) char smem[kLds];
+    GEMM_POISON_LDS(smem);
+
+    const int tid = threadIdx.x, lane = tid & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const int wm = wave / C::WN, wn = wave % C::WN;
+    const TileCoord tc = tile_coord<uint32_t>(p.first + blockIdx.x, p.num_m, p.num_n, p.swizzle, p.xcd != 0);
+    const int m0 = (int)tc.m_block * BM, n0 = (int)tc.n_block * BN;
+    if (p.k_tiles == 0) return;  // never launched so
+
+    OpA opa;
+    OpB opb;
+    opa.init(p.a + (int64_t)m0 * p.k, min(BM, p.m - m0), p.k, p.k_tiles, wave, lane, wm * C::TM, 0);
+    opb.init(p.b + (int64_t)n0 * p.k, min(BN, p.n - n0), p.k, p.k_tiles, wave, lane, wn * C::TN, kLdsB);
+    floatx4 acc[FN][FM];
+    fused_k_loop<C>(opa, opb, acc, smem, 0, p.k_tiles);
+
+    // (opaque copies: what hangs on them is computed here, not held through the K loop)
+    int l = lane, row0 = m0 + wm * C::TM, col0 = n0 + wn * C::TN;
+    asm volatile("" : "+v"(l), "+s"(row0), "+s"(col0));
+    constexpr int U = FM * FN / 2, kAhead = U < 16 ? U : 16;
+    const int m_l = row0 + l % 16, n_l = col0 + 8 * (l / 16);
+    auto inside = [&](int u) { return m_l + 16 * (u % FM) < p.m && n_l + 32 * (u / FM) < p.n; };
+    auto at_of = [&](int u) { return (int64_t)(m_l + 16 * (u % FM)) * p.n + n_l + 32 * (u / FM); };
+    float bias[FN / 2][8];
+#pragma unroll
+    for (int q = 0; q < FN / 2; ++q) load_bias(p, n_l + 32 * q, bias[q]);
+    half8 res[RES ? kAhead : 1];
+    auto load_res = [&](auto u_c) {
+        constexpr int u = decltype(u_c)::value;
+        if constexpr (RES && u < U) {
+            if (inside(u)) res[u % kAhead] = *reinterpret_cast<const half8 *>(static_cast<const _Float16 *>(p.residual) + at_of(u));
+        }
+    };
+    static_range<0, kAhead>(load_res);
+    static_range<0, U>([&](auto u_c) {
+        constexpr int u = decltype(u_c)::value, q = u / FM, i = u % FM;
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            z[e] = acc[2 * q][i][e] + bias[q][e];
+            z[4 + e] = acc[2 * q + 1][i][e] + bias[q][4 + e];
+        }
+        const bool in = inside(u);
+        const int64_t at = at_of(u);
+        if (p.pre && in) store_row(p.pre, false, at, z, p.c_store);
+        activate(ACT, z);
+        if constexpr (RES) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) z[e] += (float)res[u % kAhead][e];
+            load_res(std::integral_constant<int, u + kAhead>{});
+        }
+        if (in) store_row(p.c, false, at, z, p.c_store);
+    });
 #endif
 }
 
@@ -440,10 +523,25 @@ inline hipError_t launch_fused_grid(const void *kernel, int64_t grid, int parts,
     return hipSuccess;
 }
 
+template <class C, int ACT>
+const void *fused_direct(const FusedParams &p) {
+    return p.residual ? reinterpret_cast<const void *>(fused_direct_kernel<C, ACT, true>)
+                      : reinterpret_cast<const void *>(fused_direct_kernel<C, ACT, false>);
+}
+
 template <class C>
 hipError_t launch_fused_tile(const FusedParams &p, hipStream_t s) {
-    return launch_fused_grid(reinterpret_cast<const void *>(fused_tile_kernel<C>), (int64_t)p.num_m * p.num_n, p.parts,
-                             C::kThreads, s, p);
+    const void *kernel = reinterpret_cast<const void *>(fused_tile_kernel<C>);
+    if (p.vec && !p.out_f32 && p.parts == 1) {
+        switch (p.act) {
+            case kActRelu: kernel = fused_direct<C, kActRelu>(p); break;
+            case kActGelu: kernel = fused_direct<C, kActGelu>(p); break;
+            case kActGeluTanh: kernel = fused_direct<C, kActGeluTanh>(p); break;
+            case kActSilu: kernel = fused_direct<C, kActSilu>(p); break;
+            default: kernel = fused_direct<C, kActNone>(p); break;
+        }
+    }
+    return launch_fused_grid(kernel, (int64_t)p.num_m * p.num_n, p.parts, C::kThreads, s, p);
 }
 
 // One unit per block tile, so that they compile in parallel.
@@ -454,6 +552,12 @@ hipError_t launch_fused_128x128(const FusedParams &p, hipStream_t s);
 hipError_t launch_fused_128x64(const FusedParams &p, hipStream_t s);
 hipError_t launch_fused_64x128(const FusedParams &p, hipStream_t s);
 hipError_t launch_fused_64x64(const FusedParams &p, hipStream_t s);
+
+// More tiles than CUs, fp16 C in whole 16-byte chunks, at least 3 K-tiles (256 x 256: an even
+// number of whole ones): fused_walk.h.  dev: device-scope stores, else streaming ones.
+hipError_t launch_fused_walk_256x256(bool dev, const FusedParams &p, int cus, hipStream_t s);
+hipError_t launch_fused_walk_256x128(bool dev, const FusedParams &p, int cus, hipStream_t s);
+hipError_t launch_fused_walk_128x256(bool dev, const FusedParams &p, int cus, hipStream_t s);
 
 // Rows that are not 16-byte aligned, any K >= 1 (fused_staged.hip): wide: a 128 x 128 tile,
 // else 64 x 64.

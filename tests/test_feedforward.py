@@ -3,6 +3,7 @@
 the definitions that the GPU tests compare against.  No GPU is needed."""
 import ctypes
 import os
+import re
 import subprocess
 import sys
 
@@ -11,11 +12,13 @@ import torch
 
 import dense_fp16_gemm_f16_amd as g
 from dense_fp16_gemm_f16_amd.feedforward import Epilogue, Routing
+from tests import _codeobj
 from tests import _feedforward as ref
 
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 A, B, C, D, E, F, G, H, W = (0x10000000 * i for i in range(1, 10))  # never dereferenced
 BIG = 1 << 40
+OBJDUMP = "/opt/rocm/llvm/bin/llvm-objdump"
 
 
 def _fused(m=8, n=16, k=32, a=A, b=B, c=C, act=0, bias_f32=0, out_f32=0, bias=None, residual=None, pre=None, ws=W, size=BIG,
@@ -137,6 +140,47 @@ def test_other_architectures_are_refused():
             "assert g.lib().gemm_f16_combine_rows_grad(*t.COMBINE_GRAD.values(), None) == g.EDEVICE\n")
     env = {**os.environ, "GEMM_F16_TEST_ARCH": "gfx942"}
     subprocess.run([sys.executable, "-c", code], check=True, cwd=ROOT, env=env)
+
+
+def _registers(token):
+    """Accumulator registers of an operand: a7, or a[4:7]."""
+    m = re.match(r"a\[(\d+):(\d+)\]$", token) or re.match(r"a(\d+)()$", token)
+    return set(range(int(m[1]), int(m[2] or m[1]) + 1)) if m else set()
+
+
+@pytest.mark.skipif(not os.path.exists(OBJDUMP), reason="llvm-objdump not installed")
+def test_accumulators_rest_behind_their_mfmas(tmp_path):
+    """The MFMAs are inline asm, so the compiler leaves no wait before it reads or moves what
+    they write: no such move may stand within 18 wait states behind one (16x16x32: 8 passes of 4
+    cycles and a few more) in any kernel of the products with an epilogue."""
+    with open(g.LIB_PATH, "rb") as f:
+        blob = f.read()
+    kernels, bad = set(), []
+    for i, (triple, obj) in enumerate(_codeobj._bundles(blob)):
+        if "gfx950" not in triple or b"fused_" not in obj:
+            continue
+        path = tmp_path / f"co{i}.o"
+        path.write_bytes(obj)
+        asm = subprocess.run([OBJDUMP, "-d", "--no-show-raw-insn", str(path)], capture_output=True, text=True, check=True).stdout
+        name, age, recent = None, 0, []
+        for line in asm.splitlines():
+            head = re.match(r"[0-9a-f]+ <(\S+)>:", line)
+            if head:
+                name, recent = head[1], []
+                kernels.add(name)
+                continue
+            op, _, rest = line.split("//")[0].strip().partition(" ")
+            if not name or not op:
+                continue
+            args = [x.strip() for x in rest.split(",")]
+            age += 1 + (int(args[0], 0) if op == "s_nop" else 0)
+            if op.startswith("v_mfma"):
+                recent = [r for r in recent if age - r[0] < 40] + [(age, _registers(args[0]))]
+            elif "accvgpr" in op:
+                touched = set().union(*map(_registers, args))
+                bad += [(name, line.strip()) for at, r in recent if r & touched and age - at < 18]
+    assert any("fused_walk_kernel" in k for k in kernels) and any("fused_tile_kernel" in k for k in kernels)
+    assert not bad, (len(bad), bad[:4])
 
 
 def _h(*shape):

@@ -57,6 +57,49 @@ def test_fused_exact_sums(m, n, k, act):
         assert torch.equal(got, y.to(out_type))
 
 
+# (tile that the automatic choice takes, whether there are more of them than 256 CUs, sizes):
+# even, odd and partial K-tile counts, a last row and column of tiles cut short
+TILED = [("256x256", False, (3000, 4104, 1024)), ("256x256", False, (3000, 4104, 1032)), ("256x256", True, (6000, 4104, 512)),
+         ("256x256", True, (6000, 4104, 1032)), ("256x128", False, (2048, 2056, 512)), ("256x128", False, (2048, 2056, 1032)),
+         ("256x128", True, (3000, 4104, 192)), ("256x128", True, (3000, 4104, 200)), ("256x128", True, (4100, 5000, 128)),
+         ("128x256", False, (5000, 1000, 384)), ("128x256", False, (4100, 1000, 1032)), ("128x256", True, (4096, 4096, 192)),
+         ("128x256", True, (6000, 2056, 200)), ("128x256", True, (6000, 2056, 264)), ("128x128", False, (2100, 1000, 192)),
+         ("128x128", False, (2100, 1000, 256)), ("128x128", True, (4100, 1000, 200)), ("128x64", False, (1536, 1000, 192)),
+         ("128x64", True, (2048, 2056, 192)), ("64x128", True, (4100, 1000, 192)), ("64x128", True, (2100, 1536, 128)),
+         ("64x64", True, (2100, 1000, 128))]
+
+
+@pytest.mark.parametrize("tile,more,size", TILED)
+def test_fused_on_every_tile(tile, more, size):
+    _say("fused tiles", tile, more, size)
+    m, n, k = size
+    names = {v: name[5:] for name, v in vars(g).items() if name.startswith("TILE_")}
+    bm, bn = (int(x) for x in tile.split("x"))
+    assert names[g.select_tile(m, n, k)] == tile and (-(-m // bm) * -(-n // bn) > 256) == more
+    gen = _gen(m + n + k)
+    a, b = ref.eighths(gen, m, k), ref.eighths(gen, n, k)
+    bias, res = ref.eighths(gen, n), ref.eighths(gen, m, n)
+    product = ref.fused(a, b, None, None, None)[1]
+    for bias_t in (None, bias, bias.float()):
+        for act in (None, "relu"):
+            for res_t in (None, res):
+                z = product if bias_t is None else product + bias_t.double()
+                y = ref.act(act, z) if res_t is None else ref.act(act, z) + res_t.double()
+                buf = torch.full((m * n + 64,), 7.0, dtype=F16, device="cuda")
+                out = buf[32:32 + m * n].view(m, n)
+                got, pre = g.gemm_f16_fused_nt(a, b, bias_t, act=act, residual=res_t, return_pre=True, out=out)
+                assert torch.equal(out, y.to(F16)) and torch.equal(pre, z.to(F16)), (bias_t is None, act, res_t is None)
+                assert bool((buf[:32] == 7).all()) and bool((buf[32 + m * n:] == 7).all())
+                assert torch.equal(g.gemm_f16_fused_nt(a, b, bias_t, act=act, residual=res_t), out)
+    y = product + bias.double()
+    assert torch.equal(g.gemm_f16_fused_nt(a, b, bias, residual=res.float(), out_dtype=F32), (y + res.double()).float())
+    # the other activations, and none of the exact sums' help
+    b = ref.normal(gen, n, k, std=2 * k**-0.5)
+    for act in ("gelu", "gelu_tanh", "silu"):
+        y, z, err, ez = ref.fused(a, b, bias, act, None)
+        assert ref.worst(g.gemm_f16_fused_nt(a, b, bias, act=act), y, err, F16) <= 1
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 1000, 2048), (33, 200, 777), (200, 264, 512), (1500, 1200, 320), (4352, 4096, 256)])
 @pytest.mark.parametrize("act", ref.ACTS)
 def test_fused_random(m, n, k, act):
