@@ -10,6 +10,8 @@
 
 namespace gemm_f16 {
 
+// gfx950's CUs: the sizes alone say what workspace a call takes
+constexpr int kFusedCus = 256;
 constexpr int64_t kMaxSide = int64_t(1) << 30, kMaxDepth = int64_t(1) << 22, kMaxArea = int64_t(1) << 47;
 
 static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -20,8 +22,6 @@ static int check_fused(int64_t m, int64_t n, int64_t k) {
     if (m < 0 || n < 0 || k < 0 || m >= kMaxSide || n >= kMaxSide || k >= kMaxDepth) return GEMM_F16_EINVAL;
     return below(kMaxArea, m, n) ? GEMM_F16_OK : GEMM_F16_EINVAL;
 }
-
-static bool fused_is_few(int64_t m, int64_t k) { return m <= kFusedFewRows && k >= 8; }
 
 struct TileSize {
     int bm, bn;
@@ -47,6 +47,103 @@ static bool walk_takes(int tile, const TileSize &ts, int cus, const FusedParams 
         return false;
     if (tile == GEMM_F16_TILE_256x256) return p.k % 128 == 0 && p.k >= 256;
     return (tile == GEMM_F16_TILE_256x128 || tile == GEMM_F16_TILE_128x256) && p.k_tiles >= 3;
+}
+
+static hipError_t launch_tile(bool direct, bool ring, int tile, const FusedParams &p, hipStream_t s) {
+    if (!direct) return launch_fused_staged(tile == GEMM_F16_TILE_128x128, p, s);
+    if (ring) return launch_fused_ring(p, s);
+    switch (tile) {
+        case GEMM_F16_TILE_256x256: return launch_fused_256x256(p, s);
+        case GEMM_F16_TILE_256x128: return launch_fused_256x128(p, s);
+        case GEMM_F16_TILE_128x256: return launch_fused_128x256(p, s);
+        case GEMM_F16_TILE_128x128: return launch_fused_128x128(p, s);
+        case GEMM_F16_TILE_128x64: return launch_fused_128x64(p, s);
+        case GEMM_F16_TILE_64x128: return launch_fused_64x128(p, s);
+        default: return launch_fused_64x64(p, s);
+    }
+}
+
+// Modelled time (us) of a product, or of one in parts of K:
+//     c + a K-tiles of a part x (1, or e share where more than a workgroup falls to a CU) + b share
+// with share the workgroups per CU, no less for the K loop than 0.18 us for each MB of A and B;
+// with parts, 2.05 + 0.26 a part + 0.118 for each MB of their sums, written and read, for the
+// join.  Least-squares fits, in relative error, to 1852 timings of 120 shapes (rows 17 to 16384, N
+// 8 to 8192, K 64 to 8192, inputs cold in the caches) on MI355X.
+struct FusedCost {
+    int tile, bm, bn;
+    bool ring;
+    double c, a, e, b;
+};
+
+static double fused_us(const FusedCost &f, int64_t m, int64_t n, int64_t k, int parts, int part_kt) {
+    const double share = (double)(cdiv(m, f.bm) * cdiv(n, f.bn) * parts) / kFusedCus;
+    const double loop = f.a * part_kt * (share > 1 ? std::max(1.0, f.e * share) : 1.0);
+    const double inputs = 0.18 * 2e-6 * (double)((m + n) * k);
+    const double join = parts > 1 ? 2.05 + 0.26 * parts + 0.118 * 8e-6 * (double)(m * n) * parts : 0;
+    return f.c + std::max(loop, inputs) + f.b * share + join;
+}
+
+// Block tile of a product, and the parts of its K (1: none) of part_kt K-tiles each.  By the
+// sizes alone: they say what workspace a call takes.
+struct FusedPlan {
+    int tile;
+    bool ring;
+    int parts, part_kt;
+    double us;
+};
+
+// The dense product's choice of tile, unless the model has one in parts of K, or on the ring, at
+// less than 0.9 of its time.  On those 120 shapes the plan took 1.034 of the fastest variant's time
+// in the geometric mean (the dense choice alone: 1.28); 128 rows of 4096 x 4096 take 16.6 us in 3
+// parts, 26 undivided; 1024 of 64 x 4096 12 and 26; 512 of 4096 x 4096 30, undivided.
+static FusedPlan fused_plan(int64_t m, int64_t n, int64_t k) {
+    static const FusedCost costs[] = {
+        {GEMM_F16_TILE_64x64, 64, 64, false, 2.41, 0.358, 1.253, 1.63},
+        {GEMM_F16_TILE_64x128, 64, 128, false, 3.19, 0.408, 1.438, 2.11},
+        {GEMM_F16_TILE_128x64, 128, 64, false, 3.12, 0.412, 1.493, 2.02},
+        {GEMM_F16_TILE_128x256, 128, 256, false, 7.56, 0.645, 2.536, 4.27},
+        {GEMM_F16_TILE_128x128, 128, 128, false, 4.99, 0.444, 1.519, 3.56},  // from here on also in parts
+        {GEMM_F16_TILE_256x128, 256, 128, false, 7.45, 0.619, 1.896, 4.03},
+        {GEMM_F16_TILE_64x64, 64, 64, true, 4.14, 0.294, 0.808, 1.00},
+    };
+    const int k_tiles = (int)cdiv(k, 64);
+    FusedPlan plan = {gemm_f16_select_tile(m, n, k), false, 1, k_tiles, 1e300};
+    if (plan.tile < 0) return plan;
+    double whole = 1e300;  // 256 x 256: enough tiles, or nearly
+    for (const FusedCost &f : costs)
+        if (f.tile == plan.tile && !f.ring) whole = fused_us(f, m, n, k, 1, k_tiles);
+    if (whole == 1e300) return plan;
+    plan.us = whole;
+    // One tile's width holds all of the columns (rows), and the rows' (columns') bytes, read
+    // once, are what the time is: the ring keeps more of them in flight (16384 rows of 64 x 4096:
+    // 31.6 us, 44.9 with two stages).
+    if (plan.tile == GEMM_F16_TILE_64x64 && std::min(m, n) <= 64 && (m + n) * k * 2 >= int64_t(32) << 20) {
+        plan.ring = true;
+        plan.us = whole = fused_us(costs[6], m, n, k, 1, k_tiles);
+    }
+    FusedPlan best = {0, false, 1, k_tiles, 0.9 * whole};
+    for (const FusedCost &f : costs) {
+        if (!f.ring && f.tile != GEMM_F16_TILE_128x128 && f.tile != GEMM_F16_TILE_256x128) continue;
+        const int64_t tiles = cdiv(m, f.bm) * cdiv(n, f.bn);
+        for (int parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
+            if (parts == 1 ? !f.ring : 2 * parts > k_tiles || tiles * parts > 10 * kFusedCus) continue;
+            const int part_kt = (int)cdiv(k_tiles, parts), really = (int)cdiv(k_tiles, part_kt);
+            const double us = fused_us(f, m, n, k, really, part_kt);
+            if (us < best.us) best = {f.tile, f.ring, really, part_kt, us};
+        }
+    }
+    return best.tile ? best : plan;
+}
+
+// Whether the few-row kernel takes a product: up to 16 rows always, up to 64 where the model has
+// it ahead.  Its time is what each workgroup reads of A, 16 rows of it at a time (N 64, K 4096: 9.6
+// us for 16 rows, 23 for 64, where 8 parts take 9), and B's bytes.
+static bool fused_is_few(int64_t m, int64_t n, int64_t k) {
+    if (k < 8 || m > kFusedFewRows) return false;
+    if (m <= 16) return true;
+    const double tiles = (double)cdiv(m, 16);
+    const double us = 4.1 + (double)k / 4096 * (2.6 + 2.2 * tiles + 0.55 * tiles * tiles) + 0.07 * 2e-6 * (double)(n * k);
+    return us < fused_plan(m, n, k).us;
 }
 
 static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, void *c, const gemm_f16_epilogue &e,
@@ -102,22 +199,27 @@ static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, 
         p.parts = 0;
         return status(launch_fused_join(p, s));
     }
-    if (fused_is_few(m, k)) return status(launch_fused_few(p, s));
+    if (fused_is_few(m, n, k)) return status(launch_fused_few(p, s));
     const bool direct = k % 8 == 0 && aligned16(a) && aligned16(b);
-    int tile = gemm_f16_select_tile(m, n, k);
-    if (tile < 0) return tile;
-    if (!direct) {
-        const bool wide = tile != GEMM_F16_TILE_64x64;
-        tile = wide ? GEMM_F16_TILE_128x128 : GEMM_F16_TILE_64x64;
-    }
+    const FusedPlan plan = fused_plan(m, n, k);
+    if (plan.tile < 0) return plan.tile;
+    int tile = plan.tile;
+    if (!direct) tile = tile != GEMM_F16_TILE_64x64 ? GEMM_F16_TILE_128x128 : GEMM_F16_TILE_64x64;
     const TileSize ts = tile_size(tile);
     p.num_m = (int32_t)cdiv(m, ts.bm);
     p.num_n = (int32_t)cdiv(n, ts.bn);
     if ((int64_t)p.num_m * p.num_n >= (int64_t(1) << 31)) return GEMM_F16_EINVAL;
     p.swizzle = 4;
     p.xcd = gemm_f16_select_xcd(p.num_m, p.num_n, p.swizzle, cus);
-    if (!direct) return status(launch_fused_staged(tile == GEMM_F16_TILE_128x128, p, s));
-    if (walk_takes(tile, ts, cus, p)) {
+    if (plan.parts > 1) {
+        FusedParams q = p;
+        q.parts = plan.parts;
+        q.part_kt = plan.part_kt;
+        const hipError_t e = launch_tile(direct, plan.ring, tile, q, s);
+        if (e != hipSuccess) return status(e);
+        return status(launch_fused_join(q, s));
+    }
+    if (direct && !plan.ring && walk_takes(tile, ts, cus, p)) {
         const bool dev = p.c_store == kStoreDevice;
         switch (tile) {
             case GEMM_F16_TILE_256x256: return status(launch_fused_walk_256x256(dev, p, cus, s));
@@ -125,15 +227,7 @@ static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, 
             default: return status(launch_fused_walk_128x256(dev, p, cus, s));
         }
     }
-    switch (tile) {
-        case GEMM_F16_TILE_256x256: return status(launch_fused_256x256(p, s));
-        case GEMM_F16_TILE_256x128: return status(launch_fused_256x128(p, s));
-        case GEMM_F16_TILE_128x256: return status(launch_fused_128x256(p, s));
-        case GEMM_F16_TILE_128x128: return status(launch_fused_128x128(p, s));
-        case GEMM_F16_TILE_128x64: return status(launch_fused_128x64(p, s));
-        case GEMM_F16_TILE_64x128: return status(launch_fused_64x128(p, s));
-        default: return status(launch_fused_64x64(p, s));
-    }
+    return status(launch_tile(direct, plan.ring, tile, p, s));
 }
 
 static int check_routing(int64_t tokens, int64_t experts, int64_t fan, int32_t logits_f32, const gemm_f16_routing *r) {
@@ -177,7 +271,10 @@ extern "C" {
 
 int64_t gemm_f16_fused_workspace(int64_t m, int64_t n, int64_t k) {
     const int rc = check_fused(m, n, k);
-    return rc != GEMM_F16_OK ? rc : 0;
+    if (rc != GEMM_F16_OK || m == 0 || n == 0 || k == 0 || fused_is_few(m, n, k)) return rc;
+    const FusedPlan plan = fused_plan(m, n, k);
+    if (plan.tile < 0) return plan.tile;
+    return plan.parts > 1 ? plan.parts * m * n * 4 : 0;
 }
 
 int gemm_f16_fused_nt(int64_t m, int64_t n, int64_t k, const void *a, const void *b, void *c,

@@ -559,6 +559,9 @@ hipError_t launch_fused_walk_256x256(bool dev, const FusedParams &p, int cus, hi
 hipError_t launch_fused_walk_256x128(bool dev, const FusedParams &p, int cus, hipStream_t s);
 hipError_t launch_fused_walk_128x256(bool dev, const FusedParams &p, int cus, hipStream_t s);
 
+// 64 x 64 tiles on a ring of LDS stages (fused_ring.hip).
+hipError_t launch_fused_ring(const FusedParams &p, hipStream_t s);
+
 // Rows that are not 16-byte aligned, any K >= 1 (fused_staged.hip): wide: a 128 x 128 tile,
 // else 64 x 64.
 hipError_t launch_fused_staged(bool wide, const FusedParams &p, hipStream_t s);
