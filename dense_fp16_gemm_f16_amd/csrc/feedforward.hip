@@ -192,9 +192,11 @@ static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, 
     // as the dense product's: device scope while everything fits in the 256 MiB Infinity
     // Cache, past it streaming stores on rows of whole 128-byte lines
     const int64_t each = es * (e.residual ? 2 : 1) + (e.pre ? 2 : 0);
-    p.c_store = (m + n) * k * 2 + m * n * each <= (int64_t(256) << 20)             ? kStoreDevice
-                : (n * es) % 128 == 0 && (uintptr_t)c % 128 == 0 ? kStoreStream
-                                                                                   : kStoreDefault;
+    p.c_store = kStoreDefault;
+    if ((m + n) * k * 2 + m * n * each <= (int64_t(256) << 20))
+        p.c_store = kStoreDevice;
+    else if ((n * es) % 128 == 0 && (uintptr_t)c % 128 == 0)
+        p.c_store = kStoreStream;
     if (k == 0) {
         p.parts = 0;
         return status(launch_fused_join(p, s));

@@ -60,7 +60,116 @@ __global__ __launch_bounds__(kFewWaves *kWave) void fused_few_kernel(const Fused
 #endif
 }
 
+// ---- one or two rows ---------------------------------------------------------------
+//
+// A wave takes R rows of B and multiplies lane by lane: 16 bytes a lane, so that a load covers a
+// whole kilobyte of a row, where the MFMA's layout takes 64 bytes of each of 16 rows.  R rows by S
+// steps of 512 elements, 16 loads, are in flight a wave.  The lanes' sums meet in a fixed order.
+// Cold weights, us, beside the MFMA's kernel: one row of 4096 x 4096 8.1 (9.9), 1024 x 4096 4.6
+// (7.8), 4096 x 1024 4.8 (5.1), two rows 9.2 (10.2), 5.2 (8.4), 5.6 (5.1): taken by dot_takes.
+// From three rows on the vector unit's products cost more than the loads gain (four: 11.3, 10.4).
+constexpr int kDotWaves = 4;
+
+// Up to S steps of a row (K >= 8), 512 elements each, `count` of them from step top - 1 downwards;
+// 8 elements at 8 lane of each.  The first one, where `partial`, reaches past K (as in thin_load).
+template <int S>
+__device__ __forceinline__ void dot_load(half8 (&v)[S], const _Float16 *row, int top, int count, bool partial, int lane,
+                                         int k_elems) {
+    const int k0 = 512 * (top - 1) + 8 * lane;
+#pragma unroll
+    for (int s = 0; s < S; ++s) {
+        v[s] = half8{};
+        if (s >= count) continue;
+        const int k = s == 0 && partial ? min(k0, k_elems - 8) : k0 - 512 * s;
+        v[s] = __builtin_bit_cast(half8, (int4v)*reinterpret_cast<const int4u *>(row + k));
+    }
+    if (partial) {
+        const int past = 8 - (k_elems - k0);  // elements to shift out
+        unsigned __int128 w = __builtin_bit_cast(unsigned __int128, v[0]);
+        if (past > 0) w = past < 8 ? w >> (16 * past) : 0;
+        v[0] = __builtin_bit_cast(half8, w);
+    }
+}
+
+// x from the lane `by` places away in its row of 16.
+template <int CTRL>
+__device__ __forceinline__ float dot_turn(float x) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
+}
+
+template <int M, int R, int S>
+__global__ __launch_bounds__(kDotWaves *kWave) void fused_dot_kernel(const FusedParams p) {
+#ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int64_t n0 = ((int64_t)(p.first + blockIdx.x) * kDotWaves + wave) * R;
+    if (n0 >= p.n) return;
+    float sum[M][R] = {};
+    for (int top = (p.k + 511) / 512; top > 0; top -= S) {
+        const int count = min(top, S);
+        const bool partial = 512 * top > p.k;
+        half8 a[M][S], b[R][S];
+#pragma unroll
+        for (int r = 0; r < R; ++r)  // (past the last row the last one again: not stored)
+            dot_load(b[r], p.b + (n0 + r < p.n ? n0 + r : p.n - 1) * p.k, top, count, partial, lane, p.k);
+#pragma unroll
+        for (int m = 0; m < M; ++m) dot_load(a[m], p.a + (int64_t)m * p.k, top, count, partial, lane, p.k);
+#pragma unroll
+        for (int s = 0; s < S; ++s) {
+            if (s >= count) continue;
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum[m][r] = __builtin_fmaf((float)a[m][s][e], (float)b[r][s][e], sum[m][r]);
+        }
+    }
+    // lane m R + r: row m, column n0 + r
+    float z = 0.0f;
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float x = sum[m][r];
+            x += dot_turn<0x128>(x);  // rotations of a row of 16 lanes by 8, 4, 2 and 1
+            x += dot_turn<0x124>(x);
+            x += dot_turn<0x122>(x);
+            x += dot_turn<0x121>(x);
+            x += __shfl_xor(x, 16);
+            x += __shfl_xor(x, 32);
+            z = lane == m * R + r ? x : z;
+        }
+    const int m = lane / R;
+    const int64_t n = n0 + lane % R;
+    if (m >= M || n >= p.n) return;
+    const int64_t at = (int64_t)m * p.n + n;
+    float y[1] = {z + (p.bias ? load1(p.bias, p.bias_f32 != 0, n) : 0.0f)};
+    if (p.pre) p.pre[at] = (_Float16)y[0];
+    activate(p.act, y);
+    if (p.residual) y[0] += load1(p.residual, p.out_f32 != 0, at);
+    if (p.out_f32)
+        static_cast<float *>(p.c)[at] = y[0];
+    else
+        static_cast<_Float16 *>(p.c)[at] = (_Float16)y[0];
+#endif
+}
+
+// Short rows, and two that are not long, are the MFMA's: 300 x 200 takes one row 3.6 us there, 4.0 here.
+static bool dot_takes(const FusedParams &p) { return p.m <= 2 && p.k > 512 * p.m; }
+
+// Rows a wave by K: its loads stay 16.
+static hipError_t launch_dot(const FusedParams &p, hipStream_t s) {
+    const int rows = p.k > 2048 ? 2 : p.k > 1024 ? 4 : 8;  // (8: one row of A)
+    const void *kernel = p.m == 2    ? (rows == 2 ? reinterpret_cast<const void *>(fused_dot_kernel<2, 2, 8>)
+                                                  : reinterpret_cast<const void *>(fused_dot_kernel<2, 4, 4>))
+                         : rows == 2 ? reinterpret_cast<const void *>(fused_dot_kernel<1, 2, 8>)
+                         : rows == 4 ? reinterpret_cast<const void *>(fused_dot_kernel<1, 4, 4>)
+                                     : reinterpret_cast<const void *>(fused_dot_kernel<1, 8, 2>);
+    return launch_fused_grid(kernel, ((int64_t)p.n + rows * kDotWaves - 1) / (rows * kDotWaves), 1, kDotWaves * kWave, s, p);
+}
+
 hipError_t launch_fused_few(const FusedParams &p, hipStream_t s) {
+    if (dot_takes(p)) return launch_dot(p, s);
     int waves = 1;  // that K keeps busy in one pass
     while (waves < kFewWaves && waves * kFewSteps * 32 < p.k) waves *= 2;
     const int tiles = (p.m + 15) / 16;

@@ -57,6 +57,24 @@ def test_fused_exact_sums(m, n, k, act):
         assert torch.equal(got, y.to(out_type))
 
 
+# One and two rows: K below, at and above what the vector unit's kernel takes, its steps of 512 and
+# passes of 8 of them ending anywhere, and column counts that end inside a wave's and a workgroup's.
+@pytest.mark.parametrize("m", [1, 2])
+@pytest.mark.parametrize("n,k", [(1, 513), (3, 520), (8, 1023), (33, 1024), (31, 1025), (50, 1544), (100, 2047), (17, 2048), (9, 2049),
+                                 (7, 4096), (1000, 4097), (66, 4103), (5, 9999), (2, 512)])
+def test_fused_one_and_two_rows(m, n, k):
+    _say("fused one and two rows", m, n, k)
+    gen = _gen(n + k)
+    a, b, bias = ref.eighths(gen, m, k), ref.eighths(gen, n, k), ref.eighths(gen, n)
+    for offset in (0, 1):
+        for out_type in (F16, F32):
+            residual = ref.eighths(gen, m, n).to(out_type)
+            y, z, _, _ = ref.fused(a, b, bias, "relu", residual)
+            got, pre = g.gemm_f16_fused_nt(_offset(a, offset), _offset(b, offset), bias, act="relu", residual=residual,
+                                           return_pre=True, out_dtype=out_type)
+            assert torch.equal(got, y.to(out_type)) and torch.equal(pre, z.to(F16))
+
+
 # (tile that the automatic choice takes, whether there are more of them than 256 CUs, sizes):
 # even, odd and partial K-tile counts, a last row and column of tiles cut short
 TILED = [("256x256", False, (3000, 4104, 1024)), ("256x256", False, (3000, 4104, 1032)), ("256x256", True, (6000, 4104, 512)),
