@@ -75,28 +75,31 @@ struct FusedCost {
     double c, a, e, b;
 };
 
-static double fused_us(const FusedCost &f, int64_t m, int64_t n, int64_t k, int parts, int part_kt) {
-    const double share = (double)(cdiv(m, f.bm) * cdiv(n, f.bn) * parts) / kFusedCus;
+static int64_t fused_tiles(const FusedCost &f, int64_t m, int64_t n) { return cdiv(m, f.bm) * cdiv(n, f.bn); }
+
+static double fused_us(const FusedCost &f, int64_t tiles, int64_t m, int64_t n, int64_t k, int parts, int part_kt) {
+    const double share = (double)(tiles * parts) / kFusedCus;
     const double loop = f.a * part_kt * (share > 1 ? std::max(1.0, f.e * share) : 1.0);
     const double inputs = 0.18 * 2e-6 * (double)((m + n) * k);
     const double join = parts > 1 ? 2.05 + 0.26 * parts + 0.118 * 8e-6 * (double)(m * n) * parts : 0;
     return f.c + std::max(loop, inputs) + f.b * share + join;
 }
 
-// Block tile of a product, and the parts of its K (1: none) of part_kt K-tiles each.  By the
-// sizes alone: they say what workspace a call takes.
+// Block tile of a product, and the parts of its K (1: none) of part_kt K-tiles each; or the
+// few-row kernel.  By the sizes alone: they say what workspace a call takes.
 struct FusedPlan {
     int tile;
     bool ring;
     int parts, part_kt;
     double us;
+    bool few;
 };
 
 // The dense product's choice of tile, unless the model has one in parts of K, or on the ring, at
 // less than 0.9 of its time.  On those 120 shapes the plan took 1.034 of the fastest variant's time
 // in the geometric mean (the dense choice alone: 1.28); 128 rows of 4096 x 4096 take 16.6 us in 3
 // parts, 26 undivided; 1024 of 64 x 4096 12 and 26; 512 of 4096 x 4096 30, undivided.
-static FusedPlan fused_plan(int64_t m, int64_t n, int64_t k) {
+static FusedPlan fused_tile_plan(int64_t m, int64_t n, int64_t k) {
     static const FusedCost costs[] = {
         {GEMM_F16_TILE_64x64, 64, 64, false, 2.41, 0.358, 1.253, 1.63},
         {GEMM_F16_TILE_64x128, 64, 128, false, 3.19, 0.408, 1.438, 2.11},
@@ -107,11 +110,11 @@ static FusedPlan fused_plan(int64_t m, int64_t n, int64_t k) {
         {GEMM_F16_TILE_64x64, 64, 64, true, 4.14, 0.294, 0.808, 1.00},
     };
     const int k_tiles = (int)cdiv(k, 64);
-    FusedPlan plan = {gemm_f16_select_tile(m, n, k), false, 1, k_tiles, 1e300};
+    FusedPlan plan = {gemm_f16_select_tile(m, n, k), false, 1, k_tiles, 1e300, false};
     if (plan.tile < 0) return plan;
     double whole = 1e300;  // 256 x 256: enough tiles, or nearly
     for (const FusedCost &f : costs)
-        if (f.tile == plan.tile && !f.ring) whole = fused_us(f, m, n, k, 1, k_tiles);
+        if (f.tile == plan.tile && !f.ring) whole = fused_us(f, fused_tiles(f, m, n), m, n, k, 1, k_tiles);
     if (whole == 1e300) return plan;
     plan.us = whole;
     // One tile's width holds all of the columns (rows), and the rows' (columns') bytes, read
@@ -119,31 +122,39 @@ static FusedPlan fused_plan(int64_t m, int64_t n, int64_t k) {
     // 31.6 us, 44.9 with two stages).
     if (plan.tile == GEMM_F16_TILE_64x64 && std::min(m, n) <= 64 && (m + n) * k * 2 >= int64_t(32) << 20) {
         plan.ring = true;
-        plan.us = whole = fused_us(costs[6], m, n, k, 1, k_tiles);
+        plan.us = whole = fused_us(costs[6], fused_tiles(costs[6], m, n), m, n, k, 1, k_tiles);
     }
-    FusedPlan best = {0, false, 1, k_tiles, 0.9 * whole};
+    FusedPlan best = {0, false, 1, k_tiles, 0.9 * whole, false};
     for (const FusedCost &f : costs) {
         if (!f.ring && f.tile != GEMM_F16_TILE_128x128 && f.tile != GEMM_F16_TILE_256x128) continue;
-        const int64_t tiles = cdiv(m, f.bm) * cdiv(n, f.bn);
+        const int64_t tiles = fused_tiles(f, m, n);
         for (int parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
             if (parts == 1 ? !f.ring : 2 * parts > k_tiles || tiles * parts > 10 * kFusedCus) continue;
-            const int part_kt = (int)cdiv(k_tiles, parts), really = (int)cdiv(k_tiles, part_kt);
-            const double us = fused_us(f, m, n, k, really, part_kt);
-            if (us < best.us) best = {f.tile, f.ring, really, part_kt, us};
+            const int part_kt = (k_tiles + parts - 1) / parts, really = (k_tiles + part_kt - 1) / part_kt;
+            const double us = fused_us(f, tiles, m, n, k, really, part_kt);
+            if (us < best.us) best = {f.tile, f.ring, really, part_kt, us, false};
         }
     }
     return best.tile ? best : plan;
 }
 
-// Whether the few-row kernel takes a product: up to 16 rows always, up to 64 where the model has
-// it ahead.  Its time is what each workgroup reads of A, 16 rows of it at a time (N 64, K 4096: 9.6
-// us for 16 rows, 23 for 64, where 8 parts take 9), and B's bytes.
-static bool fused_is_few(int64_t m, int64_t n, int64_t k) {
-    if (k < 8 || m > kFusedFewRows) return false;
-    if (m <= 16) return true;
+// The few-row kernel takes up to 16 rows always, up to 64 where the model has it ahead.  Its
+// time is what each workgroup reads of A, 16 rows of it at a time (N 64, K 4096: 9.6 us for 16 rows,
+// 23 for 64, where 8 parts take 9), and B's bytes.
+static FusedPlan fused_plan(int64_t m, int64_t n, int64_t k) {
+    const FusedPlan few = {0, false, 1, 0, 0, true};
+    if (k >= 8 && m <= 16) return few;
+    const FusedPlan plan = fused_tile_plan(m, n, k);
+    if (k < 8 || m > kFusedFewRows) return plan;
     const double tiles = (double)cdiv(m, 16);
     const double us = 4.1 + (double)k / 4096 * (2.6 + 2.2 * tiles + 0.55 * tiles * tiles) + 0.07 * 2e-6 * (double)(n * k);
-    return us < fused_plan(m, n, k).us;
+    return us < plan.us ? few : plan;
+}
+
+// Bytes of workspace, or an error.
+static int64_t fused_need(const FusedPlan &plan, int64_t m, int64_t n) {
+    if (plan.tile < 0) return plan.tile;
+    return plan.parts > 1 ? plan.parts * m * n * 4 : 0;
 }
 
 static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, void *c, const gemm_f16_epilogue &e,
@@ -153,7 +164,10 @@ static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, 
     if (e.act < GEMM_F16_ACT_NONE || e.act > GEMM_F16_ACT_LAST || e.bias_f32 < 0 || e.bias_f32 > 1 || e.out_f32 < 0 ||
         e.out_f32 > 1)
         return GEMM_F16_EINVAL;
-    const int64_t need = gemm_f16_fused_workspace(m, n, k);
+    FusedPlan plan = {};
+    if (m > 0 && n > 0 && k > 0) plan = fused_plan(m, n, k);
+    const int64_t need = fused_need(plan, m, n);
+    if (need < 0) return (int)need;
     if (workspace_bytes < need) return GEMM_F16_EINVAL;
     if (m == 0 || n == 0) return GEMM_F16_OK;
     const int es = e.out_f32 ? 4 : 2, bs = e.bias_f32 ? 4 : 2;
@@ -201,10 +215,8 @@ static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, 
         p.parts = 0;
         return status(launch_fused_join(p, s));
     }
-    if (fused_is_few(m, n, k)) return status(launch_fused_few(p, s));
+    if (plan.few) return status(launch_fused_few(p, s));
     const bool direct = k % 8 == 0 && aligned16(a) && aligned16(b);
-    const FusedPlan plan = fused_plan(m, n, k);
-    if (plan.tile < 0) return plan.tile;
     int tile = plan.tile;
     if (!direct) tile = tile != GEMM_F16_TILE_64x64 ? GEMM_F16_TILE_128x128 : GEMM_F16_TILE_64x64;
     const TileSize ts = tile_size(tile);
@@ -273,10 +285,8 @@ extern "C" {
 
 int64_t gemm_f16_fused_workspace(int64_t m, int64_t n, int64_t k) {
     const int rc = check_fused(m, n, k);
-    if (rc != GEMM_F16_OK || m == 0 || n == 0 || k == 0 || fused_is_few(m, n, k)) return rc;
-    const FusedPlan plan = fused_plan(m, n, k);
-    if (plan.tile < 0) return plan.tile;
-    return plan.parts > 1 ? plan.parts * m * n * 4 : 0;
+    if (rc != GEMM_F16_OK || m == 0 || n == 0 || k == 0) return rc;
+    return fused_need(fused_plan(m, n, k), m, n);
 }
 
 int gemm_f16_fused_nt(int64_t m, int64_t n, int64_t k, const void *a, const void *b, void *c,
