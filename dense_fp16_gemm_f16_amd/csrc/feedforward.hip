@@ -23,10 +23,6 @@ static int check_fused(int64_t m, int64_t n, int64_t k) {
     return below(kMaxArea, m, n) ? GEMM_F16_OK : GEMM_F16_EINVAL;
 }
 
-struct TileSize {
-    int bm, bn;
-};
-
 static TileSize tile_size(int tile) {
     switch (tile) {
         case GEMM_F16_TILE_256x256: return {256, 256};
@@ -49,8 +45,24 @@ static bool walk_takes(int tile, const TileSize &ts, int cus, const FusedParams 
     return (tile == GEMM_F16_TILE_256x128 || tile == GEMM_F16_TILE_128x256) && p.k_tiles >= 3;
 }
 
+// Tile of rows that are not 16-byte aligned: their loads hold too many registers for the
+// largest.
+static int staged_tile(int tile) {
+    switch (tile) {
+        case GEMM_F16_TILE_256x256:
+        case GEMM_F16_TILE_128x256: return GEMM_F16_TILE_128x256;
+        case GEMM_F16_TILE_256x128:
+        case GEMM_F16_TILE_128x128: return GEMM_F16_TILE_128x128;
+        default: return GEMM_F16_TILE_64x64;
+    }
+}
+
+// direct: 16-byte aligned rows; otherwise the tile is one of staged_tile.
 static hipError_t launch_tile(bool direct, bool ring, int tile, const FusedParams &p, hipStream_t s) {
-    if (!direct) return launch_fused_staged(tile == GEMM_F16_TILE_128x128, p, s);
+    if (!direct) {
+        const bool dwords = p.k % 2 == 0 && (uintptr_t)p.a % 4 == 0 && (uintptr_t)p.b % 4 == 0;
+        return launch_fused_staged(tile_size(tile), dwords, p, s);
+    }
     if (ring) return launch_fused_ring(p, s);
     switch (tile) {
         case GEMM_F16_TILE_256x256: return launch_fused_256x256(p, s);
@@ -217,8 +229,7 @@ static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, 
     }
     if (plan.few) return status(launch_fused_few(p, s));
     const bool direct = k % 8 == 0 && aligned16(a) && aligned16(b);
-    int tile = plan.tile;
-    if (!direct) tile = tile != GEMM_F16_TILE_64x64 ? GEMM_F16_TILE_128x128 : GEMM_F16_TILE_64x64;
+    const int tile = direct ? plan.tile : staged_tile(plan.tile);
     const TileSize ts = tile_size(tile);
     p.num_m = (int32_t)cdiv(m, ts.bm);
     p.num_n = (int32_t)cdiv(n, ts.bn);

@@ -562,9 +562,13 @@ hipError_t launch_fused_walk_128x256(bool dev, const FusedParams &p, int cus, hi
 // 64 x 64 tiles on a ring of LDS stages (fused_ring.hip).
 hipError_t launch_fused_ring(const FusedParams &p, hipStream_t s);
 
-// Rows that are not 16-byte aligned, any K >= 1 (fused_staged.hip): wide: a 128 x 128 tile,
-// else 64 x 64.
-hipError_t launch_fused_staged(bool wide, const FusedParams &p, hipStream_t s);
+struct TileSize {
+    int bm, bn;
+};
+
+// Rows that are not 16-byte aligned, any K >= 1 (fused_staged.hip), on a tile of 64 x 64, 128 x 128
+// or 128 x 256; dwords: rows of whole dwords.
+hipError_t launch_fused_staged(const TileSize &tile, bool dwords, const FusedParams &p, hipStream_t s);
 
 // Few rows (fused_few.hip): K >= 8, any alignment.
 constexpr int kFusedFewRows = 64;
