@@ -26,7 +26,7 @@ __device__ __forceinline__ int64_t place_of(const CombineParams &p, int64_t r) {
 template <bool F32>
 __device__ __forceinline__ void load_cols(const CombineParams &p, const void *from, int64_t row, int n, Chunk8<F32> &v) {
     const int64_t at = row * p.n + n;
-    if (p.vec) {
+    if (n + 8 <= p.n) {
         v.load(from, at);
     } else {
 #pragma unroll
@@ -42,7 +42,7 @@ __device__ __forceinline__ void load_cols(const CombineParams &p, const void *fr
 
 __device__ __forceinline__ void store_cols(const CombineParams &p, void *to, bool f32, int64_t row, int n, const float (&v)[8]) {
     const int64_t at = row * p.n + n;
-    if (p.vec) {
+    if (n + 8 <= p.n) {
         store_row(to, f32, at, v, kStoreDefault);
     } else {
 #pragma unroll

@@ -219,9 +219,9 @@ static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, 
     // Cache, past it streaming stores on rows of whole 128-byte lines
     const int64_t each = es * (e.residual ? 2 : 1) + (e.pre ? 2 : 0);
     p.c_store = kStoreDefault;
-    if ((m + n) * k * 2 + m * n * each <= (int64_t(256) << 20))
+    if (p.vec && (m + n) * k * 2 + m * n * each <= (int64_t(256) << 20))
         p.c_store = kStoreDevice;
-    else if ((n * es) % 128 == 0 && (uintptr_t)c % 128 == 0)
+    else if (p.vec && (n * es) % 128 == 0 && (uintptr_t)c % 128 == 0)
         p.c_store = kStoreStream;
     if (k == 0) {
         p.parts = 0;
@@ -344,7 +344,6 @@ int gemm_f16_fused_grad(int64_t m, int64_t n, const void *dy, int32_t dy_f32, co
     p.n = n;
     p.act = act;
     p.dy_f32 = dy_f32;
-    p.vec = n % 8 == 0 && aligned16(dy) && aligned16(dz) && (act == GEMM_F16_ACT_NONE || aligned16(pre));
     p.parts = m > 0 ? fused_grad_parts(m, n) : 1;
     return status(launch_fused_grad(p, (hipStream_t)stream));
 }
@@ -436,7 +435,6 @@ int gemm_f16_combine_rows(int64_t tokens, int64_t fan, int64_t n, int64_t groups
     p.n = (int32_t)n;
     p.rows_f32 = rows_f32;
     p.y_f32 = y_f32;
-    p.vec = n % 8 == 0 && aligned16(rows) && aligned16(y) && aligned16(residual);
     return status(launch_combine(p, (hipStream_t)stream));
 }
 
@@ -477,7 +475,6 @@ int gemm_f16_combine_rows_grad(int64_t tokens, int64_t fan, int64_t n, int64_t g
     p.rows_f32 = rows_f32;
     p.y_f32 = dy_f32;
     p.drows_f32 = drows_f32;
-    p.vec = n % 8 == 0 && aligned16(dy) && aligned16(drows) && (!dgates || aligned16(rows));
     return status(launch_combine_grad(p, (hipStream_t)stream));
 }
 

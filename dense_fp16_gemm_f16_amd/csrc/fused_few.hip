@@ -194,7 +194,7 @@ __global__ __launch_bounds__(256) void fused_join_kernel(const FusedParams p) {
         const float *s = p.sums + (int64_t)m * p.n + n;
 #pragma unroll 4
         for (int q = 0; q < p.parts; ++q, s += each) {
-            if (p.vec) {
+            if (n + 8 <= p.n) {
                 float v[8];
                 load_row(s, true, 0, v);
 #pragma unroll

@@ -43,15 +43,15 @@ __global__ __launch_bounds__(kGradThreads) void fused_grad_kernel(const FusedGra
     const int64_t per = (p.m + p.parts - 1) / p.parts;
     const int64_t lo = (int64_t)blockIdx.y * per, hi = lo + per < p.m ? lo + per : p.m;
     float sum[8] = {};
-    if (n < p.n && p.vec) {
+    if (n + 8 <= p.n) {
         for (int64_t r0 = lo + h; r0 < hi; r0 += H * kGradRows) {
             Chunk8<F32> raw[kGradRows];
-            half8 pre[kGradRows];
+            Chunk8<false> pre[kGradRows];
 #pragma unroll
             for (int i = 0; i < kGradRows; ++i) {
                 const int64_t r = r0 + i * H < hi ? r0 + i * H : r0;  // (the first again: not used)
                 raw[i].load(p.dy, r * p.n + n);
-                if constexpr (ACT != kActNone) pre[i] = *reinterpret_cast<const half8 *>(p.pre + r * p.n + n);
+                if constexpr (ACT != kActNone) pre[i].load(p.pre, r * p.n + n);
             }
 #pragma unroll
             for (int i = 0; i < kGradRows; ++i) {
@@ -61,7 +61,7 @@ __global__ __launch_bounds__(kGradThreads) void fused_grad_kernel(const FusedGra
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     dy[e] = raw[i][e];
-                    z[e] = ACT != kActNone ? (float)pre[i][e] : 0.0f;
+                    z[e] = ACT != kActNone ? pre[i][e] : 0.0f;
                 }
                 activate_grad<ACT>(z, dy);
                 if (p.dz) store_row(p.dz, false, r * p.n + n, dy, kStoreDefault);
@@ -69,7 +69,7 @@ __global__ __launch_bounds__(kGradThreads) void fused_grad_kernel(const FusedGra
                 for (int e = 0; e < 8; ++e) sum[e] += dy[e];
             }
         }
-    } else if (n < p.n) {
+    } else if (n < p.n) {  // the last columns, fewer than 8
         for (int64_t r = lo + h; r < hi; r += H) {
             const int64_t at = r * p.n + n;
             float dy[8], z[8];

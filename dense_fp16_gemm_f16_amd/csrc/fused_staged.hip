@@ -6,8 +6,8 @@ namespace gemm_f16 {
 // The K loop of gemm_f16_kernel for such rows (KMajorOperand; G: 2 rows of whole dwords, 1 any),
 // over one part of K: K-tile t + 2 comes into registers and t + 1 goes from there to LDS, shifted
 // and masked, among the MFMAs of K-tile t.  (Chunks loaded at their own 2-byte addresses, and
-// stored between the K-tiles: 4096 x 4096 x 4097 with silu and residual 247 us, STG1 now; 1000 x
-// 1000 x 1001 18.7, STG2.)
+// stored between the K-tiles: 4096 x 4096 x 4097 with silu and residual 247 us, 230 now; 1000 x
+// 1000 x 1001 18.7, 11.7.)
 template <class C, int G>
 __global__ __launch_bounds__(C::kThreads)
 __attribute__((amdgpu_waves_per_eu(C::kMinWavesPerEU, C::kMinWavesPerEU)))

@@ -36,7 +36,6 @@ struct CombineParams {
     float *dgates;           // gradient: [tokens, fan], or null
     int64_t tokens, places, first;  // places: tokens fan; first: tokens that earlier launches hold
     int32_t fan, n, rows_f32, y_f32, drows_f32;
-    int32_t vec;             // rows in whole aligned chunks of 8 columns, everywhere
 };
 hipError_t launch_combine(const CombineParams &p, hipStream_t s);
 hipError_t launch_combine_grad(const CombineParams &p, hipStream_t s);
