@@ -46,13 +46,16 @@ HIPCC_FLAGS = [
 ]
 
 
+def _dense_sources() -> list[str]:
+    return ([os.path.join(CSRC, "gemm_f16.hip")] + sorted(glob.glob(os.path.join(CSRC, "tile_*.hip")))
+            + sorted(glob.glob(os.path.join(CSRC, "ring_*.hip"))))
+
+
 def sources() -> list[str]:
     """Translation units of libgemm_f16.so: the host side, one per block tile, one
     per block tile of the ring kernel's variants, the segmented products' and the
     feed-forward layer's."""
-    return ([os.path.join(CSRC, "gemm_f16.hip")] + sorted(glob.glob(os.path.join(CSRC, "tile_*.hip")))
-            + sorted(glob.glob(os.path.join(CSRC, "ring_*.hip")))
-            + [os.path.join(CSRC, "segments.hip")] + sorted(glob.glob(os.path.join(CSRC, "seg_*.hip")))
+    return (_dense_sources() + [os.path.join(CSRC, "segments.hip")] + sorted(glob.glob(os.path.join(CSRC, "seg_*.hip")))
             + [os.path.join(CSRC, "feedforward.hip"), os.path.join(CSRC, "route.hip"), os.path.join(CSRC, "combine.hip")]
             + sorted(glob.glob(os.path.join(CSRC, "fused_*.hip"))))
 
@@ -67,9 +70,10 @@ def _run(cmd: list[str], verbose: bool) -> None:
     subprocess.run(cmd, check=True)
 
 
-def _build_lib(lib: str, obj_dir: str, flags: list[str], verbose: bool, jobs: int | None) -> str:
+def _build_lib(lib: str, obj_dir: str, flags: list[str], verbose: bool, jobs: int | None,
+               srcs: list[str] | None = None) -> str:
     os.makedirs(obj_dir, exist_ok=True)
-    srcs = sources()
+    srcs = srcs or sources()
     objs = [os.path.join(obj_dir, os.path.splitext(os.path.basename(s))[0] + ".o") for s in srcs]
     cmds = [[_hipcc(), *HIPCC_FLAGS, *flags, "-I", INCLUDE, "-I", CSRC, "-c", s, "-o", o]
             for s, o in zip(srcs, objs)]
@@ -89,11 +93,12 @@ def build(verbose: bool = False, extra: list[str] | None = None, jobs: int | Non
 
 
 def build_trace(verbose: bool = False, jobs: int | None = None, ktiles: bool = False) -> str:
-    """The timestamp-traced copy of the library (measurement tool); ktiles:
+    """The timestamp-traced copy of the dense products (measurement tool); ktiles:
     the copy that also stamps the K-tiles around the first tile change."""
+    flags = ["-DGEMM_F16_TRACE"]
     if ktiles:
-        return _build_lib(TRACE_KT_LIB, TRACE_KT_OBJ_DIR, ["-DGEMM_F16_TRACE", "-DGEMM_F16_TRACE_KTILES"], verbose, jobs)
-    return _build_lib(TRACE_LIB, TRACE_OBJ_DIR, ["-DGEMM_F16_TRACE"], verbose, jobs)
+        return _build_lib(TRACE_KT_LIB, TRACE_KT_OBJ_DIR, [*flags, "-DGEMM_F16_TRACE_KTILES"], verbose, jobs, _dense_sources())
+    return _build_lib(TRACE_LIB, TRACE_OBJ_DIR, flags, verbose, jobs, _dense_sources())
 
 
 def build_ceiling(verbose: bool = False) -> str:

@@ -118,6 +118,42 @@ def test_fused_on_every_tile(tile, more, size):
         assert ref.worst(g.gemm_f16_fused_nt(a, b, bias, act=act), y, err, F16) <= 1
 
 
+# Rows that are not 16-byte aligned, on each of their tiles and in parts of K: whole dwords (K even,
+# operands at an even element) and not; the K loop's first, last and only K-tiles broken.
+@pytest.mark.parametrize("m,n,k", [(3000, 4104, 1022), (3000, 4104, 1023), (5000, 1000, 391), (2100, 1000, 193), (2048, 2056, 1030),
+                                   (128, 512, 4099), (128, 512, 4098), (300, 264, 77), (257, 100, 66), (70, 70, 1), (4352, 64, 2051),
+                                   (1500, 300, 129), (1025, 1032, 2047)])
+def test_fused_rows_of_any_alignment(m, n, k):
+    _say("fused unaligned rows", m, n, k)
+    gen = _gen(m + n + k)
+    a, b, bias = ref.eighths(gen, m, k), ref.eighths(gen, n, k), ref.eighths(gen, n)
+    res = ref.eighths(gen, m, n)
+    y, z, _, _ = ref.fused(a, b, bias, "relu", res)
+    for by_a, by_b in ((0, 0), (2, 0), (0, 1), (1, 3)):
+        got, pre = g.gemm_f16_fused_nt(_offset(a, by_a), _offset(b, by_b), bias, act="relu", residual=res, return_pre=True)
+        assert torch.equal(got, y.to(F16)) and torch.equal(pre, z.to(F16)), (by_a, by_b)
+    assert torch.equal(g.gemm_f16_fused_nt(a, b, bias, act="relu", residual=res.float(), out_dtype=F32), y.float())
+
+
+# Every number of columns left over, every path; results at each offset of their element; in place too.
+@pytest.mark.parametrize("n", range(257, 264))
+@pytest.mark.parametrize("m,k", [(1, 1024), (13, 256), (200, 512), (70, 4096), (4352, 64)])
+def test_fused_columns_left_over(m, n, k):
+    _say("fused columns left over", m, n, k)
+    gen = _gen(m + n + k)
+    a, b, bias = ref.eighths(gen, m, k), ref.eighths(gen, n, k), ref.eighths(gen, n)
+    for out_type in (F16, F32):
+        res = ref.eighths(gen, m, n).to(out_type)
+        y, z, _, _ = ref.fused(a, b, bias, "relu", res)
+        buf = torch.full((m * n + 64,), 7.0, dtype=out_type, device="cuda")
+        for by in (16, 17, 18):
+            out = buf[by:by + m * n].view(m, n).copy_(res)
+            got, pre = g.gemm_f16_fused_nt(a, b, bias, act="relu", residual=out, return_pre=True, out=out, out_dtype=out_type)
+            assert torch.equal(out, y.to(out_type)) and torch.equal(pre, z.to(F16)), (out_type, by)
+            assert bool((buf[:by] == 7).all()) and bool((buf[by + m * n:] == 7).all())
+            buf.fill_(7.0)
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 1000, 2048), (33, 200, 777), (200, 264, 512), (1500, 1200, 320), (4352, 4096, 256)])
 @pytest.mark.parametrize("act", ref.ACTS)
 def test_fused_random(m, n, k, act):
