@@ -332,10 +332,20 @@ __device__ __forceinline__ uint64_t open_groups(const RouteParams &p, const Keys
 template <class T, int L, int V>
 __device__ __forceinline__ void close_groups(const RouteParams &p, Keys<T, L, V> &k, uint64_t open, int sub) {
     using E = Experts<L, V>;
-    const float inv_per = 1.0f / (float)(p.experts / p.groups);
+    const int per = p.experts / p.groups;
+    const float inv_per = 1.0f / (float)per;
+    auto is_open = [&](int v) { return ((open >> (group_of(E::at(v, sub), inv_per) & 63)) & 1) != 0; };
+    if (E::B == 4 && per % 4 == 0) {  // four neighbours are in one group
 #pragma unroll
-    for (int v = 0; v < V; ++v)
-        if (!((open >> (group_of(E::at(v, sub), inv_per) & 63)) & 1)) k.key[v] = T(kNone);
+        for (int v = 0; v + 3 < V; v += 4) {
+            const bool in = is_open(v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) k.key[v + i] = in ? k.key[v + i] : T(kNone);
+        }
+    } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) k.key[v] = is_open(v) ? k.key[v] : T(kNone);
+    }
 }
 
 // A bound from below of the fan-th largest key of a token of 16 lanes: the fan-th largest among
@@ -522,10 +532,14 @@ __device__ __forceinline__ void choose(const RouteParams &p, const float (&l)[V]
             key = (p.sigmoid ? sigmoid_of<double>(x) : exp_below<double>(x, (float)m) / sum) + (double)p.bias[mine];
         }
         int place = 0;
-        for (int f = 0; f < made; ++f) {
-            const double other = __shfl(key, row * L + f);
-            const int who = __shfl(mine, row * L + f);
-            place += who >= 0 && (other > key || (other == key && who < mine));
+        auto meet = [&](double other, int who) { place += who >= 0 && (other > key || (other == key && who < mine)); };
+        if constexpr (L == 16) {
+            static_range<1, 16>([&](auto r_c) {
+                constexpr int turn = 0x120 + decltype(r_c)::value;
+                meet(rot<turn>(key), rot<turn>(mine));
+            });
+        } else {
+            for (int f = 0; f < made; ++f) meet(__shfl(key, row * L + f), __shfl(mine, row * L + f));
         }
         // (lanes without a pick, and picks of none, keep to the end)
         if (mine < 0) place = sub;
