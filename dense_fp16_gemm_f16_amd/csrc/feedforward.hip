@@ -150,16 +150,19 @@ static FusedPlan fused_tile_plan(int64_t m, int64_t n, int64_t k) {
     return best.tile ? best : plan;
 }
 
-// The few-row kernel takes up to 16 rows always, up to 64 where the model has it ahead.  Its
-// time is what each workgroup reads of A, 16 rows of it at a time (N 64, K 4096: 9.6 us for 16 rows,
-// 23 for 64, where 8 parts take 9), and B's bytes.
+// The few-row kernel takes one and two rows always, up to 64 where the model has it ahead.  Its time
+// is what each workgroup of 16 columns reads of A, for each round of them over the CUs (whole
+// rounds where K takes a CU's 16 waves), and B's bytes.  With it 160 timings (rows 3 to 64, N 64 to
+// 16384, K 200 to 8192) are 1.014 of the faster way's in the geometric mean; 16384 x 4096 takes 32
+// rows 56 us there and 31 on a tile, 4096 x 1024 6.4 and 8.6.
 static FusedPlan fused_plan(int64_t m, int64_t n, int64_t k) {
     const FusedPlan few = {0, false, 1, 0, 0, true};
-    if (k >= 8 && m <= 16) return few;
+    if (k >= 8 && m <= 2) return few;
     const FusedPlan plan = fused_tile_plan(m, n, k);
     if (k < 8 || m > kFusedFewRows) return plan;
-    const double tiles = (double)cdiv(m, 16);
-    const double us = 4.1 + (double)k / 4096 * (2.6 + 2.2 * tiles + 0.55 * tiles * tiles) + 0.07 * 2e-6 * (double)(n * k);
+    double rounds = std::max(1.0, (double)n / (16 * kFusedCus));
+    if (k > 2048) rounds = (double)cdiv(n, 16 * kFusedCus);
+    const double us = 2.4 + rounds * (0.8 + (double)k / 4096 * (4.5 + 0.22 * (double)m)) + 0.075 * 2e-6 * (double)(n * k);
     return us < plan.us ? few : plan;
 }
 

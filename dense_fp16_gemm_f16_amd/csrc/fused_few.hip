@@ -26,15 +26,49 @@ __global__ __launch_bounds__(kFewWaves *kWave) void fused_few_kernel(const Fused
     floatx4 acc[T];
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[t] = floatx4{};
+    // the lane's row of tile t of A (up to 64 rows of less than 2^22 elements; opaque, as held through
+    // the pass they cost registers)
+    auto row_of = [&](int t) {
+        int l = lane;
+        asm volatile("" : "+v"(l));
+        return p.a + (uint32_t)min(16 * t + l % 16, p.m - 1) * (uint32_t)p.k;
+    };
     for (int top = part1; top > part0; top -= kFewSteps) {
         const int count = min(top - part0, kFewSteps);
         const bool partial = 32 * top > p.k;
-        half8 bf[kFewSteps];
+        if (count == kFewSteps && !partial) {
+            // no branch between the loads, and two half passes of A's tiles in flight behind the
+            // one that is multiplied
+            constexpr int H = kFewSteps / 2, U = 2 * T;
+            half8 bf[kFewSteps], af[3][H];
+            const uint32_t k0 = 32 * (top - 1) + kl;
+            auto load = [&](half8 &v, const _Float16 *at) { v = __builtin_bit_cast(half8, (int4v)*reinterpret_cast<const int4u *>(at)); };
+            auto load_a = [&](int u) {
+                const _Float16 *at = row_of(u / 2) + k0;
+#pragma unroll
+                for (int s = 0; s < H; ++s) load(af[u % 3][s], at - 32 * (u % 2 * H + s));
+            };
+#pragma unroll
+            for (int s = 0; s < kFewSteps; ++s) load(bf[s], br + k0 - 32 * s);
+            load_a(0);
+            load_a(1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (u + 2 < U) load_a(u + 2);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int s = 0; s < H; ++s) acc[u / 2] = Mfma<16>::run(bf[u % 2 * H + s], af[u % 3][s], acc[u / 2]);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            continue;
+        }
+        half8 bf[kFewSteps] = {};  // (set, so that nothing of a pass is carried into the next)
         thin_load(bf, br, top, count, partial, kl, p.k);
 #pragma unroll
         for (int t = 0; t < T; ++t) {
-            half8 af[kFewSteps];
-            thin_load(af, p.a + (int64_t)min(16 * t + lane % 16, p.m - 1) * p.k, top, count, partial, kl, p.k);
+            half8 af[kFewSteps] = {};
+            thin_load(af, row_of(t), top, count, partial, kl, p.k);
 #pragma unroll
             for (int s = 0; s < kFewSteps; ++s)
                 if (s < count) acc[t] = Mfma<16>::run(bf[s], af[s], acc[t]);
