@@ -171,6 +171,44 @@ __device__ __forceinline__ void store_row(void *to, bool f32, int64_t at, const 
     }
 }
 
+// N (4 or 8) values of a row as they come, fp16 or fp32, for loads that go out before anything
+// waits for them.
+template <int N>
+struct RawRow {
+    floatx4 v[N / 4];
+
+    __device__ __forceinline__ void load(const void *from, bool f32, int64_t at) {
+        if (f32) {
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i) v[i] = reinterpret_cast<const floatx4u *>(static_cast<const float *>(from) + at)[i];
+        } else {
+            const halfnu<N> h = *reinterpret_cast<const halfnu<N> *>(static_cast<const _Float16 *>(from) + at);
+            __builtin_memcpy(v, &h, sizeof(_Float16) * N);
+        }
+    }
+    __device__ __forceinline__ void values(bool f32, float (&x)[N]) const {
+        _Float16 h[N];
+        __builtin_memcpy(h, v, sizeof(h));
+#pragma unroll
+        for (int e = 0; e < N; ++e) x[e] = f32 ? v[e / 4][e % 4] : (float)h[e];
+    }
+};
+
+// Bias and residual of row m, columns n .. n + N - 1 (n < p.n): asked for early, taken late.
+// (Where columns are outside, the bias is read late and the residual by finish_row.)
+template <int N>
+struct EpilogueRow {
+    RawRow<N> bias, res;
+
+    __device__ __forceinline__ void load(const FusedParams &p, int m, int n) {
+        if (m >= p.m || n + N > p.n) return;
+        if (p.bias) bias.load(p.bias, p.bias_f32 != 0, n);
+        if (p.residual) res.load(p.residual, p.out_f32 != 0, (int64_t)m * p.n + n);
+    }
+    // z += bias; r: the residual
+    __device__ __forceinline__ void add(const FusedParams &p, int n, float (&z)[N], float (&r)[N]) const;
+};
+
 // The bias of columns n .. n + N - 1, zeros past the last and without one.
 template <int N>
 __device__ __forceinline__ void load_bias(const FusedParams &p, int n, float (&b)[N]) {
@@ -190,6 +228,20 @@ __device__ __forceinline__ void load_bias(const FusedParams &p, int n, float (&b
 template <int N>
 __device__ __forceinline__ void load_residual(const FusedParams &p, int m, int n, float (&r)[N]) {
     if (p.residual && n + N <= p.n) load_row(p.residual, p.out_f32 != 0, (int64_t)m * p.n + n, r);
+}
+
+template <int N>
+__device__ __forceinline__ void EpilogueRow<N>::add(const FusedParams &p, int n, float (&z)[N], float (&r)[N]) const {
+    if (p.bias) {
+        float b[N];
+        if (n + N <= p.n)
+            bias.values(p.bias_f32 != 0, b);
+        else
+            load_bias(p, n, b);
+#pragma unroll
+        for (int e = 0; e < N; ++e) z[e] += b[e];
+    }
+    if (p.residual && n + N <= p.n) res.values(p.out_f32 != 0, r);
 }
 
 // Row m, columns n .. n + N - 1 (n < p.n) of C from z, with r of load_residual (where columns are

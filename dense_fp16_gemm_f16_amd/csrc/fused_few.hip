@@ -26,6 +26,11 @@ __global__ __launch_bounds__(kFewWaves *kWave) void fused_few_kernel(const Fused
     floatx4 acc[T];
 #pragma unroll
     for (int t = 0; t < T; ++t) acc[t] = floatx4{};
+    // the bias and residual of what the lane will store: row 16 wave + l % 16, columns n .. (early, but
+    // for four tiles, which leave no registers)
+    const int n = n0 + 4 * (lane / 16), m = 16 * wave + lane % 16;
+    EpilogueRow<4> out = {};
+    if (T < 4 && wave < T) out.load(p, m, n);
     // the lane's row of tile t of A (up to 64 rows of less than 2^22 elements; opaque, as held through
     // the pass they cost registers)
     auto row_of = [&](int t) {
@@ -77,20 +82,16 @@ __global__ __launch_bounds__(kFewWaves *kWave) void fused_few_kernel(const Fused
 #pragma unroll
     for (int t = 0; t < T; ++t) red[t][wave][lane] = acc[t];
     __syncthreads();
-    // lane l of tile t: row 16 t + l % 16, columns n0 + 4 (l / 16) ..
-    const int n = n0 + 4 * (lane / 16);
-    for (int t = wave; t < T; t += waves) {
-        const int m = 16 * t + lane % 16;
-        if (m >= p.m || n >= p.n) continue;
-        float bias[4], res[4], z[4];
-        load_bias(p, n, bias);
-        load_residual(p, m, n, res);
-        floatx4 sum = red[t][0][lane];
-        for (int w = 1; w < waves; ++w) sum += red[t][w][lane];
+    // (a workgroup has a wave for each tile: launch_fused_few)
+    if (wave >= T || m >= p.m || n >= p.n) return;
+    if (T == 4) out.load(p, m, n);
+    floatx4 sum = red[wave][0][lane];
+    for (int w = 1; w < waves; ++w) sum += red[wave][w][lane];
+    float z[4], res[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) z[e] = sum[e] + bias[e];
-        finish_row(p, m, n, z, res);
-    }
+    for (int e = 0; e < 4; ++e) z[e] = sum[e];
+    out.add(p, n, z, res);
+    finish_row(p, m, n, z, res);
 #endif
 }
 
@@ -99,9 +100,9 @@ __global__ __launch_bounds__(kFewWaves *kWave) void fused_few_kernel(const Fused
 // A wave takes R rows of B and multiplies lane by lane: 16 bytes a lane, so that a load covers a
 // whole kilobyte of a row, where the MFMA's layout takes 64 bytes of each of 16 rows.  R rows by S
 // steps of 512 elements, 16 loads, are in flight a wave.  The lanes' sums meet in a fixed order.
-// Cold weights, us, beside the MFMA's kernel: one row of 4096 x 4096 8.1 (9.9), 1024 x 4096 4.6
-// (7.8), 4096 x 1024 4.8 (5.1), two rows 9.2 (10.2), 5.2 (8.4), 5.6 (5.1): taken by dot_takes.
-// From three rows on the vector unit's products cost more than the loads gain (four: 11.3, 10.4).
+// Cold weights, us, beside the MFMA's kernel: one row of 4096 x 4096 7.8 (9.5), 1024 x 4096 4.3
+// (7.8), 4096 x 1024 4.6 (4.7), two rows 8.8 (9.6), 5.0 (7.9), 5.5 (4.7): taken by dot_takes.
+// From three rows on the vector unit's products cost more than the loads gain (four: 11.0, 9.7).
 constexpr int kDotWaves = 4;
 
 // Up to S steps of a row (K >= 8), 512 elements each, `count` of them from step top - 1 downwards;
@@ -131,12 +132,28 @@ __device__ __forceinline__ float dot_turn(float x) {
     return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, true));
 }
 
+// An element as it comes, and its value (as in RawRow).
+__device__ __forceinline__ float load_bits(const void *from, bool f32, int64_t at) {
+    return f32 ? static_cast<const float *>(from)[at]
+               : __builtin_bit_cast(float, (uint32_t) static_cast<const uint16_t *>(from)[at]);
+}
+__device__ __forceinline__ float value_of(float bits, bool f32) {
+    return f32 ? bits : (float)__builtin_bit_cast(_Float16, (uint16_t)__builtin_bit_cast(uint32_t, bits));
+}
+
 template <int M, int R, int S>
 __global__ __launch_bounds__(kDotWaves *kWave) void fused_dot_kernel(const FusedParams p) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int64_t n0 = ((int64_t)(p.first + blockIdx.x) * kDotWaves + wave) * R;
     if (n0 >= p.n) return;
+    // lane m R + r stores row m, column n0 + r: its bias and residual
+    const int m = lane / R;
+    const int64_t n = n0 + lane % R, at = (int64_t)m * p.n + n;
+    const bool mine = m < M && n < p.n;
+    float bias = 0.0f, res = 0.0f;
+    if (mine && p.bias) bias = load_bits(p.bias, p.bias_f32 != 0, n);
+    if (mine && p.residual) res = load_bits(p.residual, p.out_f32 != 0, at);
     float sum[M][R] = {};
     for (int top = (p.k + 511) / 512; top > 0; top -= S) {
         const int count = min(top, S);
@@ -158,7 +175,6 @@ __global__ __launch_bounds__(kDotWaves *kWave) void fused_dot_kernel(const Fused
                     for (int e = 0; e < 8; ++e) sum[m][r] = __builtin_fmaf((float)a[m][s][e], (float)b[r][s][e], sum[m][r]);
         }
     }
-    // lane m R + r: row m, column n0 + r
     float z = 0.0f;
 #pragma unroll
     for (int m = 0; m < M; ++m)
@@ -173,14 +189,11 @@ __global__ __launch_bounds__(kDotWaves *kWave) void fused_dot_kernel(const Fused
             x += __shfl_xor(x, 32);
             z = lane == m * R + r ? x : z;
         }
-    const int m = lane / R;
-    const int64_t n = n0 + lane % R;
-    if (m >= M || n >= p.n) return;
-    const int64_t at = (int64_t)m * p.n + n;
-    float y[1] = {z + (p.bias ? load1(p.bias, p.bias_f32 != 0, n) : 0.0f)};
+    if (!mine) return;
+    float y[1] = {p.bias ? z + value_of(bias, p.bias_f32 != 0) : z};
     if (p.pre) p.pre[at] = (_Float16)y[0];
     activate(p.act, y);
-    if (p.residual) y[0] += load1(p.residual, p.out_f32 != 0, at);
+    if (p.residual) y[0] += value_of(res, p.out_f32 != 0);
     if (p.out_f32)
         static_cast<float *>(p.c)[at] = y[0];
     else
@@ -188,7 +201,7 @@ __global__ __launch_bounds__(kDotWaves *kWave) void fused_dot_kernel(const Fused
 #endif
 }
 
-// Short rows, and two that are not long, are the MFMA's: 300 x 200 takes one row 3.6 us there, 4.0 here.
+// Short rows, and two that are not long, are the MFMA's: 300 x 200 takes one row 2.8 us there, 3.4 here.
 static bool dot_takes(const FusedParams &p) { return p.m <= 2 && p.k > 512 * p.m; }
 
 // Rows a wave by K: its loads stay 16.
@@ -207,6 +220,7 @@ hipError_t launch_fused_few(const FusedParams &p, hipStream_t s) {
     int waves = 1;  // that K keeps busy in one pass
     while (waves < kFewWaves && waves * kFewSteps * 32 < p.k) waves *= 2;
     const int tiles = (p.m + 15) / 16;
+    while (waves < tiles) waves *= 2;
     const void *kernel = tiles <= 1   ? reinterpret_cast<const void *>(fused_few_kernel<1>)
                          : tiles == 2 ? reinterpret_cast<const void *>(fused_few_kernel<2>)
                          : tiles == 3 ? reinterpret_cast<const void *>(fused_few_kernel<3>)
@@ -215,32 +229,41 @@ hipError_t launch_fused_few(const FusedParams &p, hipStream_t s) {
 }
 
 // C from the parts' sums of A B^T, added in their order (none: K == 0), 8 columns of a row a
-// thread.
+// thread.  All of a thread's loads go out before it waits for one: 48 rows of 1024 x
+// 4096 in 8 parts take 9.8 us with the join (one after the other, and with the row found by a 64-bit
+// division, 11.3).
 __global__ __launch_bounds__(256) void fused_join_kernel(const FusedParams p) {
     const int per = (p.n + 7) / 8;
     const int64_t all = (int64_t)p.m * per, stride = (int64_t)gridDim.x * 256, each = (int64_t)p.m * p.n;
     for (int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x; x < all; x += stride) {
-        const int m = (int)(x / per), n = (int)(x % per) * 8;
-        float z[8], res[8];
-        load_bias(p, n, z);
-        load_residual(p, m, n, res);
-        float sum[8] = {};
+        const int m = all < (int64_t(1) << 31) ? (int)((uint32_t)x / (uint32_t)per) : (int)(x / per);
+        const int n = (int)(x - (int64_t)m * per) * 8;
         const float *s = p.sums + (int64_t)m * p.n + n;
-#pragma unroll 4
-        for (int q = 0; q < p.parts; ++q, s += each) {
-            if (n + 8 <= p.n) {
-                float v[8];
-                load_row(s, true, 0, v);
+        float z[8] = {}, res[8];
+        EpilogueRow<8> out;
+        if (n + 8 <= p.n) {
+            constexpr int B = 4;
+            RawRow<8> v[B];
+            for (int q0 = 0; q0 < p.parts; q0 += B) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) sum[e] += v[e];
-            } else {
+                for (int b = 0; b < B; ++b)
+                    if (q0 + b < p.parts) v[b].load(s + (q0 + b) * each, true, 0);
+                if (q0 == 0) out.load(p, m, n);
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    if (q0 + b >= p.parts) continue;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) z[e] += v[b].v[e / 4][e % 4];
+                }
+            }
+            if (p.parts == 0) out.load(p, m, n);
+        } else {
+            for (int q = 0; q < p.parts; ++q)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (n + e < p.n) sum[e] += s[e];
-            }
+                    if (n + e < p.n) z[e] += s[q * each + e];
         }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] += sum[e];
+        out.add(p, n, z, res);
         finish_row(p, m, n, z, res);
     }
 }
