@@ -77,10 +77,11 @@ static hipError_t launch_tile(bool direct, bool ring, int tile, const FusedParam
 
 // Modelled time (us) of a product, or of one in parts of K:
 //     c + a K-tiles of a part x (1, or e share where more than a workgroup falls to a CU) + b share
-// with share the workgroups per CU, no less for the K loop than 0.18 us for each MB of A and B;
-// with parts, 2.05 + 0.26 a part + 0.118 for each MB of their sums, written and read, for the
-// join.  Least-squares fits, in relative error, to 1852 timings of 120 shapes (rows 17 to 16384, N
-// 8 to 8192, K 64 to 8192, inputs cold in the caches) on MI355X.
+// with share the workgroups per CU, no less for the K loop than 0.175 us for each MB of A and B, and
+// up to 2.5 times that where CUs are left over; with parts, 1.6 + 0.12 a part + 0.123 for each MB of
+// their sums, written and read, for the join.  Least-squares fits, in relative error, to 1852 timings
+// of 120 shapes (rows 17 to 16384, N 8 to 8192, K 64 to 8192, six copies of the inputs in turn) on
+// MI355X, the join's and the left-over CUs' to 48 of them (rows 24 to 1024).
 struct FusedCost {
     int tile, bm, bn;
     bool ring;
@@ -92,8 +93,8 @@ static int64_t fused_tiles(const FusedCost &f, int64_t m, int64_t n) { return cd
 static double fused_us(const FusedCost &f, int64_t tiles, int64_t m, int64_t n, int64_t k, int parts, int part_kt) {
     const double share = (double)(tiles * parts) / kFusedCus;
     const double loop = f.a * part_kt * (share > 1 ? std::max(1.0, f.e * share) : 1.0);
-    const double inputs = 0.18 * 2e-6 * (double)((m + n) * k);
-    const double join = parts > 1 ? 2.05 + 0.26 * parts + 0.118 * 8e-6 * (double)(m * n) * parts : 0;
+    const double inputs = 0.175 * 2e-6 * (double)((m + n) * k) * std::min(std::max(1.0, 1 / share), 2.5);
+    const double join = parts > 1 ? 1.6 + 0.12 * parts + 0.123 * 8e-6 * (double)(m * n) * parts : 0;
     return f.c + std::max(loop, inputs) + f.b * share + join;
 }
 
@@ -109,8 +110,8 @@ struct FusedPlan {
 
 // The dense product's choice of tile, unless the model has one in parts of K, or on the ring, at
 // less than 0.9 of its time.  On those 120 shapes the plan took 1.034 of the fastest variant's time
-// in the geometric mean (the dense choice alone: 1.28); 128 rows of 4096 x 4096 take 16.6 us in 3
-// parts, 26 undivided; 1024 of 64 x 4096 12 and 26; 512 of 4096 x 4096 30, undivided.
+// in the geometric mean (the dense choice alone: 1.28); 128 rows of 4096 x 4096 take 16.7 us in 3
+// parts, 26 undivided; 1024 of 64 x 4096 11 and 26; 512 of 4096 x 4096 32, undivided.
 static FusedPlan fused_tile_plan(int64_t m, int64_t n, int64_t k) {
     static const FusedCost costs[] = {
         {GEMM_F16_TILE_64x64, 64, 64, false, 2.41, 0.358, 1.253, 1.63},
