@@ -94,12 +94,16 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(const CombineP
     }
 }
 
-// A wave a token: dy once, B of the token's rows at a time, two chunks of columns in flight.
+// 2^log waves a token, which share its columns: dy once, B of the token's rows at a time, two
+// chunks of columns in flight.  The waves' sums meet in LDS, in their order.
 template <int B, bool ROWS, bool Y>
-__global__ __launch_bounds__(kCombineThreads) void combine_grad_kernel(const CombineParams p, int) {
-    const int lane = threadIdx.x % kWave;
-    const int64_t token = p.first + (int64_t)blockIdx.x * (kCombineThreads / kWave) + threadIdx.x / kWave;
-    if (token >= p.tokens) return;
+__global__ __launch_bounds__(kCombineThreads) void combine_grad_kernel(const CombineParams p, int log) {
+    constexpr int kWaves = kCombineThreads / kWave;
+    __shared__ float red[kWaves][B];
+    const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int part = wave & ((1 << log) - 1);
+    const int64_t token = p.first + (int64_t)blockIdx.x * (kWaves >> log) + (wave >> log);
+    const bool in = token < p.tokens;
     const int last = *p.last;
     for (int f0 = 0; f0 < p.fan; f0 += B) {
         int64_t at[B];
@@ -109,33 +113,35 @@ __global__ __launch_bounds__(kCombineThreads) void combine_grad_kernel(const Com
         for (int b = 0; b < B; ++b) {
             at[b] = -1;
             gate[b] = dot[b] = 0.0f;
-            if (f0 + b < p.fan) {
+            if (in && f0 + b < p.fan) {
                 const int64_t r = token * p.fan + f0 + b;
                 at[b] = place_of(p, r);
                 if (at[b] < last) gate[b] = p.gates ? p.gates[r] : 1.0f;
             }
             live[b] = at[b] >= 0 && at[b] < last;
         }
+        if (in) {
 #pragma unroll 2
-        for (int n = lane * 8; n < p.n; n += kWave * 8) {
-            Chunk8<Y> dy;
-            Chunk8<ROWS> v[B];
-            load_cols(p, p.y, token, n, dy);
-            if (p.dgates) {
+            for (int n = (part * kWave + lane) * 8; n < p.n; n += (kWave * 8) << log) {
+                Chunk8<Y> dy;
+                Chunk8<ROWS> v[B];
+                load_cols(p, p.y, token, n, dy);
+                if (p.dgates) {
 #pragma unroll
-                for (int b = 0; b < B; ++b)  // (a row out of play is the first one: not used)
-                    load_cols(p, p.rows, live[b] ? at[b] : 0, n, v[b]);
-            }
-#pragma unroll
-            for (int b = 0; b < B; ++b) {
-                if (at[b] < 0) continue;
-                float d[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    d[e] = live[b] ? gate[b] * dy[e] : 0.0f;
-                    if (p.dgates) dot[b] = live[b] ? __builtin_fmaf(dy[e], v[b][e], dot[b]) : dot[b];
+                    for (int b = 0; b < B; ++b)  // (a row out of play is the first one: not used)
+                        load_cols(p, p.rows, live[b] ? at[b] : 0, n, v[b]);
                 }
-                if (p.drows) store_cols(p, p.drows, p.drows_f32 != 0, at[b], n, d);
+#pragma unroll
+                for (int b = 0; b < B; ++b) {
+                    if (at[b] < 0) continue;
+                    float d[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        d[e] = live[b] ? gate[b] * dy[e] : 0.0f;
+                        if (p.dgates) dot[b] = live[b] ? __builtin_fmaf(dy[e], v[b][e], dot[b]) : dot[b];
+                    }
+                    if (p.drows) store_cols(p, p.drows, p.drows_f32 != 0, at[b], n, d);
+                }
             }
         }
         if (!p.dgates) continue;
@@ -143,8 +149,22 @@ __global__ __launch_bounds__(kCombineThreads) void combine_grad_kernel(const Com
         for (int b = 0; b < B; ++b) {
 #pragma unroll
             for (int d = 1; d < kWave; d <<= 1) dot[b] += __shfl_xor(dot[b], d);
-            if (lane == 0 && f0 + b < p.fan) p.dgates[token * p.fan + f0 + b] = dot[b];
         }
+        if (log > 0) {
+            if (f0 > 0) __syncthreads();  // (read before it is written again)
+            if (lane == 0)
+#pragma unroll
+                for (int b = 0; b < B; ++b) red[wave][b] = dot[b];
+            __syncthreads();
+            if (part != 0) continue;
+            for (int w = 1; w < 1 << log; ++w)
+#pragma unroll
+                for (int b = 0; b < B; ++b) dot[b] += red[wave + w][b];
+        }
+        if (lane != 0 || !in) continue;
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (f0 + b < p.fan) p.dgates[token * p.fan + f0 + b] = dot[b];
     }
 }
 
@@ -183,7 +203,11 @@ hipError_t launch_combine(const CombineParams &p, hipStream_t s) {
 }
 
 hipError_t launch_combine_grad(const CombineParams &p, hipStream_t s) {
-    return launch(kernel_of(true, p), p, kCombineThreads / kWave, 0, s);
+    // waves a token: one for each 1024 columns (8192 tokens of 2 rows of 4096: 73 us, with one wave each
+    // 85, the last of them alone on the chip; 64 tokens 5.0 and 10.2; 1000 of 6 rows of 7168 43 and 71)
+    int log = 0;
+    while (log < 2 && (1024 << log) < p.n) ++log;
+    return launch(kernel_of(true, p), p, (kCombineThreads / kWave) >> log, log, s);
 }
 
 }  // namespace gemm_f16
