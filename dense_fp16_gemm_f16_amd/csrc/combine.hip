@@ -56,13 +56,14 @@ __device__ __forceinline__ void store_cols(const CombineParams &p, void *to, boo
     }
 }
 
-// 2^log threads a token, 8 columns each at a time; B rows in flight.  ROWS, Y: fp32 rows, y.
+// 2^log threads a token, 8 columns each at a time, in as many workgroups as the grid is high; B rows
+// in flight.  ROWS, Y: fp32 rows, y.
 template <int B, bool ROWS, bool Y>
 __global__ __launch_bounds__(kCombineThreads) void combine_kernel(const CombineParams p, int log) {
     const int64_t token = p.first + ((int64_t)blockIdx.x << (8 - log)) + (threadIdx.x >> log);
     if (token >= p.tokens) return;
     const int step = 8 << log, last = *p.last;
-    for (int n = ((int)threadIdx.x & ((1 << log) - 1)) * 8; n < p.n; n += step) {
+    for (int n = (int)blockIdx.y * step + ((int)threadIdx.x & ((1 << log) - 1)) * 8; n < p.n; n += step * (int)gridDim.y) {
         float y[8] = {};
         if (p.residual) {
             Chunk8<Y> r;
@@ -168,13 +169,14 @@ __global__ __launch_bounds__(kCombineThreads) void combine_grad_kernel(const Com
     }
 }
 
-// `per` tokens a workgroup; a launch holds fewer than 2^32 threads.
-static hipError_t launch(const void *kernel, CombineParams p, int per, int log, hipStream_t s) {
-    constexpr int64_t kMost = ((int64_t(1) << 32) - 1) / kCombineThreads;
+// `per` tokens a workgroup, `high` workgroups a token; a launch holds fewer than 2^32 threads.
+static hipError_t launch(const void *kernel, CombineParams p, int per, int high, int log, hipStream_t s) {
+    const int64_t kMost = ((int64_t(1) << 32) - 1) / kCombineThreads / high;
     void *args[] = {&p, &log};
     for (int64_t at = 0, all = (p.tokens + per - 1) / per; at < all; at += kMost) {
         p.first = at * per;
-        const hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)std::min(kMost, all - at)), dim3(kCombineThreads), args, 0, s);
+        const hipError_t e = hipLaunchKernel(kernel, dim3((unsigned)std::min(kMost, all - at), (unsigned)high),
+                                             dim3(kCombineThreads), args, 0, s);
         if (e != hipSuccess) return e;
     }
     return hipSuccess;
@@ -199,7 +201,12 @@ static const void *kernel_of(bool grad, const CombineParams &p) {
 hipError_t launch_combine(const CombineParams &p, hipStream_t s) {
     int log = 3;  // threads a token: its chunks of 8 columns, or a workgroup
     while (log < 8 && (8 << log) < p.n) ++log;
-    return launch(kernel_of(false, p), p, kCombineThreads >> log, log, s);
+    // few tokens: long rows go to several workgroups (64 tokens of 8 rows of 7168: 5.5 us,
+    // 13.5 with one)
+    const int per = kCombineThreads >> log;
+    const int64_t blocks = (p.tokens + per - 1) / per, steps = (p.n + (8 << log) - 1) / (8 << log);
+    const int high = (int)std::max<int64_t>(1, std::min(steps, 1024 / blocks));
+    return launch(kernel_of(false, p), p, per, high, log, s);
 }
 
 hipError_t launch_combine_grad(const CombineParams &p, hipStream_t s) {
@@ -207,7 +214,7 @@ hipError_t launch_combine_grad(const CombineParams &p, hipStream_t s) {
     // 85, the last of them alone on the chip; 64 tokens 5.0 and 10.2; 1000 of 6 rows of 7168 43 and 71)
     int log = 0;
     while (log < 2 && (1024 << log) < p.n) ++log;
-    return launch(kernel_of(true, p), p, (kCombineThreads / kWave) >> log, log, s);
+    return launch(kernel_of(true, p), p, (kCombineThreads / kWave) >> log, 1, log, s);
 }
 
 }  // namespace gemm_f16

@@ -520,7 +520,8 @@ def _routed(gen, tokens, fan, experts, dropped=0.1):
     return g.group_rows(ids, experts)
 
 
-COMBINE = [(1, 1, 1), (1, 2, 4096), (5, 1, 7), (33, 2, 64), (40, 3, 100), (100, 8, 520), (17, 11, 40), (300, 4, 1032), (64, 2, 3001), (9, 32, 8)]
+COMBINE = [(1, 1, 1), (1, 2, 4096), (5, 1, 7), (33, 2, 64), (40, 3, 100), (100, 8, 520), (17, 11, 40), (300, 4, 1032), (64, 2, 3001), (9, 32, 8),
+           (3, 8, 7000), (40, 3, 9001), (700, 6, 4100)]
 
 
 @pytest.mark.parametrize("tokens,fan,n", COMBINE)
