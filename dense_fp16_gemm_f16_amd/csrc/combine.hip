@@ -25,17 +25,21 @@ __device__ __forceinline__ int64_t place_of(const CombineParams &p, int64_t r) {
 // 8 columns of a row (n < p.n), those past the last 0.
 template <bool F32>
 __device__ __forceinline__ void load_cols(const CombineParams &p, const void *from, int64_t row, int n, Chunk8<F32> &v) {
-    const int64_t at = row * p.n + n;
-    if (n + 8 <= p.n) {
-        v.load(from, at);
+    if (n + 8 <= p.n || (!F32 && p.n >= 8)) {
+        const int at = chunk_at<8>(n, p.n);
+        v.load(from, row * p.n + at);
+        if constexpr (!F32)  // (as drop_first)
+            if (at < n)
+                v.v[0] = __builtin_bit_cast(half8, __builtin_bit_cast(unsigned __int128, v.v[0]) >> (16 * (n - at)));
     } else {
+        float last[8];
+        load_cols(from, F32, row * p.n, n, p.n, last);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float x = n + e < p.n ? load1(from, F32, at + e) : 0.0f;
             if constexpr (F32)
-                v.v[e / 4][e % 4] = x;
+                v.v[e / 4][e % 4] = last[e];
             else
-                v.v[0][e] = (_Float16)x;
+                v.v[0][e] = (_Float16)last[e];
         }
     }
 }

@@ -194,85 +194,110 @@ struct RawRow {
     }
 };
 
-// Bias and residual of row m, columns n .. n + N - 1 (n < p.n): asked for early, taken late.
-// (Where columns are outside, the bias is read late and the residual by finish_row.)
+// Columns n .. n + N - 1 of a row of `cols` (n < cols): where some are outside, the row's last N are
+// loaded, one chunk still, and moved down by drop_first; a row of fewer than N has no chunk.
 template <int N>
-struct EpilogueRow {
-    RawRow<N> bias, res;
+__device__ __forceinline__ int chunk_at(int n, int cols) {
+    return n + N <= cols ? n : cols - N;
+}
 
-    __device__ __forceinline__ void load(const FusedParams &p, int m, int n) {
-        if (m >= p.m || n + N > p.n) return;
-        if (p.bias) bias.load(p.bias, p.bias_f32 != 0, n);
-        if (p.residual) res.load(p.residual, p.out_f32 != 0, (int64_t)m * p.n + n);
+// v[e] = v[e + by], zeros behind, by < N.
+template <int N>
+__device__ __forceinline__ void drop_first(float (&v)[N], int by) {
+#pragma unroll
+    for (int d = 1; d < N; d *= 2)
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = (by & d) ? (e + d < N ? v[e + d] : 0.0f) : v[e];
+}
+
+// Columns n .. n + N - 1 (n < cols) of the row that begins at element `at`, zeros past the last.
+template <int N>
+__device__ __forceinline__ void load_cols(const void *from, bool f32, int64_t at, int n, int cols, float (&v)[N]) {
+    if (n + N <= cols) {
+        load_row(from, f32, at + n, v);
+    } else if (cols >= N) {
+        load_row(from, f32, at + cols - N, v);
+        drop_first(v, n + N - cols);
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) v[e] = n + e < cols ? load1(from, f32, at + n + e) : 0.0f;
     }
-    // z += bias; r: the residual
-    __device__ __forceinline__ void add(const FusedParams &p, int n, float (&z)[N], float (&r)[N]) const;
-};
+}
 
 // The bias of columns n .. n + N - 1, zeros past the last and without one.
 template <int N>
 __device__ __forceinline__ void load_bias(const FusedParams &p, int n, float (&b)[N]) {
 #pragma unroll
     for (int e = 0; e < N; ++e) b[e] = 0.0f;
-    if (!p.bias || n >= p.n) return;
-    if (n + N <= p.n) {
-        load_row(p.bias, p.bias_f32 != 0, n, b);
-    } else {
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            if (n + e < p.n) b[e] = load1(p.bias, p.bias_f32 != 0, n + e);
-    }
+    if (p.bias && n < p.n) load_cols(p.bias, p.bias_f32 != 0, 0, n, p.n, b);
 }
 
-// The residual of row m, columns n .. n + N - 1, where they are all inside.
+// The residual of row m, columns n .. n + N - 1 (n < p.n), if there is one.
 template <int N>
 __device__ __forceinline__ void load_residual(const FusedParams &p, int m, int n, float (&r)[N]) {
-    if (p.residual && n + N <= p.n) load_row(p.residual, p.out_f32 != 0, (int64_t)m * p.n + n, r);
+    if (p.residual) load_cols(p.residual, p.out_f32 != 0, (int64_t)m * p.n, n, p.n, r);
 }
 
+// Bias and residual of row m, columns n .. n + N - 1 (n < p.n): asked for early, taken late.
 template <int N>
-__device__ __forceinline__ void EpilogueRow<N>::add(const FusedParams &p, int n, float (&z)[N], float (&r)[N]) const {
-    if (p.bias) {
-        float b[N];
-        if (n + N <= p.n)
-            bias.values(p.bias_f32 != 0, b);
-        else
+struct EpilogueRow {
+    RawRow<N> bias, res;
+
+    __device__ __forceinline__ void load(const FusedParams &p, int m, int n) {
+        if (m >= p.m || n >= p.n || p.n < N) return;
+        const int from = chunk_at<N>(n, p.n);
+        if (p.bias) bias.load(p.bias, p.bias_f32 != 0, from);
+        if (p.residual) res.load(p.residual, p.out_f32 != 0, (int64_t)m * p.n + from);
+    }
+    // z += bias; r: the residual
+    __device__ __forceinline__ void add(const FusedParams &p, int m, int n, float (&z)[N], float (&r)[N]) const {
+        float b[N] = {};
+        if (p.n < N) {
             load_bias(p, n, b);
+            load_residual(p, m, n, r);
+        } else {
+            if (p.bias) bias.values(p.bias_f32 != 0, b);
+            if (p.residual) res.values(p.out_f32 != 0, r);
+            if (n + N > p.n) {
+                drop_first(b, n + N - p.n);
+                if (p.residual) drop_first(r, n + N - p.n);
+            }
+        }
 #pragma unroll
         for (int e = 0; e < N; ++e) z[e] += b[e];
     }
-    if (p.residual && n + N <= p.n) res.values(p.out_f32 != 0, r);
-}
+};
 
-// Row m, columns n .. n + N - 1 (n < p.n) of C from z, with r of load_residual (where columns are
-// outside, the residual is read here).
+// Row m, columns n .. n + N - 1 (n < p.n) of C from z, with r of load_residual.
 template <int N>
 __device__ __forceinline__ void finish_row(const FusedParams &p, int m, int n, float (&z)[N], const float (&r)[N]) {
     const int64_t at = (int64_t)m * p.n + n;
-    if (n + N <= p.n) {
-        if (p.pre) store_row(p.pre, false, at, z, p.c_store);
-        activate(p.act, z);
-        if (p.residual) {
+    const bool whole = n + N <= p.n;
+    if (p.pre) {
+        if (whole) {
+            store_row(p.pre, false, at, z, p.c_store);
+        } else {
 #pragma unroll
-            for (int e = 0; e < N; ++e) z[e] += r[e];
+            for (int e = 0; e < N; ++e)
+                if (n + e < p.n) p.pre[at + e] = (_Float16)z[e];
         }
+    }
+    activate(p.act, z);
+    if (p.residual) {
+#pragma unroll
+        for (int e = 0; e < N; ++e) z[e] += r[e];
+    }
+    if (whole) {
         store_row(p.c, p.out_f32 != 0, at, z, p.c_store);
         return;
     }
-    if (p.pre) {
-#pragma unroll
-        for (int e = 0; e < N; ++e)
-            if (n + e < p.n) p.pre[at + e] = (_Float16)z[e];
-    }
-    activate(p.act, z);
 #pragma unroll
     for (int e = 0; e < N; ++e) {
         if (n + e >= p.n) continue;
-        const float v = p.residual ? z[e] + load1(p.residual, p.out_f32 != 0, at + e) : z[e];
         if (p.out_f32)
-            static_cast<float *>(p.c)[at + e] = v;
+            static_cast<float *>(p.c)[at + e] = z[e];
         else
-            static_cast<_Float16 *>(p.c)[at + e] = (_Float16)v;
+            static_cast<_Float16 *>(p.c)[at + e] = (_Float16)z[e];
     }
 }
 

@@ -90,7 +90,7 @@ __global__ __launch_bounds__(kFewWaves *kWave) void fused_few_kernel(const Fused
     float z[4], res[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) z[e] = sum[e];
-    out.add(p, n, z, res);
+    out.add(p, m, n, z, res);
     finish_row(p, m, n, z, res);
 #endif
 }
@@ -241,7 +241,7 @@ __global__ __launch_bounds__(256) void fused_join_kernel(const FusedParams p) {
         const float *s = p.sums + (int64_t)m * p.n + n;
         float z[8] = {}, res[8];
         EpilogueRow<8> out;
-        if (n + 8 <= p.n) {
+        if (n + 8 <= p.n && p.parts > 0) {
             constexpr int B = 4;
             RawRow<8> v[B];
             for (int q0 = 0; q0 < p.parts; q0 += B) {
@@ -256,14 +256,14 @@ __global__ __launch_bounds__(256) void fused_join_kernel(const FusedParams p) {
                     for (int e = 0; e < 8; ++e) z[e] += v[b].v[e / 4][e % 4];
                 }
             }
-            if (p.parts == 0) out.load(p, m, n);
         } else {
+            out.load(p, m, n);
             for (int q = 0; q < p.parts; ++q)
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
                     if (n + e < p.n) z[e] += s[q * each + e];
         }
-        out.add(p, n, z, res);
+        out.add(p, m, n, z, res);
         finish_row(p, m, n, z, res);
     }
 }

@@ -43,15 +43,18 @@ __global__ __launch_bounds__(kGradThreads) void fused_grad_kernel(const FusedGra
     const int64_t per = (p.m + p.parts - 1) / p.parts;
     const int64_t lo = (int64_t)blockIdx.y * per, hi = lo + per < p.m ? lo + per : p.m;
     float sum[8] = {};
-    if (n + 8 <= p.n) {
+    // (the last columns, where they are no whole chunk, come with the ones before them)
+    const int64_t from = n + 8 <= p.n ? n : p.n - 8;
+    const int skip = (int)(n - from);  // elements of the chunk that are another thread's
+    if (n < p.n && p.n >= 8) {
         for (int64_t r0 = lo + h; r0 < hi; r0 += H * kGradRows) {
             Chunk8<F32> raw[kGradRows];
             Chunk8<false> pre[kGradRows];
 #pragma unroll
             for (int i = 0; i < kGradRows; ++i) {
                 const int64_t r = r0 + i * H < hi ? r0 + i * H : r0;  // (the first again: not used)
-                raw[i].load(p.dy, r * p.n + n);
-                if constexpr (ACT != kActNone) pre[i].load(p.pre, r * p.n + n);
+                raw[i].load(p.dy, r * p.n + from);
+                if constexpr (ACT != kActNone) pre[i].load(p.pre, r * p.n + from);
             }
 #pragma unroll
             for (int i = 0; i < kGradRows; ++i) {
@@ -64,12 +67,18 @@ __global__ __launch_bounds__(kGradThreads) void fused_grad_kernel(const FusedGra
                     z[e] = ACT != kActNone ? pre[i][e] : 0.0f;
                 }
                 activate_grad<ACT>(z, dy);
-                if (p.dz) store_row(p.dz, false, r * p.n + n, dy, kStoreDefault);
+                if (p.dz && skip == 0) store_row(p.dz, false, r * p.n + n, dy, kStoreDefault);
+                if (p.dz && skip != 0) {
+#pragma unroll
+                    for (int e = 1; e < 8; ++e)
+                        if (e >= skip) p.dz[r * p.n + from + e] = (_Float16)dy[e];
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) sum[e] += dy[e];
             }
         }
-    } else if (n < p.n) {  // the last columns, fewer than 8
+        if (skip != 0) drop_first(sum, skip);
+    } else if (n < p.n) {  // rows of fewer than 8 columns
         for (int64_t r = lo + h; r < hi; r += H) {
             const int64_t at = r * p.n + n;
             float dy[8], z[8];
