@@ -154,6 +154,24 @@ def test_fused_columns_left_over(m, n, k):
             buf.fill_(7.0)
 
 
+# Rows of C of fewer columns than a chunk, on every way there is: one and two rows, few rows, tiles, the
+# ring, parts of K, unaligned rows.
+@pytest.mark.parametrize("n", range(1, 9))
+@pytest.mark.parametrize("m,k", [(1, 2048), (2, 64), (5, 300), (20, 4096), (70, 100), (300, 4096), (300, 4097), (6000, 128), (5000, 4096)])
+def test_fused_fewer_columns_than_a_chunk(m, n, k):
+    _say("fused fewer columns", m, n, k)
+    gen = _gen(m + n + k)
+    a, b, bias = ref.eighths(gen, m, k), ref.eighths(gen, n, k), ref.eighths(gen, n)
+    for out_type in (F16, F32):
+        res = ref.eighths(gen, m, n).to(out_type)
+        y, z, _, _ = ref.fused(a, b, bias, "relu", res)
+        buf = torch.full((m * n + 64,), 7.0, dtype=out_type, device="cuda")
+        out = buf[17:17 + m * n].view(m, n).copy_(res)
+        got, pre = g.gemm_f16_fused_nt(a, b, bias, act="relu", residual=out, return_pre=True, out=out, out_dtype=out_type)
+        assert torch.equal(out, y.to(out_type)) and torch.equal(pre, z.to(F16)), out_type
+        assert bool((buf[:17] == 7).all()) and bool((buf[17 + m * n:] == 7).all())
+
+
 @pytest.mark.parametrize("m,n,k", [(1, 1000, 2048), (33, 200, 777), (200, 264, 512), (1500, 1200, 320), (4352, 4096, 256)])
 @pytest.mark.parametrize("act", ref.ACTS)
 def test_fused_random(m, n, k, act):
@@ -263,7 +281,8 @@ def test_fused_outputs_past_2_31_elements():
     assert torch.equal(got[rows], want)
 
 
-@pytest.mark.parametrize("m,n", [(1, 1), (1, 4096), (5, 7), (33, 40), (1000, 24), (777, 130), (4096, 264), (5000, 1003), (20000, 64)])
+@pytest.mark.parametrize("m,n", [(1, 1), (1, 4096), (5, 7), (33, 40), (1000, 24), (777, 130), (4096, 264), (5000, 1003), (20000, 64),
+                                 *((300, n) for n in range(2, 17))])
 @pytest.mark.parametrize("act", ref.ACTS)
 def test_fused_grad(m, n, act):
     _say("fused grad", m, n, act)
@@ -297,6 +316,24 @@ def test_fused_grad_in_place_unaligned_and_empty():
     assert rc == g.OK and torch.equal(own, want[0])
     dz, dbias = g.gemm_f16_fused_grad(dy[:0], pre[:0], act="gelu")
     assert dz.shape == (0, 72) and torch.equal(dbias, torch.zeros(72, device="cuda"))
+
+
+@pytest.mark.parametrize("m,n", [(40, 9), (300, 75), (1000, 131), (70, 263)])
+@pytest.mark.parametrize("act", ["relu", "silu"])
+def test_fused_grad_in_place_with_columns_left_over(m, n, act):
+    """The last columns are read with the ones before them, which another thread overwrites, and where
+    something may not be finite."""
+    gen = _gen(m + n)
+    dy, pre = ref.normal(gen, m, n), ref.normal(gen, m, n)
+    dy[0, n - 8], dy[m - 1, n - 9] = INF, NAN
+    want, dbias = g.gemm_f16_fused_grad(dy, pre, act=act)
+    bad = ~torch.isfinite(dbias)
+    assert bool(bad[n - 9]) == (act != "relu" or float(pre[m - 1, n - 9]) > 0)  # (relu's slope is a choice, not a factor)
+    assert not bool(bad[:n - 9].any()) and not bool(bad[n - 7:].any())
+    own = dy.clone()
+    rc = g.lib().gemm_f16_fused_grad(m, n, own.data_ptr(), 0, pre.data_ptr(), {"relu": 1, "silu": 4}[act], own.data_ptr(), None,
+                                     None, 0, torch.cuda.current_stream().cuda_stream)
+    assert rc == g.OK and torch.equal(own.view(torch.int16), want.view(torch.int16))
 
 
 def test_fused_grad_past_2_31_elements():
