@@ -84,7 +84,7 @@ def gemm_f16_fused_nt(a, b, bias=None, *, act=None, residual=None, return_pre: b
 
     def call(handle):
         c = _result(out, (m, n), dtype, device)
-        pre = torch.empty((m, n), dtype=torch.float16, device=device) if return_pre else None
+        pre = torch.empty(m, n, dtype=torch.float16, device=device) if return_pre else None
         ws = _buffer(size, device)
         e = Epilogue(code, bias is not None and bias.dtype is torch.float32, dtype is torch.float32, _ptr(bias),
                      _ptr(residual), _ptr(pre))
@@ -120,7 +120,7 @@ def gemm_f16_fused_grad(dy, pre=None, *, act=None, bias_grad: bool = True, strea
     size = _workspace_bytes("gemm_f16_fused_grad_workspace", m, n) if bias_grad else 0
 
     def call(handle):
-        dz = torch.empty((m, n), dtype=torch.float16, device=device) if act is not None else None
+        dz = torch.empty(m, n, dtype=torch.float16, device=device) if act is not None else None
         dbias = torch.empty(n, dtype=torch.float32, device=device) if bias_grad else None
         ws = _buffer(size, device)
         rc = _g.lib().gemm_f16_fused_grad(m, n, dy.data_ptr(), dtype is torch.float32, None if act is None else pre.data_ptr(),
@@ -166,8 +166,8 @@ def route(logits, fan: int, *, score: str = "softmax", bias=None, groups: int = 
     r = _routing(score, groups, top_groups, group_top, renormalize, scale)
 
     def call(handle):
-        ids = torch.empty((tokens, fan), dtype=torch.int32, device=device)
-        gates = torch.empty((tokens, fan), dtype=torch.float32, device=device)
+        ids = torch.empty(tokens, fan, dtype=torch.int32, device=device)
+        gates = torch.empty(tokens, fan, dtype=torch.float32, device=device)
         rc = _g.lib().gemm_f16_route(tokens, experts, fan, logits.data_ptr(), dtype is torch.float32, _ptr(bias), ctypes.byref(r),
                                      ids.data_ptr(), gates.data_ptr(), handle)
         if rc:
@@ -192,7 +192,7 @@ def route_grad(logits, ids, dgates, *, score: str = "softmax", renormalize: bool
     r = _routing(score, 1, 1, 1, renormalize, scale)
 
     def call(handle):
-        dlogits = torch.empty((tokens, experts), dtype=dtype, device=device)
+        dlogits = torch.empty(tokens, experts, dtype=dtype, device=device)
         rc = _g.lib().gemm_f16_route_grad(tokens, experts, fan, logits.data_ptr(), dtype is torch.float32, ids.data_ptr(),
                                           dgates.data_ptr(), ctypes.byref(r), dlogits.data_ptr(), handle)
         if rc:
@@ -263,8 +263,8 @@ def combine_rows_grad(dy, rows, inverse, offsets, gates, *, rows_dtype=None, str
     _operand("gates", gates, torch.float32, (tokens, fan), device)
 
     def call(handle):
-        drows = torch.empty((tokens * fan, n), dtype=dtype, device=device)
-        dgates = torch.empty((tokens, fan), dtype=torch.float32, device=device)
+        drows = torch.empty(tokens * fan, n, dtype=dtype, device=device)
+        dgates = torch.empty(tokens, fan, dtype=torch.float32, device=device)
         rc = _g.lib().gemm_f16_combine_rows_grad(tokens, fan, n, groups, dy.data_ptr(), dy_type is torch.float32, rows.data_ptr(),
                                                  rows_type is torch.float32, inverse.data_ptr(), offsets.data_ptr(),
                                                  gates.data_ptr(), drows.data_ptr(), dtype is torch.float32, dgates.data_ptr(),
