@@ -30,8 +30,9 @@ __device__ __forceinline__ void activate_grad(const float (&z)[N], float (&dy)[N
 
 // A workgroup takes W chunks of 8 columns and the rows of one part, 256 / W of them at a
 // time; a thread keeps the sums of its 8 columns, which meet in LDS in a fixed order.
-// Bound by bytes: 16384 x 4096 with gelu_tanh 85 us for 403 MB, a copy's rate.  Four rows of dy and z are in flight a thread, as they come (as
-// floats they took twice the registers, and half the waves were left: 146 us).
+// Bound by bytes: 16384 x 4096 with gelu_tanh 85 us for 403 MB, a copy's rate.  Four rows of dy and
+// z are in flight a thread, as they come (as floats they took twice the registers, and half the
+// waves were left: 146 us).
 constexpr int kGradThreads = 256, kGradRows = 4;
 
 template <int W, bool F32, int ACT>
