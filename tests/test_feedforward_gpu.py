@@ -749,6 +749,39 @@ def test_a_captured_layer_follows_new_inputs():
                 assert torch.equal(have, want), (tokens, i)
 
 
+def test_two_graphs_of_one_pool_with_workspaces():
+    """Parts of K and of the rows: two graphs whose workspaces may be the same memory, replayed in turn."""
+    gen = _gen(77)
+    cases = []
+    for m, n, k in ((48, 1024, 4096), (130, 264, 2056)):
+        assert g.lib().gemm_f16_fused_workspace(m, n, k) > 0
+        a, b, res = ref.normal(gen, m, k), ref.normal(gen, n, k, std=k**-0.5), ref.normal(gen, m, n)
+        dy, pre = ref.normal(gen, 40 * m, n), ref.normal(gen, 40 * m, n)
+        assert g.lib().gemm_f16_fused_grad_workspace(40 * m, n) > 0
+        cases.append((a, lambda a=a, b=b, res=res, dy=dy, pre=pre: [g.gemm_f16_fused_nt(a, b, act="silu", residual=res),
+                                                                   *g.gemm_f16_fused_grad(dy, pre, act="silu")]))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _, call in cases:
+            call()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graphs, pool = [], torch.cuda.graph_pool_handle()
+    for _, call in cases:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, pool=pool):
+            out = call()
+        graphs.append((graph, out))
+    for i in range(6):
+        (a, call), (graph, out) = cases[i % 2], graphs[i % 2]
+        a.copy_(ref.normal(gen, *a.shape))
+        graph.replay()
+        torch.cuda.synchronize()
+        for have, want in zip([o.clone() for o in out], call()):
+            assert torch.equal(have, want), i
+
+
 def test_calls_on_streams_of_their_own():
     gen = _gen(31)
     calls = []
@@ -760,7 +793,8 @@ def test_calls_on_streams_of_their_own():
     assert g.lib().gemm_f16_fused_grad_workspace(5000, 264) > 0
     calls.append(lambda **k: g.gemm_f16_fused_grad(dy, pre, act="gelu", **k))
     logits = torch.randn(500, 64, generator=gen, device="cuda")
-    calls.append(lambda **k: g.route(logits, 4, score="sigmoid", bias=logits[0] * 0.1, groups=4, top_groups=2, **k))
+    tilt = logits[0] * 0.1  # (here: the streams below do not wait for this one)
+    calls.append(lambda **k: g.route(logits, 4, score="sigmoid", bias=tilt, groups=4, top_groups=2, **k))
     want = [[t.clone() for t in c()] for c in calls]
     side, third = torch.cuda.Stream(), torch.cuda.Stream()
     torch.cuda.synchronize()
