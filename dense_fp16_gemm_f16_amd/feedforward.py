@@ -206,14 +206,16 @@ def _plan(rows, inverse, offsets, fan, dtype):
     """Sizes of a routed batch and its operands' device."""
     import torch
 
-    if rows.dim() != 2 or offsets.dim() != 1 or offsets.numel() < 2:
+    shape, ends = rows.shape, offsets.shape
+    if len(shape) != 2 or len(ends) != 1 or ends[0] < 2:
         raise ValueError("expected rows [tokens * fan, N] and offsets [groups + 1]")
-    if fan < 1 or rows.shape[0] % fan != 0:
+    places, n = shape
+    if fan < 1 or places % fan != 0:
         raise ValueError("rows must hold fan rows of each token")
     device = _first("rows", rows, dtype)
-    _operand("inverse", inverse, torch.int32, (rows.shape[0],), device)
-    _operand("offsets", offsets, torch.int32, (offsets.numel(),), device)
-    return rows.shape[0] // fan, rows.shape[1], offsets.numel() - 1, device
+    _operand("inverse", inverse, torch.int32, (places,), device)
+    _operand("offsets", offsets, torch.int32, ends, device)
+    return places // fan, n, ends[0] - 1, device
 
 
 def combine_rows(rows, inverse, offsets, fan: int, *, gates=None, residual=None, out_dtype=None, out=None, stream=None):
