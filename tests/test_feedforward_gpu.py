@@ -447,6 +447,25 @@ def test_route_tells_close_keys_apart():
     assert ids.tolist() == [[0, 1, 2, 3, 4, 5]] * 9
 
 
+@pytest.mark.parametrize("experts,groups,fan", [(256, 8, 8), (64, 16, 6), (40, 8, 5), (16, 4, 4), (16, 16, 3), (100, 20, 8), (8, 2, 2),
+                                                (512, 8, 8)])
+@pytest.mark.parametrize("alike", ["groups", "experts"])
+def test_route_tells_close_groups_apart(experts, groups, fan, alike):
+    """Groups whose values differ by steps of a logit in fp32: each a copy of the same logits but for those
+    steps; or all experts alike but for them."""
+    _say("route close groups", experts, groups, fan, alike)
+    gen = _gen(experts + groups)
+    per = experts // groups
+    base = torch.randn(33, 1, per, generator=gen, device="cuda") if alike == "groups" else torch.full((33, 1, per), 0.75, device="cuda")
+    steps = torch.randint(-2, 3, (33, groups, per), generator=gen, device="cuda")
+    logits = (base.expand(-1, groups, -1) * (1 + steps * 2.0**-23)).reshape(33, experts)
+    logits[::5, ::3] = -INF
+    tilt = torch.randn(1, per, generator=gen, device="cuda").mul_(0.1).expand(groups, -1).reshape(-1).contiguous()
+    for bias in (None, tilt):
+        for group_top in (1, 2):
+            _check_route(logits, fan, score="sigmoid", bias=bias, groups=groups, top_groups=max(1, groups // 2), group_top=group_top)
+
+
 def test_route_unaligned_logits_and_no_tokens():
     gen = _gen(4)
     logits = torch.randn(30, 64, generator=gen, device="cuda")
