@@ -5,8 +5,8 @@ the templates of csrc/kernels.h) and the host side (csrc/gemm_f16.hip) on its
 own, all in parallel, then linked into one shared library.
 
 build_ceiling() builds the MFMA-rate probe libmfma_ceiling.so, and
-build_trace() the timestamp-traced copy of the library, libgemm_f16_trace.so
-(the same sources with -DGEMM_F16_TRACE), and build_poison() the debug copy
+build_trace() the timestamp-traced copy of the dense products, libgemm_f16_trace.so
+(their sources with -DGEMM_F16_TRACE), and build_poison() the debug copy
 whose kernels fill their LDS with NaN before the first load,
 libgemm_f16_poison.so (-DGEMM_F16_POISON_LDS): measurement and debug tools
 that are not part of the library (tune.py --ceiling, trace.py and the tests
