@@ -86,12 +86,14 @@ struct FusedCost {
     int tile, bm, bn;
     bool ring;
     double c, a, e, b;
+    bool rounds;  // share in whole rounds: a workgroup has its CU alone, and a tile is long
 };
 
 static int64_t fused_tiles(const FusedCost &f, int64_t m, int64_t n) { return cdiv(m, f.bm) * cdiv(n, f.bn); }
 
 static double fused_us(const FusedCost &f, int64_t tiles, int64_t m, int64_t n, int64_t k, int parts, int part_kt) {
-    const double share = (double)(tiles * parts) / kFusedCus;
+    double share = (double)(tiles * parts) / kFusedCus;
+    if (f.rounds && share > 1) share = (double)cdiv(tiles * parts, kFusedCus);
     const double loop = f.a * part_kt * (share > 1 ? std::max(1.0, f.e * share) : 1.0);
     const double inputs = 0.175 * 2e-6 * (double)((m + n) * k) * std::min(std::max(1.0, 1 / share), 2.5);
     const double join = parts > 1 ? 1.6 + 0.12 * parts + 0.123 * 8e-6 * (double)(m * n) * parts : 0;
@@ -108,19 +110,47 @@ struct FusedPlan {
     bool few;
 };
 
+// Takes the parts of K into which `f` is divided at less than best's time, if there are any; `whole`:
+// or not divided.
+static void fused_parts(const FusedCost &f, int64_t m, int64_t n, int64_t k, bool whole, FusedPlan &best) {
+    const int64_t tiles = fused_tiles(f, m, n);
+    const int k_tiles = (int)cdiv(k, 64);
+    for (int parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
+        if (parts == 1 ? !whole : 2 * parts > k_tiles || tiles * parts > 10 * kFusedCus) continue;
+        const int part_kt = (k_tiles + parts - 1) / parts, really = (k_tiles + part_kt - 1) / part_kt;
+        const double us = fused_us(f, tiles, m, n, k, really, part_kt);
+        if (us < best.us) best = {f.tile, f.ring, really, part_kt, us, false};
+    }
+}
+
+// Rows that are not 16-byte aligned, as K says: a fit to 396 timings of 31 shapes (rows 24 to
+// 16384, K 333 to 4097), whose choice took 1.01 of the fastest variant's time in the geometric mean;
+// 719 x 784 x 1899 takes 17.7 us, 23.9 with the aligned rows' choice, 128 x 4096 x 4097 23 and 29.6.
+static FusedPlan fused_staged_plan(int64_t m, int64_t n, int64_t k) {
+    static const FusedCost costs[] = {
+        {GEMM_F16_TILE_64x64, 64, 64, false, 4.77, 0.373, 1.163, 2.15, false},
+        {GEMM_F16_TILE_128x128, 128, 128, false, 7.73, 0.734, 1.526, 3.02, false},
+        {GEMM_F16_TILE_128x256, 128, 256, false, 9.38, 1.171, 1.449, 3.96, true},
+    };
+    FusedPlan best = {GEMM_F16_TILE_128x256, false, 1, (int)cdiv(k, 64), 1e300, false};
+    for (const FusedCost &f : costs) fused_parts(f, m, n, k, true, best);
+    return best;
+}
+
 // The dense product's choice of tile, unless the model has one in parts of K, or on the ring, at
 // less than 0.9 of its time.  On those 120 shapes the plan took 1.034 of the fastest variant's time
 // in the geometric mean (the dense choice alone: 1.28); 128 rows of 4096 x 4096 take 16.7 us in 3
 // parts, 26 undivided; 1024 of 64 x 4096 11 and 26; 512 of 4096 x 4096 32, undivided.
 static FusedPlan fused_tile_plan(int64_t m, int64_t n, int64_t k) {
+    if (k % 8 != 0) return fused_staged_plan(m, n, k);
     static const FusedCost costs[] = {
-        {GEMM_F16_TILE_64x64, 64, 64, false, 2.41, 0.358, 1.253, 1.63},
-        {GEMM_F16_TILE_64x128, 64, 128, false, 3.19, 0.408, 1.438, 2.11},
-        {GEMM_F16_TILE_128x64, 128, 64, false, 3.12, 0.412, 1.493, 2.02},
-        {GEMM_F16_TILE_128x256, 128, 256, false, 7.56, 0.645, 2.536, 4.27},
-        {GEMM_F16_TILE_128x128, 128, 128, false, 4.99, 0.444, 1.519, 3.56},  // from here on also in parts
-        {GEMM_F16_TILE_256x128, 256, 128, false, 7.45, 0.619, 1.896, 4.03},
-        {GEMM_F16_TILE_64x64, 64, 64, true, 4.14, 0.294, 0.808, 1.00},
+        {GEMM_F16_TILE_64x64, 64, 64, false, 2.41, 0.358, 1.253, 1.63, false},
+        {GEMM_F16_TILE_64x128, 64, 128, false, 3.19, 0.408, 1.438, 2.11, false},
+        {GEMM_F16_TILE_128x64, 128, 64, false, 3.12, 0.412, 1.493, 2.02, false},
+        {GEMM_F16_TILE_128x256, 128, 256, false, 7.56, 0.645, 2.536, 4.27, false},
+        {GEMM_F16_TILE_128x128, 128, 128, false, 4.99, 0.444, 1.519, 3.56, false},  // from here on also in parts
+        {GEMM_F16_TILE_256x128, 256, 128, false, 7.45, 0.619, 1.896, 4.03, false},
+        {GEMM_F16_TILE_64x64, 64, 64, true, 4.14, 0.294, 0.808, 1.00, false},
     };
     const int k_tiles = (int)cdiv(k, 64);
     FusedPlan plan = {gemm_f16_select_tile(m, n, k), false, 1, k_tiles, 1e300, false};
@@ -138,16 +168,8 @@ static FusedPlan fused_tile_plan(int64_t m, int64_t n, int64_t k) {
         plan.us = whole = fused_us(costs[6], fused_tiles(costs[6], m, n), m, n, k, 1, k_tiles);
     }
     FusedPlan best = {0, false, 1, k_tiles, 0.9 * whole, false};
-    for (const FusedCost &f : costs) {
-        if (!f.ring && f.tile != GEMM_F16_TILE_128x128 && f.tile != GEMM_F16_TILE_256x128) continue;
-        const int64_t tiles = fused_tiles(f, m, n);
-        for (int parts : {1, 2, 3, 4, 6, 8, 12, 16}) {
-            if (parts == 1 ? !f.ring : 2 * parts > k_tiles || tiles * parts > 10 * kFusedCus) continue;
-            const int part_kt = (k_tiles + parts - 1) / parts, really = (k_tiles + part_kt - 1) / part_kt;
-            const double us = fused_us(f, tiles, m, n, k, really, part_kt);
-            if (us < best.us) best = {f.tile, f.ring, really, part_kt, us, false};
-        }
-    }
+    for (const FusedCost &f : costs)
+        if (f.ring || f.tile == GEMM_F16_TILE_128x128 || f.tile == GEMM_F16_TILE_256x128) fused_parts(f, m, n, k, f.ring, best);
     return best.tile ? best : plan;
 }
 
@@ -163,7 +185,8 @@ static FusedPlan fused_plan(int64_t m, int64_t n, int64_t k) {
     if (k < 8 || m > kFusedFewRows) return plan;
     double rounds = std::max(1.0, (double)n / (16 * kFusedCus));
     if (k > 2048) rounds = (double)cdiv(n, 16 * kFusedCus);
-    const double us = 2.4 + rounds * (0.8 + (double)k / 4096 * (4.5 + 0.22 * (double)m)) + 0.075 * 2e-6 * (double)(n * k);
+    const double reads = k % 8 ? 13 + 0.8 * (double)m : 4.5 + 0.22 * (double)m;  // (chunks across lines)
+    const double us = 2.4 + rounds * (0.8 + (double)k / 4096 * reads) + 0.075 * 2e-6 * (double)(n * k);
     return us < plan.us ? few : plan;
 }
 
