@@ -7,7 +7,9 @@
 
 namespace gemm_f16 {
 
-// act'(z) times dy, in place.
+// act'(z) times dy, in place.  Where the fp32 z was past fp16's range pre is an infinity, and a
+// product with z would be inf * 0: where the bell (gelu) or s (1 - s) has come to 0, the slope is what
+// is left, 0 or 1, at either infinity and short of it.  NaN stays.
 template <int ACT, int N>
 __device__ __forceinline__ void activate_grad(const float (&z)[N], float (&dy)[N]) {
 #pragma unroll
@@ -17,13 +19,14 @@ __device__ __forceinline__ void activate_grad(const float (&z)[N], float (&dy)[N
         } else if constexpr (ACT == kActGelu) {  // Phi(z) + z phi(z)
             float gauss;
             const float cdf = normal_cdf(z[e], gauss);
-            dy[e] *= __builtin_fmaf(z[e] * 0.3989422804014327f, gauss, cdf);
+            dy[e] *= gauss == 0.0f ? cdf : __builtin_fmaf(z[e] * 0.3989422804014327f, gauss, cdf);
         } else if constexpr (ACT == kActGeluTanh) {  // s = sigmoid(w): s + z s (1 - s) dw/dz
             const float q = z[e] * z[e], s = sigmoid_f32(z[e] * __builtin_fmaf(kGeluC1, q, kGeluC0));
-            dy[e] *= __builtin_fmaf(z[e] * __builtin_fmaf(3.0f * kGeluC1, q, kGeluC0), s * (1.0f - s), s);
+            const float bell = s * (1.0f - s);
+            dy[e] *= bell == 0.0f ? s : __builtin_fmaf(z[e] * __builtin_fmaf(3.0f * kGeluC1, q, kGeluC0), bell, s);
         } else if constexpr (ACT == kActSilu) {
-            const float s = sigmoid_f32(z[e]);
-            dy[e] *= __builtin_fmaf(z[e], s * (1.0f - s), s);
+            const float s = sigmoid_f32(z[e]), bell = s * (1.0f - s);
+            dy[e] *= bell == 0.0f ? s : __builtin_fmaf(z[e], bell, s);
         }
     }
 }

@@ -325,7 +325,7 @@ typedef struct {
     int32_t out_f32;      /* type of c and residual: fp16 (0) or fp32 (1) */
     const void *bias;     /* [n] */
     const void *residual; /* [m,n]; may be c itself, else must not overlap it */
-    void *pre;            /* fp16 [m,n]: z, for the gradient */
+    void *pre;            /* fp16 [m,n]: z, for the gradient; past fp16's range an infinity */
 } gemm_f16_epilogue;
 
 /*
@@ -349,7 +349,8 @@ int64_t gemm_f16_fused_workspace(int64_t m, int64_t n, int64_t k);
  *   dz[m][n] = dy[m][n] act'(pre[m][n])        dbias[n] = sum_m dz[m][n]
  *
  *   dy   fp16 or fp32 [m,n]: the gradient of c
- *   pre  fp16 [m,n]: of the forward call; not read without an activation
+ *   pre  fp16 [m,n]: of the forward call; not read without an activation.  At
+ *        an infinity (z past fp16's range) act' is its limit, 0 or 1
  *   dz   fp16 [m,n] or NULL; may be dy itself where that is fp16
  *   dbias  fp32 [n] or NULL: sums in fp32 of dz before it is rounded
  *
