@@ -99,6 +99,7 @@ struct Experts {
 };
 
 constexpr float kNone = -__builtin_inff();  // a key that is never picked
+constexpr float kMost = __FLT_MAX__;
 
 // The lane's logits; experts past the last, and NaN, as -inf.
 template <int L, int V>
@@ -261,7 +262,12 @@ __device__ __forceinline__ uint64_t open_groups(const RouteParams &p, const Keys
             size = larger(size, larger(larger(first, -first), larger(second, -second)));
         else if (first != T(kNone))
             size = larger(size, larger(first, -first));
-        return p.group_top == 2 && second != T(kNone) ? first + second : first;
+        if (p.group_top != 2 || second == T(kNone)) return first;
+        const T sum = first + second;
+        // Past fp32's range (a bias of its lowest value, say) it stays finite: -inf would be a group
+        // of no experts.  Such sums are close to one another and told apart in 64 bits.
+        if constexpr (sizeof(T) == 4) return __builtin_amdgcn_fmed3f(sum, -kMost, kMost);
+        return sum;
     };
     if (L == 16 && V >= 4 && per >= 4 && per <= 64 && (per & (per - 1)) == 0) {
         // groups of 1, 2, 4, 8 or 16 lanes' neighbours: in registers, each lane of a group
