@@ -132,9 +132,12 @@ def gemm_f16_fused_grad(dy, pre=None, *, act=None, bias_grad: bool = True, strea
     return _launch(device, stream, call)
 
 
-def _routing(score, groups, top_groups, group_top, renormalize, scale):
+def _routing(score, groups, top_groups, group_top, renormalize, scale, fan=1):
     if score not in SCORES:
         raise ValueError(f"score must be one of {', '.join(SCORES)}")
+    # (here too, as results of such a size are not allocated, and ctypes drops the bits past 32)
+    if not (1 <= fan <= 32 and 1 <= groups <= 64 and 1 <= top_groups <= 64 and 1 <= group_top <= 2):
+        raise _g.GemmError(_g.EINVAL)
     return Routing(SCORES[score], groups, top_groups, group_top, bool(renormalize), scale)
 
 
@@ -159,11 +162,11 @@ def route(logits, fan: int, *, score: str = "softmax", bias=None, groups: int = 
     dtype = _float_type("logits", logits)
     if logits.dim() != 2:
         raise ValueError("expected logits [tokens, experts]")
+    r = _routing(score, groups, top_groups, group_top, renormalize, scale, fan)
     device = _first("logits", logits, dtype)
     tokens, experts = logits.shape
     if bias is not None:
         _operand("bias", bias, torch.float32, (experts,), device)
-    r = _routing(score, groups, top_groups, group_top, renormalize, scale)
 
     def call(handle):
         ids = torch.empty(tokens, fan, dtype=torch.int32, device=device)
