@@ -1,4 +1,5 @@
-// Host-side checks that the entry points share: sizes, pointers and the status of a launch.
+// What the entry points' host sides share: checks of sizes and pointers, the status of a launch, and
+// the choice of a block tile.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -40,6 +41,9 @@ inline bool below(int64_t limit, int64_t a, int64_t b, int64_t c = 1) {
     if (a == 0 || b == 0 || c == 0) return true;
     return a * b < limit && a * b <= (limit - 1) / c;
 }
+
+// The dense products' block tile on a device of `cus` compute units (gemm_f16.hip).
+int auto_tile(int64_t m, int64_t n, int64_t k, int cus);
 
 inline int status(hipError_t e) { return e == hipSuccess ? GEMM_F16_OK : e == hipErrorInvalidValue ? GEMM_F16_EINVAL : GEMM_F16_EHIP; }
 

@@ -10,7 +10,8 @@
 
 namespace gemm_f16 {
 
-// gfx950's CUs: the sizes alone say what workspace a call takes
+// gfx950's CUs.  A plan counts with them whatever the device has (a part of one, say): the sizes
+// alone say what workspace a call takes, and they are asked for it with no device at hand.
 constexpr int kFusedCus = 256;
 constexpr int64_t kMaxSide = int64_t(1) << 30, kMaxDepth = int64_t(1) << 22, kMaxArea = int64_t(1) << 47;
 
@@ -153,8 +154,7 @@ static FusedPlan fused_tile_plan(int64_t m, int64_t n, int64_t k) {
         {GEMM_F16_TILE_64x64, 64, 64, true, 4.14, 0.294, 0.808, 1.00, false},
     };
     const int k_tiles = (int)cdiv(k, 64);
-    FusedPlan plan = {gemm_f16_select_tile(m, n, k), false, 1, k_tiles, 1e300, false};
-    if (plan.tile < 0) return plan;
+    FusedPlan plan = {auto_tile(m, n, k, kFusedCus), false, 1, k_tiles, 1e300, false};
     double whole = 1e300;  // 256 x 256: enough tiles, or nearly
     for (const FusedCost &f : costs)
         if (f.tile == plan.tile && !f.ring) whole = fused_us(f, fused_tiles(f, m, n), m, n, k, 1, k_tiles);
@@ -190,9 +190,8 @@ static FusedPlan fused_plan(int64_t m, int64_t n, int64_t k) {
     return us < plan.us ? few : plan;
 }
 
-// Bytes of workspace, or an error.
+// Bytes of workspace.
 static int64_t fused_need(const FusedPlan &plan, int64_t m, int64_t n) {
-    if (plan.tile < 0) return plan.tile;
     return plan.parts > 1 ? plan.parts * m * n * 4 : 0;
 }
 
@@ -206,7 +205,6 @@ static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, 
     FusedPlan plan = {};
     if (m > 0 && n > 0 && k > 0) plan = fused_plan(m, n, k);
     const int64_t need = fused_need(plan, m, n);
-    if (need < 0) return (int)need;
     if (workspace_bytes < need) return GEMM_F16_EINVAL;
     if (m == 0 || n == 0) return GEMM_F16_OK;
     const int es = e.out_f32 ? 4 : 2, bs = e.bias_f32 ? 4 : 2;
