@@ -19,6 +19,9 @@ static int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 static bool aligned16(const void *p) { return (uintptr_t)p % 16 == 0; }
 
+// Whether all rows are whole 128-byte lines.
+static bool whole_lines(const void *p, int64_t row_bytes) { return !p || ((uintptr_t)p % 128 == 0 && row_bytes % 128 == 0); }
+
 static int check_fused(int64_t m, int64_t n, int64_t k) {
     if (m < 0 || n < 0 || k < 0 || m >= kMaxSide || n >= kMaxSide || k >= kMaxDepth) return GEMM_F16_EINVAL;
     return below(kMaxArea, m, n) ? GEMM_F16_OK : GEMM_F16_EINVAL;
@@ -240,13 +243,15 @@ static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, 
     p.bias_f32 = e.bias_f32;
     p.out_f32 = e.out_f32;
     p.vec = n % 8 == 0 && aligned16(c) && aligned16(e.bias) && aligned16(e.residual) && aligned16(e.pre);
-    // as the dense product's: device scope while everything fits in the 256 MiB Infinity
-    // Cache, past it streaming stores on rows of whole 128-byte lines
+    // as the dense product's: device scope while everything fits in the 256 MiB Infinity Cache, past
+    // it streaming stores on rows of whole 128-byte lines and the default on others (60000 x 1544 x 512
+    // with silu and pre 240 us, 350 streaming; 16384 x 4104 x 2048 with gelu_tanh and pre 320 and 355; 16384
+    // x 4128 x 2048 in fp32 with pre, whose rows alone end inside a line, 314 and 351)
     const int64_t each = es * (e.residual ? 2 : 1) + (e.pre ? 2 : 0);
     p.c_store = kStoreDefault;
     if (p.vec && (m + n) * k * 2 + m * n * each <= (int64_t(256) << 20))
         p.c_store = kStoreDevice;
-    else if (p.vec && (n * es) % 128 == 0 && (uintptr_t)c % 128 == 0)
+    else if (p.vec && whole_lines(c, n * es) && whole_lines(e.pre, n * 2))
         p.c_store = kStoreStream;
     if (k == 0) {
         p.parts = 0;
@@ -270,11 +275,10 @@ static int fused(int64_t m, int64_t n, int64_t k, const void *a, const void *b, 
         return status(launch_fused_join(q, s));
     }
     if (direct && !plan.ring && walk_takes(tile, ts, cus, p)) {
-        const bool dev = p.c_store == kStoreDevice;
         switch (tile) {
-            case GEMM_F16_TILE_256x256: return status(launch_fused_walk_256x256(dev, p, cus, s));
-            case GEMM_F16_TILE_256x128: return status(launch_fused_walk_256x128(dev, p, cus, s));
-            default: return status(launch_fused_walk_128x256(dev, p, cus, s));
+            case GEMM_F16_TILE_256x256: return status(launch_fused_walk_256x256(p, cus, s));
+            case GEMM_F16_TILE_256x128: return status(launch_fused_walk_256x128(p, cus, s));
+            default: return status(launch_fused_walk_128x256(p, cus, s));
         }
     }
     return status(launch_tile(direct, plan.ring, tile, p, s));

@@ -636,10 +636,10 @@ hipError_t launch_fused_64x128(const FusedParams &p, hipStream_t s);
 hipError_t launch_fused_64x64(const FusedParams &p, hipStream_t s);
 
 // More tiles than CUs, fp16 C in whole 16-byte chunks, at least 3 K-tiles (256 x 256: an even
-// number of whole ones): fused_walk.h.  dev: device-scope stores, else streaming ones.
-hipError_t launch_fused_walk_256x256(bool dev, const FusedParams &p, int cus, hipStream_t s);
-hipError_t launch_fused_walk_256x128(bool dev, const FusedParams &p, int cus, hipStream_t s);
-hipError_t launch_fused_walk_128x256(bool dev, const FusedParams &p, int cus, hipStream_t s);
+// number of whole ones): fused_walk.h.
+hipError_t launch_fused_walk_256x256(const FusedParams &p, int cus, hipStream_t s);
+hipError_t launch_fused_walk_256x128(const FusedParams &p, int cus, hipStream_t s);
+hipError_t launch_fused_walk_128x256(const FusedParams &p, int cus, hipStream_t s);
 
 // 64 x 64 tiles on a ring of LDS stages (fused_ring.hip).
 hipError_t launch_fused_ring(const FusedParams &p, hipStream_t s);

@@ -4,11 +4,16 @@
 
 namespace gemm_f16 {
 
-hipError_t launch_fused_walk_128x256_stream(const FusedParams &p, int cus, hipStream_t s);  // a unit of its own
+// units of their own
+hipError_t launch_fused_walk_128x256_stream(const FusedParams &p, int cus, hipStream_t s);
+hipError_t launch_fused_walk_128x256_default(const FusedParams &p, int cus, hipStream_t s);
 
-hipError_t launch_fused_walk_128x256(bool dev, const FusedParams &p, int cus, hipStream_t s) {
-    return dev ? launch_walk<Cfg<128, 256, 2, 2, 16>, kStoreDevice, false>(p, cus, s)
-               : launch_fused_walk_128x256_stream(p, cus, s);
+hipError_t launch_fused_walk_128x256(const FusedParams &p, int cus, hipStream_t s) {
+    switch (p.c_store) {
+        case kStoreDevice: return launch_walk<Cfg<128, 256, 2, 2, 16>, kStoreDevice, false>(p, cus, s);
+        case kStoreStream: return launch_fused_walk_128x256_stream(p, cus, s);
+        default: return launch_fused_walk_128x256_default(p, cus, s);
+    }
 }
 
 }  // namespace gemm_f16
