@@ -105,6 +105,7 @@ template <int B, bool ROWS, bool Y>
 __global__ __launch_bounds__(kCombineThreads) void combine_grad_kernel(const CombineParams p, int log) {
     constexpr int kWaves = kCombineThreads / kWave;
     __shared__ float red[kWaves][B];
+    GEMM_POISON_LDS(red);
     const int lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int part = wave & ((1 << log) - 1);
     const int64_t token = p.first + (int64_t)blockIdx.x * (kWaves >> log) + (wave >> log);

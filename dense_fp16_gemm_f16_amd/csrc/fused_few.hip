@@ -16,6 +16,7 @@ template <int T>
 __global__ __launch_bounds__(kFewWaves *kWave) void fused_few_kernel(const FusedParams p) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
     __shared__ floatx4 red[T][kFewWaves][kWave];
+    GEMM_POISON_LDS(red);
     const int tid = threadIdx.x, lane = tid % kWave, waves = blockDim.x / kWave;
     const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const int n0 = (int)(p.first + blockIdx.x) * 16, kl = 8 * (lane / 16);

@@ -42,6 +42,7 @@ template <int W, bool F32, int ACT>
 __global__ __launch_bounds__(kGradThreads) void fused_grad_kernel(const FusedGradParams p) {
     constexpr int H = kGradThreads / W;
     __shared__ float red[H][W * 8 + 1];
+    GEMM_POISON_LDS(red);
     const int c = threadIdx.x % W, h = threadIdx.x / W;
     const int64_t n = ((int64_t)blockIdx.x * W + c) * 8;
     const int64_t per = (p.m + p.parts - 1) / p.parts;
@@ -117,6 +118,7 @@ __global__ __launch_bounds__(kGradThreads) void fused_grad_kernel(const FusedGra
 // dbias from the parts' sums: 32 columns a workgroup, eight threads a column.
 __global__ __launch_bounds__(256) void fused_grad_join_kernel(const FusedGradParams p) {
     __shared__ float red[8][32];
+    GEMM_POISON_LDS(red);
     const int x = threadIdx.x % 32, h = threadIdx.x / 32;
     const int64_t col = (int64_t)blockIdx.x * 32 + x;
     float v = 0.0f;

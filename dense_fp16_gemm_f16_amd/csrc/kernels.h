@@ -169,20 +169,22 @@ constexpr uint32_t kOutOfRange = 0x80000000u;  // buffer offset past any num_rec
 
 // LDS poisoning (built only with -DGEMM_F16_POISON_LDS, a debug build of
 // the library, never the library itself): every kernel fills its LDS with
-// fp16 NaN (0x7E00) before its first load, and waits for it, so an MFMA
-// operand read from LDS that no load (or zero-filling out-of-range load)
-// has written turns its outputs into NaN, which the parity tests catch.
+// what is a NaN as fp16, fp32 and double, and as an integer past any index,
+// before its first load, and waits for it.  So an MFMA operand, a sum or a key
+// read from LDS that no load (or zero-filling out-of-range load) has written
+// turns its outputs into NaN, which the parity tests catch.  (The row plan's
+// kernels clear all of theirs themselves.)  GEMM_POISON_LDS_BYTES: LDS whose
+// size the launch gives.
 #ifdef GEMM_F16_POISON_LDS
-__device__ __forceinline__ void poison_lds(char *smem, int bytes) {
-    typedef int int4p __attribute__((ext_vector_type(4)));
-    const int4p nan = {0x7E007E00, 0x7E007E00, 0x7E007E00, 0x7E007E00};
-    for (int o = (int)threadIdx.x * 16; o < bytes; o += (int)blockDim.x * 16)
-        *reinterpret_cast<int4p *>(smem + o) = nan;
+__device__ __forceinline__ void poison_lds(void *smem, int bytes) {
+    for (int o = (int)threadIdx.x; o < bytes / 4; o += (int)blockDim.x) static_cast<int *>(smem)[o] = 0x7FF87FF8;
     __syncthreads();
 }
 #define GEMM_POISON_LDS(smem) poison_lds(smem, (int)sizeof(smem))
+#define GEMM_POISON_LDS_BYTES(smem, bytes) poison_lds(smem, bytes)
 #else
 #define GEMM_POISON_LDS(smem)
+#define GEMM_POISON_LDS_BYTES(smem, bytes)
 #endif
 
 // Timestamp trace (built only with -DGEMM_F16_TRACE, a profiling build of

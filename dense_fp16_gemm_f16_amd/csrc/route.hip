@@ -505,6 +505,7 @@ __device__ __forceinline__ void choose(const RouteParams &p, const float (&l)[V]
     bool close = false, sorted = false;
     if constexpr (L == 16) {
         __shared__ float2 slots[kRouteWaves<16> * kWave];
+        GEMM_POISON_LDS(slots);
         if (p.fan <= 16) {
             sorted = sort_candidates<V>(p, k, sub, row, live, by_score ? error : -1.0f, slots + threadIdx.x / kWave * kWave, close,
                                         id[0]);
@@ -583,6 +584,7 @@ template <int L, int V>
 __global__ __launch_bounds__(kRouteWaves<L> *kWave) __attribute__((amdgpu_waves_per_eu(L == 16 || V <= 8 ? 4 : V <= 16 ? 3 : 1))) void route_kernel(const RouteParams p) {
     extern __shared__ __attribute__((aligned(16))) char lds[];
     constexpr int R = kWave / L;  // tokens of a wave
+    GEMM_POISON_LDS_BYTES(lds, p.groups > 1 ? kRouteWaves<L> * R * (p.experts + 2 * p.groups) * 8 : 0);
     const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave, sub = lane % L, row = lane / L;
     const int64_t token = p.first + ((int64_t)blockIdx.x * kRouteWaves<L> + wave) * R + row;
     const bool live = token < p.tokens;

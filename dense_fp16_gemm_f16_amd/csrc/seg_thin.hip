@@ -108,6 +108,7 @@ template <bool F32, bool DOWN>
 __global__ __launch_bounds__(kThinWaves *kWave) void seg_thin_kernel(const SegParams p) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass needs the signature only
     __shared__ floatx4 red[2][kThinWaves][kWave];
+    GEMM_POISON_LDS(red);
     const int tid = threadIdx.x;
     const uint32_t pid = seg_pid(p);
     const int n0 = (int)(pid % (uint32_t)p.num_n) * 16;
