@@ -40,7 +40,8 @@ static TileSize tile_size(int tile) {
 }
 
 // Whether the product can walk its tiles: more of them than CUs, fp16 results in whole 16-byte
-// chunks, and what the kernels of fused_walk.h take.
+// chunks, and what the kernels of fused_walk.h take (launch_walk there says why not an activation with
+// a residual).
 static bool walk_takes(int tile, const TileSize &ts, int cus, const FusedParams &p) {
     if ((int64_t)p.num_m * p.num_n <= cus || !p.vec || p.out_f32 || (p.residual && p.act != kActNone) ||
         (int64_t)ts.bm * p.n * 2 >= (int64_t(1) << 31))

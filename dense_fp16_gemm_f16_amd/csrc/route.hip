@@ -7,8 +7,11 @@
 //   gates = scale s[ids], or scale s[ids] / sum of s[ids]
 //
 // A row of 16 lanes takes a token (64 lanes past 256 experts), V logits a lane in registers;
-// a reduction over a row is four rotations within it.  Each pick is one such reduction for
-// the largest key and one for its lowest index.
+// a reduction over a row is four rotations within it.  Up to 256 experts and 16 picks the candidates
+// are sorted at once (sort_candidates); else each pick is one such reduction for the largest key and
+// one for its lowest index.
+// Bound by the vector unit's issue: 16384 tokens, 8 of 256 experts in 4 of 8 groups, take 15.6 to 17.3 us
+// for 17.8 MB; a wave of four tokens issues 1440 vector instructions, which fill 76% of the cycles.
 //
 // The choice is that of the formula in 64 bits, so which experts a token gets does not hang on
 // the order of a sum.  Keys are computed in fp32 and the picks made with them; where keys that

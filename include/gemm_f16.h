@@ -390,9 +390,10 @@ typedef struct {
  *
  * The choice is that of the formula in 64 bits (keys that differ by less than
  * their rounding in fp32 are told apart in 64).  An expert whose logit or key
- * is -inf or NaN is never chosen, and counts as 0 in the softmax; where too
- * few are left, the remaining ids are -1, which gemm_f16_group_rows sorts
- * behind all experts, with gates of 0.
+ * is -inf or NaN is never chosen; where too few are left, the remaining ids
+ * are -1, which gemm_f16_group_rows sorts behind all experts, with gates of 0.
+ * In the softmax a logit of -inf or NaN counts as 0; the bias, which is for the
+ * choice alone, takes no expert out of it.
  * 0 <= tokens < 2^30; 1 <= experts <= 2048; 1 <= fan <= 32; fan <= experts /
  * groups * top_groups; 1 <= groups <= 64, a divisor of experts.
  */
